@@ -106,6 +106,8 @@ def load(path: str = LIB_PATH):
     lib.ssm_calib_read.argtypes = [vp, sz, vp, vp]
     lib.ssm_calib_read_sink_floats.restype = sz
     lib.ssm_calib_read_sink_floats.argtypes = []
+    from . import attn
+    attn.declare(lib)
     if lib.ssm_abi_version() != ABI_VERSION:
         raise ImportError(f"libssm ABI {lib.ssm_abi_version()} != binding ABI {ABI_VERSION}")
     _lib = lib

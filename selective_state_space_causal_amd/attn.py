@@ -1,0 +1,370 @@
+"""ctypes binding of the attention operators of include/ssm_attn.h: rotary positions, the paged
+key/value cache (written quantised, read back), attention over packed prompts, and attention of one
+token per sequence against the cache.  Argument marshalling only: every step runs in the library's
+HIP kernels, there is no fallback.
+
+[T, H, D] tensors may be views with any token and head strides that are multiples of 16 bytes (the
+heads of a packed q/k/v projection are used in place); the D values of a head are contiguous."""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._lib import SSM_BF16, SSM_F32, SsmError, stream_handle
+
+KV_IO, KV_I8, KV_E4M3 = 0, 1, 2
+MIN_PAGE, MAX_PAGE = 16, 1024
+MAX_HEAD_DIM = 256
+
+_IO = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+_CODES = {torch.int8: KV_I8, torch.float8_e4m3fn: KV_E4M3}
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("pairs", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+class _Dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_tokens", ctypes.c_int64), ("k_tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def declare(lib):
+    """Argument types of the entry points (called once by _lib.load)."""
+    vp, i64, i32, pv = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(_View)
+    pc, pr = ctypes.POINTER(_Cache), ctypes.POINTER(_Rope)
+    lib.ssm_rope.restype = ctypes.c_int
+    lib.ssm_rope.argtypes = [i64, i32, i32, i32, i32, pr, pv, pv, pv, pv, vp]
+    lib.ssm_kv_write.restype = ctypes.c_int
+    lib.ssm_kv_write.argtypes = [i64, i32, pc, vp, pv, pv, pr, i32, pv, pv, pv, vp]
+    lib.ssm_kv_read.restype = ctypes.c_int
+    lib.ssm_kv_read.argtypes = [i64, i32, pc, vp, pv, pv, vp]
+    lib.ssm_attn_prefill.restype = ctypes.c_int
+    lib.ssm_attn_prefill.argtypes = [ctypes.POINTER(_Dims), pv, pv, pv, vp, vp, pv, vp, vp]
+    lib.ssm_attn_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_attn_decode_workspace_bytes.argtypes = [i64, i32, pc, i64]
+    lib.ssm_attn_decode_step.restype = ctypes.c_int
+    lib.ssm_attn_decode_step.argtypes = [i64, i32, i32, ctypes.c_float, pc, pv, vp, i64, vp, pv, vp, vp,
+                                         ctypes.c_size_t, vp]
+
+
+def _io(t: torch.Tensor) -> int:
+    code = _IO.get(t.dtype)
+    if code is None:
+        raise TypeError(f"io tensors must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _view(t: torch.Tensor, name: str, shape, dtype, device) -> _View:
+    """A [T, H, D] tensor's view, checked for shape, dtype, GPU device and contiguous heads."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device} (a GPU)")
+    st = t.stride()
+    if st[2] != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous (stride {st[2]})")
+    # the stride of an axis of length 1 is never used, and torch leaves it arbitrary
+    return _View(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+
+
+def _three(t, name):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _index(t: torch.Tensor, name: str, shape, dtype, device):
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _status(lib, name, st):
+    if st != 0:
+        raise SsmError(name, st, lib.ssm_status_str(st).decode())
+
+
+def _own(stream, *tensors):
+    """Tensors allocated here and used on a stream that is not the current one: the allocator must
+    not hand them out again before that stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_max: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(freq, mscale): the radians per position of each of the rot_dim / 2 pairs (fp64, on device),
+    and the factor on cos and sin.  freq_i = base^(-2 i / rot_dim); for contexts longer than the model
+    was trained on, `scaling` is
+      "linear"  positions divided by factor
+      "ntk"     base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is slowed by factor, the
+                fastest kept
+      "yarn"    pairs that turn more than beta_fast times over original_max tokens are kept, those that
+                turn less than beta_slow times are slowed by factor, a linear ramp between, and
+                mscale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    if not (base > 1.0 and math.isfinite(base)) or not (factor > 0.0 and math.isfinite(factor)):
+        raise ValueError("base must be above 1 and factor above 0")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim of at least 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = torch.tensor(base, dtype=torch.float64) ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        def pair_of(turns):
+            return rot_dim * math.log(original_max / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(0, math.floor(pair_of(beta_fast))), min(rot_dim - 1, math.ceil(pair_of(beta_slow)))
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq / factor * ramp + freq * (1 - ramp)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    return freq.to(device), mscale
+
+
+def _rope_desc(positions, freq, interleaved, mscale, T, device) -> _Rope:
+    return _Rope(_index(positions, "positions", (T,), torch.int64, device),
+                 _index(freq, "freq", (freq.numel(),), torch.float64, device), freq.numel(), bool(interleaved), mscale)
+
+
+def rope(q, k, positions, freq, *, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None,
+         stream=None):
+    """ssm_rope: q [T, Hq, D] and k [T, Hkv, D] (or None) rotated by positions [T] int64; freq (and
+    mscale) as rope_frequencies gives them.  Returns (q_out, k_out); pass q_out=q, k_out=k for in place."""
+    lib = _lib.load()
+    T, Hq, D = _three(q, "q")
+    dev = q.device
+    io = _io(q)
+    vq = _view(q, "q", (T, Hq, D), q.dtype, dev)
+    desc = _rope_desc(positions, freq, interleaved, mscale, T, dev)
+    new = []
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        new.append(q_out)
+    vqo = _view(q_out, "q_out", (T, Hq, D), q.dtype, dev)
+    Hk, vk, vko = 0, None, None
+    if k is not None:
+        Hk = _three(k, "k")[1]
+        vk = _view(k, "k", (T, Hk, D), q.dtype, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
+            new.append(k_out)
+        vko = _view(k_out, "k_out", (T, Hk, D), q.dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _status(lib, "ssm_rope", lib.ssm_rope(T, Hq, Hk, D, io, desc, vq, vqo, vk, vko, stream_handle(stream, dev)))
+    _own(stream, *new)
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------- the paged cache
+
+class KVCache:
+    """A paged key/value cache: k and v [pages, Hkv, page_size, D] in the io dtype, int8 or
+    float8_e4m3fn, and for the 8-bit types k_scale and v_scale [pages, Hkv, page_size] fp32.  The
+    tensors are the caller's; this holds them and their description."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "device", "kv_heads", "head_dim", "page_size", "pages")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4:
+            raise ValueError(f"k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
+        kind = _CODES.get(k.dtype)
+        if kind is None:
+            if k.dtype not in _IO:
+                raise TypeError(f"a cache holds float32, bfloat16, int8 or float8_e4m3fn, got {k.dtype}")
+            kind = KV_IO
+        dev = k.device
+        for t, name, shape, dtype in ((k, "k", k.shape, k.dtype), (v, "v", k.shape, k.dtype),
+                                      (k_scale, "k_scale", k.shape[:3], torch.float32),
+                                      (v_scale, "v_scale", k.shape[:3], torch.float32)):
+            scale = name.endswith("scale")
+            if scale and kind == KV_IO:
+                if t is not None:
+                    raise ValueError(f"{name}: only the 8-bit types have scales")
+                continue
+            if t is None:
+                raise ValueError(f"{name} is required")
+            if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a GPU),"
+                                 f" got {t.dtype} {tuple(t.shape)} on {t.device}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.device = dev
+        self.desc = _Cache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                           None if v_scale is None else v_scale.data_ptr(), self.pages, self.page_size, self.kv_heads,
+                           self.head_dim, kind)
+
+    @classmethod
+    def allocate(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,
+                 device="cuda"):
+        """A cache with uninitialised contents (a row is written before a sequence's length covers it)."""
+        k = torch.empty(pages, kv_heads, page_size, head_dim, dtype=dtype, device=device)
+        scale = [torch.empty(k.shape[:3], device=device) for _ in range(2)] if dtype in _CODES else [None, None]
+        return cls(k, torch.empty_like(k), *scale)
+
+    def check_io(self, dtype):
+        if self.k.dtype in _IO and self.k.dtype != dtype:
+            raise TypeError(f"a cache of {self.k.dtype} is written and read in that type, got {dtype}")
+
+
+def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, interleaved: bool = False,
+             mscale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """ssm_kv_write: keys and values k, v [T, Hkv, D] into the cache rows slots [T] int64 (page *
+    page_size + place; out of range: skipped).  With positions and freq the keys are rotated on the way, and q
+    [T, Hq, D] too where given; a k_out tensor receives the rotated keys.  Returns q_out (None without q)."""
+    lib = _lib.load()
+    T, Hk, D = _three(k, "k")
+    dev = cache.device
+    shape = (T, cache.kv_heads, cache.head_dim)
+    cache.check_io(k.dtype)
+    io = _io(k)
+    vk, vv = _view(k, "k", shape, k.dtype, dev), _view(v, "v", shape, k.dtype, dev)
+    ps = _index(slots, "slots", (T,), torch.int64, dev)
+    desc, vq, vqo, vko, Hq, new = None, None, None, None, 0, None
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq go together")
+    if positions is not None:
+        desc = _rope_desc(positions, freq, interleaved, mscale, T, dev)
+        if k_out is not None:
+            vko = _view(k_out, "k_out", shape, k.dtype, dev)
+        if q is not None:
+            Hq = _three(q, "q")[1]
+            vq = _view(q, "q", (T, Hq, D), k.dtype, dev)
+            if q_out is None:
+                q_out = new = torch.empty((T, Hq, D), dtype=k.dtype, device=dev)
+            vqo = _view(q_out, "q_out", (T, Hq, D), k.dtype, dev)
+    elif q is not None or k_out is not None:
+        raise ValueError("q and k_out are for a call with positions and freq")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    _status(lib, "ssm_kv_write", lib.ssm_kv_write(T, io, cache.desc, ps, vk, vv, desc, Hq, vq, vqo, vko,
+                                                  stream_handle(stream, dev)))
+    _own(stream, new)
+    return q_out
+
+
+def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream=None):
+    """ssm_kv_read: the rows at slots [T] int64 as (k, v) [T, Hkv, D] in dtype (the cache's own, or bfloat16
+    for the 8-bit types, where not given); slots out of range read as zeros."""
+    lib = _lib.load()
+    dev = cache.device
+    if slots.dim() != 1:
+        raise ValueError(f"slots must have one axis, got {tuple(slots.shape)}")
+    T = slots.shape[0]
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else cache.k.dtype if cache.k.dtype in _IO else torch.bfloat16
+    cache.check_io(dtype)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    ps = _index(slots, "slots", (T,), torch.int64, dev)
+    new = []
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        new.append(k_out)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        new.append(v_out)
+    vk, vv = _view(k_out, "k_out", shape, dtype, dev), _view(v_out, "v_out", shape, dtype, dev)
+    _status(lib, "ssm_kv_read", lib.ssm_kv_read(T, _io(k_out), cache.desc, ps, vk, vv, stream_handle(stream, dev)))
+    _own(stream, *new)
+    return k_out, v_out
+
+
+# ---------------------------------------------------------------- attention
+
+def attn_prefill(q, k, v, cu_q, cu_k=None, *, causal: bool = True, scale: Optional[float] = None, out=None, lse=None,
+                 stream=None):
+    """ssm_attn_prefill: softmax attention of packed sequences, q [Tq, Hq, D] over k, v [Tk, Hkv, D].
+    Sequence b holds rows cu_q[b] : cu_q[b + 1] of q and cu_k[b] : cu_k[b + 1] of k and v (int32 on the GPU; cu_k
+    defaults to cu_q); causal lets its last query see all its keys, the one before one less, and so on.  scale
+    defaults to 1 / sqrt(D).  A query that sees no key gives zeros.  Returns out [Tq, Hq, D]; an lse tensor
+    [Tq, Hq] fp32 receives the log of the softmax sums."""
+    lib = _lib.load()
+    Tq, Hq, D = _three(q, "q")
+    Tk, Hkv, _ = _three(k, "k")
+    dev = q.device
+    io = _io(q)
+    cu_k = cu_q if cu_k is None else cu_k
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError(f"cu_q must be [batch + 1] with batch >= 1, got {tuple(cu_q.shape)}")
+    B = cu_q.shape[0] - 1
+    vq = _view(q, "q", (Tq, Hq, D), q.dtype, dev)
+    vk, vv = _view(k, "k", (Tk, Hkv, D), q.dtype, dev), _view(v, "v", (Tk, Hkv, D), q.dtype, dev)
+    pq, pk = (_index(t, n, (B + 1,), torch.int32, dev) for t, n in ((cu_q, "cu_q"), (cu_k, "cu_k")))
+    new = None
+    if out is None:
+        out = new = torch.empty((Tq, Hq, D), dtype=q.dtype, device=dev)
+    vo = _view(out, "out", (Tq, Hq, D), q.dtype, dev)
+    pl = None if lse is None else _index(lse, "lse", (Tq, Hq), torch.float32, dev)
+    d = _Dims(B, Tq, Tk, Hq, Hkv, D, io, bool(causal), D ** -0.5 if scale is None else scale)
+    _status(lib, "ssm_attn_prefill", lib.ssm_attn_prefill(d, vq, vk, vv, pq, pk, vo, pl, stream_handle(stream, dev)))
+    _own(stream, new)
+    return out
+
+
+def attn_decode_workspace_bytes(batch: int, q_heads: int, cache: KVCache, table_width: int) -> int:
+    return int(_lib.load().ssm_attn_decode_workspace_bytes(batch, q_heads, cache.desc, table_width))
+
+
+def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] = None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """ssm_attn_decode_step: one token per sequence, q [B, Hq, D], over its lens[b] cached tokens (the new one
+    among them: write it first).  table [B, width] int32: the pages of each sequence; lens [B] int32.  scale defaults
+    to 1 / sqrt(D).  workspace: attn_decode_workspace_bytes() bytes, allocated where not given.  Returns out
+    [B, Hq, D]; an lse tensor [B, Hq] fp32 receives the log of the softmax sums."""
+    lib = _lib.load()
+    B, Hq, D = _three(q, "q")
+    dev = cache.device
+    cache.check_io(q.dtype)
+    io = _io(q)
+    if table.dim() != 2:
+        raise ValueError(f"table must be [batch, width], got {tuple(table.shape)}")
+    W = table.shape[1]
+    shape = (B, Hq, cache.head_dim)
+    vq = _view(q, "q", shape, q.dtype, dev)
+    pt, pn = _index(table, "table", (B, W), torch.int32, dev), _index(lens, "lens", (B,), torch.int32, dev)
+    new, ws = None, None
+    if out is None:
+        out = new = torch.empty(shape, dtype=q.dtype, device=dev)
+    vo = _view(out, "out", shape, q.dtype, dev)
+    pl = None if lse is None else _index(lse, "lse", (B, Hq), torch.float32, dev)
+    if workspace is None:
+        need = lib.ssm_attn_decode_workspace_bytes(B, Hq, cache.desc, W)
+        workspace = ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _status(lib, "ssm_attn_decode_step", lib.ssm_attn_decode_step(
+        B, Hq, io, D ** -0.5 if scale is None else scale, cache.desc, vq, pt, W, pn, vo, pl,
+        None if workspace is None else workspace.data_ptr(), size, stream_handle(stream, dev)))
+    _own(stream, new, ws)
+    return out

@@ -1,0 +1,438 @@
+"""The attention operators on the GPU against their fp64 definitions (oracle/attn.py): sizes, masks,
+strides, page tables and types where they can go wrong.  Tolerances count roundings: half a step of the
+io dtype (bf16 2^-8, fp32 2^-24) once at the end, and the terms that oracle.attn.attention_tolerance
+derives."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_causal_amd as ssm
+from oracle import attn as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def rnd(seed, *shape, io="bf16"):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(DT[io])
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def close(got, want, tol, what):
+    got = f64(got)
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    bad = np.abs(got - want) - tol
+    assert bad.max() <= 0, f"{what}: {np.abs(got - want).max():.3e} off, {bad.max():.3e} over the bound"
+
+
+def packed(seed, T, Hq, Hkv, D, io):
+    """q, k, v as the heads of a packed projection: strided views."""
+    x = rnd(seed, T, Hq + 2 * Hkv, D, io=io).to(DEV)
+    return x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+
+
+# ---------------------------------------------------------------- rope
+
+ROPE = [  # T, Hq, Hkv, D, rot, interleaved, mscale, far
+    (1, 1, 1, 8, 8, False, 1.0, 0), (1, 1, 1, 8, 2, True, 1.0, 5), (5, 3, 1, 64, 64, False, 1.0, 0),
+    (7, 4, 2, 128, 64, True, 1.3, 0), (3, 2, 2, 72, 72, False, 1.0, 0), (3, 2, 2, 80, 40, True, 0.5, 0),
+    (9, 2, 1, 40, 10, False, 1.0, 3), (9, 2, 1, 40, 10, True, 1.0, 3), (2, 1, 1, 256, 256, False, 1.0, 10 ** 6),
+    (2, 1, 1, 256, 254, True, 1.0, 10 ** 6), (4, 5, 5, 24, 24, True, 1.0, 2 ** 40), (2100, 2, 1, 64, 32, False, 1.0, 0),
+    (300, 40, 8, 128, 128, False, 1.0, 7),
+]
+
+
+def rope_tol(x, rot, interleaved, mscale, half, want):
+    """Half an io step of the result, and of the pair's magnitudes: the angle in turns rounded to fp32
+    (2 pi 2^-26), cos and sin (2^-22), their factor and three more fp32 operations (2^-22): below 2^-20."""
+    a = np.abs(x)
+    mag = a.copy()
+    h = rot // 2
+    ia = np.arange(h) * 2 if interleaved else np.arange(h)
+    ib = ia + 1 if interleaved else ia + h
+    mag[..., ia] = mag[..., ib] = a[..., ia] + a[..., ib]
+    return half * np.abs(want) + 2.0 ** -20 * max(mscale, 1.0) * mag
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", ROPE)
+def test_rope(case, io):
+    T, Hq, Hkv, D, rot, inter, ms, far = case
+    q, k, _ = packed(1, T, Hq, Hkv, D, io)
+    freq, _ = ssm.rope_frequencies(rot, device=DEV)
+    pos = (torch.arange(T) * 3 + far).to(DEV)
+    qo, ko = ssm.rope(q, k, pos, freq, interleaved=inter, mscale=ms)
+    for got, x in ((qo, q), (ko, k)):
+        want = O.rope(f64(x), f64(pos), f64(freq), inter, ms)
+        close(got, want, rope_tol(f64(x), rot, inter, ms, HALF[io], want), "rope")
+        assert torch.equal(got[..., rot:], x[..., rot:])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_in_place_and_q_alone(io, inter):
+    T, Hq, Hkv, D = 37, 6, 2, 96
+    x = rnd(2, T, Hq + 2 * Hkv, D, io=io).to(DEV)
+    before = x.clone()
+    q, k = x[:, :Hq], x[:, Hq:Hq + Hkv]
+    freq, _ = ssm.rope_frequencies(48, device=DEV)
+    pos = torch.randint(0, 4000, (T,), generator=torch.Generator().manual_seed(0)).to(DEV)
+    qo, ko = ssm.rope(q, k, pos, freq, interleaved=inter)
+    q1, none = ssm.rope(q, None, pos, freq, interleaved=inter)
+    assert none is None and torch.equal(q1, qo)
+    ssm.rope(q, k, pos, freq, interleaved=inter, q_out=q, k_out=k)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    assert torch.equal(x[:, Hq + Hkv:], before[:, Hq + Hkv:])  # v untouched
+    # heads outermost: [H, T, D] storage seen as [T, H, D]
+    qt = before[:, :Hq].transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(ssm.rope(qt, None, pos, freq, interleaved=inter)[0], qo)
+
+
+def test_rope_no_tokens():
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    freq, _ = ssm.rope_frequencies(64, device=DEV)
+    qo, ko = ssm.rope(q, None, torch.empty(0, dtype=torch.int64, device=DEV), freq)
+    assert qo.shape == (0, 4, 64) and ko is None
+
+
+# ---------------------------------------------------------------- cache
+
+def new_cache(pages, Hkv, page, D, kind, io, fill=None):
+    dtype = DT[io] if kind == "io" else {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[kind]
+    c = ssm.KVCache.allocate(pages, page, Hkv, D, dtype, DEV)
+    for t in (c.k, c.v):
+        t.view(torch.uint8).fill_(0x7F if fill is None else fill)  # e4m3 and bf16: NaN; int8: 127
+    for t in (c.k_scale, c.v_scale):
+        if t is not None:
+            t.fill_(float("nan") if fill is None else fill)
+    return c
+
+
+def values(c, n):
+    """What the cache holds, as fp64 values [pages, H, page, D]."""
+    x = f64(getattr(c, n).float())
+    s = getattr(c, n + "_scale")
+    return x if s is None else x * f64(s)[..., None]
+
+
+WRITE = [  # T, Hkv, D, page, kind, rot (0: no rotation), Hq, interleaved
+    (1, 1, 8, 16, "int8", 0, 0, False), (1, 2, 64, 16, "e4m3", 64, 4, False), (33, 3, 72, 16, "int8", 0, 0, False),
+    (50, 2, 80, 32, "e4m3", 0, 0, False), (129, 8, 128, 64, "e4m3", 128, 16, False), (65, 1, 256, 64, "int8", 0, 0, False),
+    (40, 2, 40, 16, "e4m3", 10, 2, True), (40, 2, 128, 1024, "io", 64, 0, True), (17, 4, 96, 16, "io", 0, 0, False),
+    (3000, 2, 64, 64, "int8", 0, 0, False), (20, 2, 24, 16, "int8", 24, 6, False),
+]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", WRITE)
+def test_kv_write(case, io):
+    T, Hkv, D, page, kind, rot, Hq, inter = case
+    q, k, v = packed(3, T, max(Hq, 1), Hkv, D, io)
+    if T > 2:
+        k[1] *= 1000.0
+        v[2] = 0.0
+        k[0, 0] = 2.0 ** -110  # below the smallest stored magnitude
+    pages = -(-T // page) + 2
+    c = new_cache(pages, Hkv, page, D, kind, io)
+    perm = torch.randperm(pages * page, generator=torch.Generator().manual_seed(4))[:T]
+    skip = torch.arange(T) % 7 == 5
+    slots = torch.where(skip, torch.where(torch.arange(T) % 2 == 0, -1, pages * page), perm).to(DEV)
+    pos = torch.arange(T).to(DEV) * 5
+    kw = {}
+    if rot:
+        freq, _ = ssm.rope_frequencies(rot, device=DEV)
+        kw = dict(positions=pos, freq=freq, interleaved=inter, mscale=1.1, k_out=torch.empty(T, Hkv, D, dtype=DT[io], device=DEV))
+        if Hq:
+            kw["q"] = q
+    before = [t.clone() for t in (c.k, c.v)]
+    qo = ssm.kv_write(k, v, c, slots, **kw)
+    stored_k = k
+    if rot:
+        rq, stored_k = ssm.rope(q, k, pos, freq, interleaved=inter, mscale=1.1)
+        assert torch.equal(kw["k_out"], stored_k)
+        assert (qo is None) == (Hq == 0) and (qo is None or torch.equal(qo, rq))
+    written = torch.zeros(pages * page, dtype=torch.bool)
+    written[perm[~skip]] = True
+    written = written.view(pages, page)
+    for n, x, old in (("k", stored_k, before[0]), ("v", v, before[1])):
+        got = getattr(c, n).cpu()
+        rows = got.permute(0, 2, 1, 3).reshape(pages * page, Hkv, D)[perm[~skip]]
+        src = x.cpu()[~skip]
+        if kind == "io":
+            assert torch.equal(rows, src)
+        else:
+            want, scale = O.quantize(src.float().numpy(), kind)
+            assert np.array_equal(f64(rows.float()), want)
+            s = getattr(c, n + "_scale").cpu().permute(0, 2, 1).reshape(pages * page, Hkv)[perm[~skip]]
+            assert np.array_equal(s.numpy(), scale)
+        # nothing else was written
+        keep = ~written.view(pages, 1, page, 1).expand(pages, Hkv, page, D)
+        assert torch.equal(got.view(torch.uint8).reshape(pages, Hkv, page, -1)[~written.view(pages, 1, page).expand(pages, Hkv, page)],
+                           old.cpu().view(torch.uint8).reshape(pages, Hkv, page, -1)[~written.view(pages, 1, page).expand(pages, Hkv, page)])
+        assert keep.any()
+
+
+@pytest.mark.parametrize("kind,io", [("int8", "bf16"), ("int8", "f32"), ("e4m3", "bf16"), ("e4m3", "f32"), ("io", "bf16"),
+                                     ("io", "f32")])
+@pytest.mark.parametrize("T,Hkv,D,page", [(1, 1, 8, 16), (31, 3, 72, 16), (100, 2, 128, 64), (9, 4, 256, 32), (5000, 2, 64, 128)])
+def test_kv_read(T, Hkv, D, page, kind, io):
+    pages = 5 if T < 1000 else 40
+    c = new_cache(pages, Hkv, page, D, kind, io, fill=0)
+    n = pages * page
+    x = rnd(5, n, 2 * Hkv, D, io=io).to(DEV)
+    ssm.kv_write(x[:, :Hkv], x[:, Hkv:], c, torch.arange(n, device=DEV))
+    slots = torch.randint(-3, n + 3, (T,), generator=torch.Generator().manual_seed(6)).to(DEV)
+    k, v = ssm.kv_read(c, slots, dtype=DT[io])
+    sl = slots.cpu().numpy()
+    ok = (sl >= 0) & (sl < n)
+    for got, name in ((k, "k"), (v, "v")):
+        val = values(c, name).transpose(0, 2, 1, 3).reshape(n, Hkv, D)
+        want = np.where(ok[:, None, None], val[np.clip(sl, 0, n - 1)], 0.0)
+        # one fp32 product and one rounding to the io dtype
+        close(got, want, (0 if kind == "io" else HALF[io] + 2.0 ** -24) * np.abs(want), "kv_read")
+
+
+# ---------------------------------------------------------------- prefill
+
+PREFILL = [  # lens q, past keys, Hq, Hkv, D, causal
+    ([1], [0], 1, 1, 8, True), ([1], [0], 1, 1, 64, False), ([5], [0], 2, 1, 64, True), ([33], [0], 2, 2, 128, True),
+    ([64, 1, 0, 65], [0, 0, 0, 0], 4, 2, 64, True), ([130], [70], 3, 1, 128, True), ([20, 31], [100, 1], 8, 2, 80, True),
+    ([40], [-13], 4, 2, 64, True),  # fewer keys than queries: the first 13 see none
+    ([7, 9], [-7, 3], 2, 2, 72, False),  # no keys at all
+    ([150], [0], 2, 1, 256, True), ([90], [33], 2, 2, 192, False), ([70], [0], 4, 4, 136, True),
+    ([6], [0], 17, 1, 40, True), ([3] * 70 + [200] + [2] * 60, [1] * 131, 2, 2, 64, True),
+    ([300], [0], 1, 1, 128, False), ([257], [511], 2, 1, 96, True), ([20], [0], 64, 1, 112, True),
+]
+
+
+def prefill_case(lens, past, Hq, Hkv, D, io, seed=7):
+    cu_q = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    lk = np.maximum(np.array(lens) + np.array(past), 0)
+    cu_k = np.concatenate([[0], np.cumsum(lk)]).astype(np.int32)
+    q = rnd(seed, max(int(cu_q[-1]), 1), Hq, D, io=io)
+    k = rnd(seed + 1, int(cu_k[-1]), Hkv, D, io=io)
+    v = rnd(seed + 2, int(cu_k[-1]), Hkv, D, io=io)
+    return q, k, v, cu_q, cu_k
+
+
+def check_attn(got, lse, ref, io, D, what, untouched=None):
+    out, rlse, mag, smax, qkmax = ref
+    keys = 1 << 10
+    tol, ltol = O.attention_tolerance(HALF[io], HALF["bf16"] if io == "bf16" else 0.0, out, mag, smax, qkmax, D, keys)
+    close(got, out, tol, what)
+    if lse is not None:
+        l = f64(lse)
+        empty = np.isinf(rlse)
+        assert np.array_equal(np.isneginf(l), empty), f"{what}: lse of empty rows"
+        d = np.abs(np.where(empty, 0, l) - np.where(empty, 0, rlse))
+        assert np.all(d <= ltol + 2.0 ** -22 * np.abs(np.where(empty, 0, rlse))), f"{what}: lse {d.max():.3e} off"
+        assert np.all(f64(got)[empty] == 0), f"{what}: rows without keys are zero"
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", PREFILL)
+def test_attn_prefill(case, io):
+    lens, past, Hq, Hkv, D, causal = case
+    q, k, v, cu_q, cu_k = prefill_case(lens, past, Hq, Hkv, D, io)
+    cq, ck = torch.from_numpy(cu_q).to(DEV), torch.from_numpy(cu_k).to(DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    out = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cq, ck, causal=causal, lse=lse)
+    ref = O.prefill(f64(q), f64(k), f64(v), cu_q, cu_k, causal, D ** -0.5)
+    n = int(cu_q[-1])
+    check_attn(out[:n], lse[:n], [r[:n] for r in ref], io, D, f"{case}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attn_prefill_layouts_scale_and_gaps(io):
+    """Packed projection views, heads-outermost storage, a strided output, another scale, and rows that
+    belong to no sequence (NaN there: never read for others, and their outputs untouched)."""
+    lens, Hq, Hkv, D = [40, 25], 6, 2, 64
+    T = sum(lens) + 10
+    x = rnd(11, T, Hq + 2 * Hkv, D, io=io)
+    x[sum(lens):] = float("nan")
+    xd = x.to(DEV)
+    cu = torch.tensor([0, 40, 65], dtype=torch.int32, device=DEV)
+    q, k, v = xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:]
+    big = torch.full((T, Hq + 1, D), 3.0, dtype=DT[io], device=DEV)
+    out = ssm.attn_prefill(q, k, v, cu, scale=0.3, out=big[:, 1:])
+    ref = O.prefill(f64(x[:, :Hq]), f64(x[:, Hq:Hq + Hkv]), f64(x[:, Hq + Hkv:]), [0, 40, 65], [0, 40, 65], True, 0.3)
+    check_attn(out[:65], None, [r[:65] for r in ref], io, D, "strided")
+    assert torch.all(big[65:] == 3.0) and torch.all(big[:, 0] == 3.0)
+    t = lambda y: y.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    assert torch.equal(ssm.attn_prefill(t(q), t(k), t(v), cu, scale=0.3)[:65], out[:65])
+
+
+def test_attn_prefill_bad_offsets_are_clamped():
+    """Offsets outside the tensors are clamped, descending ones make empty sequences: no access past an end."""
+    q, k, v = packed(12, 50, 2, 1, 64, "bf16")
+    cu_q = torch.tensor([-5, 20, 10, 1000], dtype=torch.int32, device=DEV)
+    cu_k = torch.tensor([0, 20, 2 ** 31 - 1, 50], dtype=torch.int32, device=DEV)
+    out = torch.zeros(50, 2, 64, dtype=torch.bfloat16, device=DEV)
+    ssm.attn_prefill(q, k, v, cu_q, cu_k, out=out)
+    ref = O.prefill(f64(q)[:20], f64(k), f64(v), [0, 20], [0, 20], True, 64 ** -0.5)
+    check_attn(out[:20][:10], None, [r[:10] for r in ref], "bf16", 64, "first sequence")
+
+
+def test_attn_prefill_large_scores():
+    """Scores of +-10^4: the running maximum has to be subtracted before the exponential."""
+    lens = [200]
+    q, k, v, cu_q, cu_k = prefill_case(lens, [0], 2, 2, 64, "f32")
+    q = q * 100
+    k = k * 100
+    cq = torch.from_numpy(cu_q).to(DEV)
+    out = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cq)
+    ref = O.prefill(f64(q), f64(k), f64(v), cu_q, cu_k, True, 64 ** -0.5)
+    check_attn(out, None, ref, "f32", 64, "large scores")
+
+
+# ---------------------------------------------------------------- decode
+
+DECODE = [  # lens, Hq, Hkv, D, page, kind
+    ([1], 1, 1, 8, 16, "int8"), ([17], 2, 1, 64, 16, "e4m3"), ([0, 5, 64, 65], 4, 2, 64, 16, "io"),
+    ([300, 1], 12, 4, 72, 16, "int8"), ([129, 1000], 8, 1, 128, 64, "e4m3"), ([33], 16, 1, 80, 32, "int8"),
+    ([50, 2], 17, 1, 64, 16, "e4m3"), ([70], 40, 2, 40, 1024, "int8"), ([90], 4, 4, 256, 16, "e4m3"),
+    ([31, 32, 33], 6, 2, 192, 32, "int8"), ([513], 3, 1, 136, 64, "io"), ([2500], 2, 2, 128, 64, "int8"),
+    ([7] * 70, 2, 1, 64, 16, "io"), ([40], 32, 1, 256, 16, "io"),
+]
+
+
+def decode_case(lens, Hq, Hkv, D, page, kind, io, seed=20):
+    need = [-(-max(n, 0) // page) for n in lens]
+    pages = sum(need) + 2
+    c = new_cache(pages, Hkv, page, D, kind, io)  # everything unwritten is NaN (int8: 127 times NaN)
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(seed))
+    W = max(max(need), 1) + 1
+    table = torch.full((len(lens), W), -1, dtype=torch.int32)
+    at, slots = 0, []
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        j = torch.arange(max(n, 0))
+        slots.append(table[b, j // page].long() * page + j % page)
+    slots = torch.cat(slots).to(DEV)
+    x = rnd(seed, max(len(slots), 1), 2 * Hkv, D, io=io).to(DEV)[:len(slots)]
+    if len(slots):
+        ssm.kv_write(x[:, :Hkv], x[:, Hkv:], c, slots)
+    return c, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), rnd(seed + 1, len(lens), Hq, D, io=io).to(DEV)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", DECODE)
+def test_attn_decode(case, io):
+    lens, Hq, Hkv, D, page, kind = case
+    c, table, n, q = decode_case(lens, Hq, Hkv, D, page, kind, io)
+    lse = torch.empty(len(lens), Hq, device=DEV)
+    out = ssm.attn_decode_step(q, c, table, n, lse=lse)
+    ref = O.decode(f64(q), values(c, "k"), values(c, "v"), table.cpu().numpy(), lens, D ** -0.5)
+    check_attn(out, lse, ref, io, D, f"{case}")
+    assert torch.equal(ssm.attn_decode_step(q, c, table, n), out)  # the same bits again
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3", "io"])
+def test_attn_decode_bad_pages_and_lengths(kind):
+    """Pages outside the cache are not seen, lengths are clamped to the table, NaN past a length stays out."""
+    lens, page = [100, 64, 40, 33], 16
+    c, table, n, q = decode_case(lens, 4, 2, 64, page, kind, "bf16")
+    table[0, 2] = 10 ** 6
+    table[1, 0] = -7
+    table[2, :] = 2 ** 31 - 1
+    n = torch.tensor([100, 64, 40, -3], dtype=torch.int32, device=DEV)
+    lse = torch.empty(4, 4, device=DEV)
+    out = ssm.attn_decode_step(q, c, table, n, lse=lse)
+    ref = O.decode(f64(q), values(c, "k"), values(c, "v"), table.cpu().numpy(), n.cpu().numpy(), 64 ** -0.5)
+    check_attn(out, lse, ref, "bf16", 64, "bad pages")
+    assert torch.all(out[2:] == 0)
+    # a length past the table is the table's
+    full = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    full[0, 0], full[0, 1] = int(table[3, 0]), int(table[3, 1])
+    a = ssm.attn_decode_step(q[3:4], c, full, torch.tensor([2 ** 31 - 1], dtype=torch.int32, device=DEV))
+    b = ssm.attn_decode_step(q[3:4], c, full, torch.tensor([32], dtype=torch.int32, device=DEV))
+    assert torch.equal(a, b)
+
+
+def test_attn_decode_strided_q_and_out():
+    c, table, n, q = decode_case([45, 80], 4, 2, 64, 16, "e4m3", "bf16")
+    want = ssm.attn_decode_step(q, c, table, n)
+    wide = torch.zeros(2, 7, 64, dtype=torch.bfloat16, device=DEV)
+    wide[:, 2:6] = q
+    big = torch.full((2, 6, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    ssm.attn_decode_step(wide[:, 2:6], c, table, n, out=big[:, :4])
+    assert torch.equal(big[:, :4], want) and torch.all(big[:, 4:] == 5.0)
+
+
+def test_prefill_and_decode_agree():
+    """The last token of a prompt by attn_prefill, and by attn_decode_step against the cache that the prompt
+    left (unquantised): the same formula, so both are within their tolerance of it."""
+    T, Hq, Hkv, D, page = 75, 8, 2, 128, 16
+    q, k, v = packed(30, T, Hq, Hkv, D, "bf16")
+    c = new_cache(6, Hkv, page, D, "io", "bf16")
+    ssm.kv_write(k, v, c, torch.arange(T, device=DEV))
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    whole = ssm.attn_prefill(q, k, v, cu)
+    one = ssm.attn_decode_step(q[-1:], c, torch.arange(6, dtype=torch.int32, device=DEV)[None],
+                               torch.tensor([T], dtype=torch.int32, device=DEV))
+    ref = O.prefill(f64(q), f64(k), f64(v), [0, T], [0, T], True, D ** -0.5)
+    check_attn(whole, None, ref, "bf16", D, "prefill")
+    check_attn(one, None, [r[-1:] for r in ref], "bf16", D, "decode")
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+def test_attn_on_another_stream():
+    s = torch.cuda.Stream()
+    c, table, n, q = decode_case([500, 30], 8, 2, 128, 16, "int8", "bf16")
+    want = ssm.attn_decode_step(q, c, table, n)
+    qp, k, v = packed(31, 200, 4, 2, 64, "bf16")
+    cu = torch.tensor([0, 90, 200], dtype=torch.int32, device=DEV)
+    wantp = ssm.attn_prefill(qp, k, v, cu)
+    s.wait_stream(torch.cuda.current_stream())
+    got = [ssm.attn_decode_step(q, c, table, n, stream=s) for _ in range(3)]
+    gotp = ssm.attn_prefill(qp, k, v, cu, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(g, want) for g in got) and torch.equal(gotp, wantp)
+
+
+def test_attn_decode_graph_replays():
+    """A decode step (rotation, cache write, attention) captured once and replayed with new inputs in the
+    same buffers, against the eager calls."""
+    B, Hq, Hkv, D, page = 3, 8, 2, 64, 16
+    lens0 = [40, 7, 100]
+    c, table, n, _ = decode_case(lens0, Hq, Hkv, D, page, "e4m3", "bf16")
+    c2 = ssm.KVCache(c.k.clone(), c.v.clone(), c.k_scale.clone(), c.v_scale.clone())
+    freq, m = ssm.rope_frequencies(D, device=DEV)
+    x = torch.empty(B, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    n += 1
+    ws = torch.empty(max(1, ssm.attn_decode_workspace_bytes(B, Hq, c, table.shape[1])), dtype=torch.uint8, device=DEV)
+    slots, pos = torch.empty(B, dtype=torch.int64, device=DEV), torch.empty(B, dtype=torch.int64, device=DEV)
+    qo, out = (torch.empty(B, Hq, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def fill(i):
+        x.copy_(rnd(40 + i, B, Hq + 2 * Hkv, D).to(DEV))
+        pos.copy_(n.long() - 1)
+        slots.copy_(table.long().gather(1, (pos // page)[:, None])[:, 0] * page + pos % page)
+
+    def step(cache):
+        ssm.kv_write(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache, slots, q=x[:, :Hq], positions=pos, freq=freq, q_out=qo)
+        ssm.attn_decode_step(qo, cache, table, n, out=out, workspace=ws)
+
+    fill(0)
+    step(c2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(c)
+    for i in range(4):
+        fill(i)
+        g.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        step(c2)
+        assert torch.equal(out, got), i
+        assert torch.equal(c.k.view(torch.uint8), c2.k.view(torch.uint8))
+        n += 1
