@@ -17,20 +17,21 @@
  *   rotation   pair i < pairs of a head holds (a, b) = (x[2i], x[2i+1]) (interleaved) or
  *              (x[i], x[i + pairs]) (half); with angle w = position * freq[i],
  *              (a, b) <- mscale * (a cos w - b sin w, b cos w + a sin w); the rest of the head
- *              stays as it is.  The angle is reduced in fp64, so far positions keep their digits;
- *              the rest is fp32, rounded once to the io dtype.
+ *              stays as it is.  The angle is reduced as a sum of two fp64, so positions below 2^53
+ *              keep their digits; the rest is fp32, rounded once to the io dtype.
  *   attention  s[i, j] = scale * <q_i, k_j>, o_i = sum_j e^(s_ij - m_i) v_j / sum_j e^(s_ij - m_i),
  *              m_i = max_j s_ij, over the keys j that query i sees; lse_i = m_i + ln(sum).  A query
  *              that sees no key gives o_i = 0 and lse_i = -inf.
  *   8-bit rows one fp32 scale per cached row (one token's key or value of one head):
- *              amax = max |x|, s = amax / top, m = top / amax (correctly rounded fp32 divisions),
- *              top = 127 (int8) or 448 (e4m3); code = clamp(x * m, -top, top) rounded to nearest
+ *              amax = max |x|, s = amax * (1 / top), m = (1 / amax) * top (each operation rounded
+ *              to fp32), top = 127 (int8) or 448 (e4m3); code = clamp(x * m, -top, top) rounded to nearest
  *              even; value = code * s.  Rows with amax < 2^-100 get s = 0 and codes 0 (m would
  *              overflow).  x is the io-dtype value (a rotated key is rounded to the io dtype first).
  *
  * Views.  A [T, H, D] tensor is a base pointer with a token and a head stride in elements (the D
  * values of a head are contiguous), so the heads of a packed q/k/v projection are used in place.
- * Base pointers are 16-byte aligned and strides are multiples of 16 bytes.  Strides are >= 0.
+ * Base pointers are 16-byte aligned and strides are multiples of 16 bytes, token strides in
+ * [0, 2^23] elements, head strides in [0, 2^48].
  *
  * Cache.  k and v are [pages, Hkv, page_size, D] in kv_dtype and k_scale, v_scale
  * [pages, Hkv, page_size] fp32 (8-bit types; NULL otherwise).  page_size is a power of two in

@@ -44,8 +44,8 @@ def quantize(x, kind):
     amax = np.abs(x).max(-1)
     live = amax >= np.float32(2.0 ** -100)
     safe = np.where(live, amax, np.float32(1))
-    scale = np.where(live, safe / top, np.float32(0))
-    mult = np.where(live, top / safe, np.float32(0))
+    scale = np.where(live, safe * (np.float32(1) / top), np.float32(0))
+    mult = np.where(live, (np.float32(1) / safe) * top, np.float32(0))
     y = np.clip(x * mult[..., None], -top, top)
     return (np.rint(y).astype(np.float64) if kind == "int8" else to_e4m3(y)), scale
 

@@ -64,7 +64,9 @@ inline Span span(const void* p, int64_t bytes) {
 inline bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 constexpr int64_t MAX_TOKENS = INT32_MAX;
-constexpr int64_t MAX_STRIDE = int64_t(1) << 31;  // elements; keeps (tokens + heads) * stride in int64
+// Largest strides in elements: 64 tokens of fp32 stay within 2^31 bytes (a tile's offsets are 32-bit), and
+// all byte counts within int64.
+constexpr int64_t MAX_TOKEN_STRIDE = int64_t(1) << 23, MAX_HEAD_STRIDE = int64_t(1) << 48;
 
 inline int check_io(int32_t io_dtype, int64_t* es) {
   if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
@@ -80,7 +82,8 @@ inline int check_heads(int32_t heads, int32_t head_dim) {
 
 inline int check_view(const ssm_view* v, int64_t es) {
   if (!v || !v->data) return SSM_ERR_NULL;
-  if (v->token_stride < 0 || v->head_stride < 0 || v->token_stride > MAX_STRIDE || v->head_stride > MAX_STRIDE)
+  if (v->token_stride < 0 || v->head_stride < 0 || v->token_stride > MAX_TOKEN_STRIDE ||
+      v->head_stride > MAX_HEAD_STRIDE)
     return SSM_ERR_SHAPE;
   if (!aligned(v->data, 16) || v->token_stride * es % 16 || v->head_stride * es % 16) return SSM_ERR_ALIGN;
   return SSM_OK;

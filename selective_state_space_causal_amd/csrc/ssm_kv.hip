@@ -233,7 +233,7 @@ __global__ __launch_bounds__(TPB) void kv_rows(RowArgs a) {
           for (int m = 1; m < LPR; m <<= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
           constexpr float TOP = KV == SSM_KV_I8 ? 127.0f : 448.0f;
           const bool live = amax >= 0x1p-100f;
-          const float m = live ? TOP / amax : 0.0f;
+          const float m = live ? (1.0f / amax) * TOP : 0.0f;
           char* dp = base + row * a.D;
 #pragma unroll
           for (int n = 0; n < NIT; ++n)
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(TPB) void kv_rows(RowArgs a) {
               store_codes<KV, VW>(dp + at[n], xa[n], m);
               store_codes<KV, VW>(dp + bt[n], xb[n], m);
             }
-          if (lig == 0) (is_k ? a.c.ks : a.c.vs)[row] = live ? amax / TOP : 0.0f;
+          if (lig == 0) (is_k ? a.c.ks : a.c.vs)[row] = live ? amax * (1.0f / TOP) : 0.0f;
         }
       }
     }
