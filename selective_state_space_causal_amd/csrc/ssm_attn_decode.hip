@@ -3,24 +3,30 @@
 //
 // The cache is read once, and that bounds it.  The query heads of a key head (up to 16 at a time) are
 // the columns of 16x16 matrix products, so a key is read once for all of them: S^T = K Q^T, then
-// O^T = V^T P^T with the softmax's running maximum and sum.  A wave works on 32 keys at a time.  Row m of
-// score tile t stands for key 8 (m / 4) + 4 t + m % 4 of the 32, which gives lane quarter w the weights
-// of keys 8 w .. 8 w + 7 in order: what the second product's right operand wants.  Its left operand
-// needs V with keys along a lane's registers; the wave passes V through its own LDS and the LDS read that
-// transposes (16-bit and 8-bit elements).  The long axis is split over waves; their partial results
-// (maximum, sum, unnormalised output, fp32) are joined by a second kernel in split order.
+// O^T = V^T P^T with the softmax's running maximum and sum.
+//
+// A wave works on 32 keys at a time, straight from memory to registers:
+//   K  row m of score tile t is key 8 (m / 4) + 4 t + m % 4 of the 32, which leaves lane quarter w with
+//      the weights of keys 8 w .. 8 w + 7 in order, as the second product's right operand wants them.  The
+//      channels of a product may come in any order if Q's do too, so a lane reads whole 16-byte pieces.
+//   V  the second product's left operand needs one channel's keys along a lane's registers.  Quarter w
+//      reads its 8 keys, lane m of it VE neighbouring channels of each, and the 8 x VE block is turned in
+//      registers while it is widened; tile c of the output then is channels m VE + c, and a
+//      lane ends with 4 VE neighbouring channels of one head.
+// The next 32 keys are loaded while these are worked on, the page numbers one step earlier still.
+//
+// The long axis is split into chunks, one workgroup each; its waves take 32 keys in turn and join their
+// results in LDS.  With more than one chunk the partial results (maximum, sum, unnormalised output, fp32)
+// are joined by a second kernel.  Both joins add in a fixed order.
 #include "ssm_attn.h"
 
 namespace ssm {
 namespace attn {
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef int i32x2 __attribute__((ext_vector_type(2)));
-#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
-
 constexpr int STEP = 32;  // keys of a wave's step
-constexpr int COLS = 16;  // query heads of a wave
+constexpr int COLS = 16;  // query heads of a workgroup
+constexpr int NW = 4;     // waves of a workgroup
 
 struct DecodeArgs {
   View q, out;
@@ -30,11 +36,14 @@ struct DecodeArgs {
   const int32_t* lens;
   int64_t W;  // table width
   int B, Hq, G, groups;  // groups: 16-head groups of a key head
-  int splits;
+  int chunks;            // most chunks of a sequence
+  int64_t work;          // workgroups
   float scale_log2;
-  float* po;  // [B, Hq, splits, D]
-  float* ml;  // [B, Hq, splits, 2]: maximum (of scores * log2 e), sum
+  float* po;  // [B, Hq, chunks, D]
+  float* ml;  // [B, Hq, chunks, 2]: maximum (of scores * log2 e), sum
 };
+
+constexpr int MIN_SHARE = 8;   // steps of a chunk, at least: two for each wave
 
 __device__ __forceinline__ int sequence_length(const DecodeArgs& a, int b) {
   const int64_t cap = a.W << a.c.page_shift;
@@ -42,297 +51,434 @@ __device__ __forceinline__ int sequence_length(const DecodeArgs& a, int b) {
   return (int)(n < 0 ? 0 : n > cap ? cap : n);
 }
 
-// Eight codes as bf16 (exact: an int8 or e4m3 value has at most 7 significant bits).
-template <int KV>
-__device__ __forceinline__ u32x4 widen_bf16(u32x2 w) {
-  u32x4 r;
-  if constexpr (KV == SSM_KV_I8) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned x = w[j / 2] >> (16 * (j & 1));
-      r[j] = pack_bf16((float)(int8_t)x, (float)(int8_t)(x >> 8));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      r[2 * j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, false));
-      r[2 * j + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.0f, true));
-    }
-  }
-  return r;
+// Steps of each of a sequence's chunks: equal shares, but no smaller ones than MIN_SHARE.
+__device__ __forceinline__ int share_of(const DecodeArgs& a, int steps) {
+  return max((steps + a.chunks - 1) / a.chunks, MIN_SHARE);
 }
+
+// The two 16-bit halves of a and b as pairs (a.lo, b.lo) and (a.hi, b.hi).
+__device__ __forceinline__ unsigned pair_lo(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ unsigned pair_hi(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
 // Code j of a word as fp32.
 template <int KV>
-__device__ __forceinline__ f32x4 widen_f32(unsigned w) {
-  if constexpr (KV == SSM_KV_I8) {
-    return f32x4{(float)(int8_t)w, (float)(int8_t)(w >> 8), (float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24)};
+__device__ __forceinline__ float widen_one(unsigned w, int j) {
+  if constexpr (KV == SSM_KV_I8) return (float)(int8_t)(w >> (8 * j));
+  const auto x = j < 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false) : __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  return x[j & 1];
+}
+
+// Codes 2 p and 2 p + 1 of a word as bf16 (exact: an int8 or e4m3 value has at most 8 significant bits).
+template <int KV>
+__device__ __forceinline__ unsigned widen_pair(unsigned w, int p) {
+  if constexpr (KV == SSM_KV_I8) return pack_bf16(widen_one<KV>(w, 2 * p), widen_one<KV>(w, 2 * p + 1));
+  return p == 0 ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false))
+                : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+}
+
+// Element c of one channel piece as fp32: V words w of VE elements of CS bytes.
+template <int KV, int CS>
+__device__ __forceinline__ float element_f32(const unsigned* w, int c) {
+  if constexpr (CS == 4) return __uint_as_float(w[c]);
+  else return widen_one<KV>(w[c / 4], c % 4);
+}
+
+__device__ __forceinline__ float quarters_max(float x) {  // over the lanes with the same lane & 15
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quarters_sum(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(unsigned* w, const char* p) {
+  if constexpr (BYTES == 16) {
+    const u32x4 x = *reinterpret_cast<const u32x4_a4*>(p);
+    w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3];
+  } else if constexpr (BYTES == 8) {
+    const u32x2 x = *reinterpret_cast<const u32x2_a4*>(p);
+    w[0] = x[0], w[1] = x[1];
   } else {
-    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-    return f32x4{lo[0], lo[1], hi[0], hi[1]};
+    w[0] = *reinterpret_cast<const unsigned*>(p);
   }
 }
 
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
-// CS: bytes of a cached element.  NW waves of a workgroup, each a split of its own.
-template <typename IO, int KV, int DP, int NW>
+// A workgroup is one (chunk, 16 heads of a key head, sequence).
+template <typename IO, int KV, int DP>
 __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
   constexpr bool BF = sizeof(IO) == 2;
-  constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1, ND = DP / 16;
-  __shared__ __attribute__((aligned(16))) char lds[NW][STEP * DP * CS];
+  constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1;
+  // K: pieces of KB bytes; 16, but 8 of 8-bit codes where a row may be that short
+  constexpr int KB = CS == 1 && DP == 64 ? 8 : 16, KE = KB / CS, NK = DP / (4 * KE), KW = KB / 4;
+  // V: VE channels of a lane, NB blocks of 16 VE channels
+  constexpr int VE = CS == 4 || DP % 128 ? 4 : 8, NB = DP / (16 * VE), VW = VE * CS / 4;
+  constexpr bool AHEAD = CS == 1 || (CS == 2 && DP <= 128);  // the next keys' registers fit beside these
+  __shared__ float wml[NW][COLS][2];
+  extern __shared__ __attribute__((aligned(16))) float wo[];  // [NW][heads][16 VE]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, w4 = lane >> 4;
-  char* vt = lds[wave];
-  const int split = blockIdx.x * NW + wave, b = blockIdx.z;
-  const int kh = blockIdx.y / a.groups, g0 = (blockIdx.y - kh * a.groups) * COLS;
-  if (split >= a.splits) return;
-  const int D = a.c.D, len = sequence_length(a, b);
-  const int page_mask = (1 << a.c.page_shift) - 1;
-  // Equal shares of whole steps.
-  const int steps = (len + STEP - 1) / STEP, share = (steps + a.splits - 1) / a.splits;
-  const int first = min((int64_t)split * share, (int64_t)steps) * STEP;
-  const int last = (int)min((int64_t)len, (int64_t)first + (int64_t)share * STEP);
+  const int D = a.c.D, row_bytes = D * CS, page_mask = (1 << a.c.page_shift) - 1;
+  const int pages = (int)(a.c.slots >> a.c.page_shift);
 
-  const int g = g0 + col;
-  const bool live = g < a.G;
-  const int head = kh * a.G + min(g, a.G - 1);
-  const char* qp = a.q.p + (int64_t)b * a.q.ts + (int64_t)head * a.q.hs;
-  constexpr int NQ = BF ? DP / 32 : DP / 16, QC = 16 / (int)sizeof(IO);
-  u32x4 qf[NQ];
+  for (int64_t unit = blockIdx.x; unit < a.work; unit += gridDim.x) {
+    const int chunk = (int)(unit % a.chunks);
+    const int64_t uh = unit / a.chunks;
+    const int heads = a.c.heads * a.groups, b = (int)(uh / heads), kg = (int)(uh - (int64_t)b * heads);
+    const int kh = kg / a.groups, g0 = (kg - kh * a.groups) * COLS, ng = min(a.G - g0, COLS);
+    const int len = sequence_length(a, b), steps = (len + STEP - 1) / STEP, share = share_of(a, steps);
+    const int s_end = min(chunk * (int64_t)share + share, (int64_t)steps);
+    if (chunk > 0 && chunk * (int64_t)share >= steps) continue;
+
+    const int head = kh * a.G + g0 + min(col, ng - 1);
+    const char* qp = a.q.p + (int64_t)b * a.q.ts + (int64_t)head * a.q.hs;
+    // Q in the order of K's pieces.  Where a row ends, a lane reads an earlier piece of it against zeros.
+    int koff[NK];
+    unsigned qf[NK][KE * (BF ? 2 : 4) / 4];
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int e = (4 * i + w4) * QC;
-    qf[i] = e < D ? *reinterpret_cast<const u32x4*>(qp + e * (int)sizeof(IO)) : u32x4{0, 0, 0, 0};
-  }
-  f32x4 o[ND] = {};
-  float m = -INFINITY, l = 0.0f;
-  const int32_t* table = a.table + (int64_t)b * a.W;
-
-  // Row of the cache that holds a key of this head, or -1.
-  const auto row_of = [&](int key) -> int64_t {
-    if (key >= last) return -1;
-    const int64_t page = table[key >> a.c.page_shift];
-    if (page < 0 || page >= (a.c.slots >> a.c.page_shift)) return -1;
-    return ((page * a.c.heads + kh) << a.c.page_shift) + (key & page_mask);
-  };
-
-  for (int j0 = first; j0 < last; j0 += STEP) {
-    // V rows into LDS, zeros where no key is.
-    constexpr int VB = CS == 1 ? 8 : 16, VC = DP * CS / VB;  // bytes of a piece, pieces of a row
-#pragma unroll 4
-    for (int c = lane; c < STEP * VC; c += 64) {
-      const int row = c / VC, piece = c - row * VC;
-      const int64_t at = row_of(j0 + row);
-      const bool in = at >= 0 && piece * VB < D * CS;
-      if constexpr (CS == 1) {
-        u32x2 x = {0, 0};
-        if (in) x = *reinterpret_cast<const u32x2_a4*>(a.c.v + at * D + piece * 8);
-        *reinterpret_cast<u32x2*>(vt + row * DP + piece * 8) = x;
-      } else {
+    for (int i = 0; i < NK; ++i) {
+      const int e = (4 * i + w4) * KE;
+      koff[i] = (e + KE <= D ? e : e < D ? D - KE : 0) * CS;
+      constexpr int QE = BF ? 8 : 4;  // elements of a 16-byte read of q
+#pragma unroll
+      for (int h = 0; h < KE / QE; ++h) {
+        const int at = koff[i] / CS + h * QE;
         u32x4 x = {0, 0, 0, 0};
-        if (in) x = *reinterpret_cast<const u32x4*>(a.c.v + at * D * CS + piece * 16);
-        *reinterpret_cast<u32x4*>(vt + row * DP * CS + piece * 16) = x;
+        if (at >= e && at < D) x = *reinterpret_cast<const u32x4*>(qp + at * (int)sizeof(IO));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[i][4 * h + j] = x[j];
       }
     }
-    wave_lds_fence();
+    int voff[NB];  // channels past the row's end are made of its first ones and not stored
+#pragma unroll
+    for (int n = 0; n < NB; ++n) voff[n] = ((n * 16 + col) * VE < D ? (n * 16 + col) * VE : 0) * CS;
 
-    f32x4 s[2] = {};
+    f32x4 o[NB * VE] = {};
+    float m = -INFINITY, l = 0.0f;
+    const int32_t* table = a.table + (int64_t)b * a.W;
+
+    struct Keys {
+      unsigned k[2][NK][KW];
+      unsigned v[NB][8][VW];
+      f32x4 sk[2], sv[2];
+    };
+    // Pages of the two 16-key groups of a step (pages hold 16 tokens or more); -1 where there are no keys.
+    const auto page_of = [&](int step, int group) -> int {
+      const int key = step * STEP + 16 * group;
+      return step < s_end && key < len ? table[key >> a.c.page_shift] : -1;
+    };
+    const auto load = [&](Keys& x, int step, int p0, int p1) {
+      const auto row_of = [&](int page, int group) -> int64_t {  // an unseen group reads row 0
+        const int key = step * STEP + 16 * group;
+        return page >= 0 && page < pages ? (((int64_t)page * a.c.heads + kh) << a.c.page_shift) + (key & page_mask) : 0;
+      };
+      const int64_t r0 = row_of(p0, 0), r1 = row_of(p1, 1);
+      // K: key 8 (m / 4) + 4 t + m % 4 lies in group m / 8
+      const char* kp = a.c.k + ((col & 8 ? r1 : r0) + 8 * ((col >> 2) & 1) + (col & 3)) * row_bytes;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t at = row_of(j0 + 8 * (col >> 2) + 4 * t + (col & 3));
-      const char* kp = a.c.k + (at < 0 ? 0 : at) * D * CS;  // an unseen key's scores are replaced below
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int e = (4 * i + w4) * QC;
-        if constexpr (BF) {
-          u32x4 kf = {0, 0, 0, 0};
-          if (e < D) {
-            if constexpr (CS == 1) kf = widen_bf16<KV>(*reinterpret_cast<const u32x2_a4*>(kp + e));
-            else kf = *reinterpret_cast<const u32x4*>(kp + e * CS);
-          }
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf),
-                                                         __builtin_bit_cast(bf16x8, qf[i]), s[t], 0, 0, 0);
-        } else {
-          f32x4 kx = {0, 0, 0, 0};
-          if (e < D) {
-            if constexpr (CS == 1) kx = widen_f32<KV>(*reinterpret_cast<const unsigned*>(kp + e));
-            else kx = *reinterpret_cast<const f32x4*>(kp + e * CS);
-          }
-          const f32x4 qx = __builtin_bit_cast(f32x4, qf[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx[j], qx[j], s[t], 0, 0, 0);
-        }
-      }
-    }
-    // This lane's keys: j0 + 8 w4 + 4 t + i, all on one page (pages are multiples of 16 tokens).
-    const int key0 = j0 + 8 * w4;
-    const int64_t at0 = row_of(key0);
-    f32x4 sk[2] = {{1, 1, 1, 1}, {1, 1, 1, 1}}, sv[2] = {{1, 1, 1, 1}, {1, 1, 1, 1}};
-    if constexpr (KV != SSM_KV_IO) {
-      if (at0 >= 0) {
+        for (int i = 0; i < NK; ++i) load_words<KB>(x.k[t][i], kp + 4 * t * row_bytes + koff[i]);
+      const int64_t rv = (w4 & 2 ? r1 : r0) + 8 * (w4 & 1);
+      if constexpr (KV != SSM_KV_IO) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          sk[t] = *reinterpret_cast<const f32x4*>(a.c.ks + at0 + 4 * t);
-          sv[t] = *reinterpret_cast<const f32x4*>(a.c.vs + at0 + 4 * t);
+          x.sk[t] = *reinterpret_cast<const f32x4*>(a.c.ks + rv + 4 * t);
+          x.sv[t] = *reinterpret_cast<const f32x4*>(a.c.vs + rv + 4 * t);
         }
       }
-    }
-    float mx = m;
+      const char* vp = a.c.v + rv * row_bytes;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool seen = at0 >= 0 && key0 + 4 * t + i < last;
-        s[t][i] = seen ? s[t][i] * sk[t][i] * a.scale_log2 : -INFINITY;
-        sv[t][i] = seen ? sv[t][i] : 0.0f;
-        mx = fmaxf(mx, s[t][i]);
-      }
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mc = mx == -INFINITY ? 0.0f : mx;
-    const float alpha = hw_exp2(m - mc);
-    m = mx;
-    float sum = 0.0f;
+        for (int j = 0; j < 8; ++j) load_words<VE * CS>(x.v[n][j], vp + j * row_bytes + voff[n]);
+    };
+    const auto work = [&](Keys& x, int step, int p0, int p1) {
+      f32x4 s[2] = {};
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = hw_exp2(s[t][i] - mc);
-        sum += p;
-        s[t][i] = p * sv[t][i];
-      }
-    l = l * alpha + sum;  // this quarter's keys only; joined at the end
+        for (int i = 0; i < NK; ++i) {
+          if constexpr (BF) {
 #pragma unroll
-    for (int d = 0; d < ND; ++d) o[d] *= alpha;
-
-    if constexpr (BF) {
-      const u32x4 pf = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                        pack_bf16(s[1][2], s[1][3])};
+            for (int h = 0; h < KE / 8; ++h) {
+              u32x4 kf;
+              if constexpr (CS == 1)
+                kf = u32x4{widen_pair<KV>(x.k[t][i][2 * h], 0), widen_pair<KV>(x.k[t][i][2 * h], 1),
+                           widen_pair<KV>(x.k[t][i][2 * h + 1], 0), widen_pair<KV>(x.k[t][i][2 * h + 1], 1)};
+              else
+                kf = u32x4{x.k[t][i][0], x.k[t][i][1], x.k[t][i][2], x.k[t][i][3]};
+              const u32x4 q = {qf[i][4 * h], qf[i][4 * h + 1], qf[i][4 * h + 2], qf[i][4 * h + 3]};
+              s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf),
+                                                             __builtin_bit_cast(bf16x8, q), s[t], 0, 0, 0);
+            }
+          } else {
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        u32x4 vf;
-        if constexpr (CS == 1) {
-          // 16 lanes give 8 rows of 16 codes and get 8 rows of one channel each
-          const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              LDS_PTR(i32x2, vt + (8 * w4 + (col >> 1)) * DP + d * 16 + (col & 1) * 8));
-          vf = widen_bf16<KV>(u32x2{(unsigned)x[0], (unsigned)x[1]});
-        } else {
-          union {
-            s16x4 x[2];
-            u32x4 v;
-          } u;
-          const char* p = vt + ((8 * w4 + (col >> 2)) * DP + d * 16 + (col & 3) * 4) * 2;
-          u.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, p));
-          u.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, p + 4 * DP * 2));
-          vf = u.v;
+            for (int j = 0; j < KE; ++j)
+              s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(x.k[t][i], j), __uint_as_float(qf[i][j]),
+                                                          s[t], 0, 0, 0);
+          }
         }
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf),
-                                                       o[d], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (KV != SSM_KV_IO) s[t] *= x.sk[t];
+        s[t] *= a.scale_log2;
       }
-    } else {
+      const bool whole = step * STEP + STEP <= len && p0 >= 0 && p0 < pages && p1 >= 0 && p1 < pages;
+      if (!whole) {  // what lies in unseen places counts for nothing, whatever it holds
+        const int p = w4 & 2 ? p1 : p0, seen = p >= 0 && p < pages ? len - step * STEP - 8 * w4 : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool in = j < seen;
+          s[j / 4][j % 4] = in ? s[j / 4][j % 4] : -INFINITY;
+          if constexpr (KV != SSM_KV_IO) x.sv[j / 4][j % 4] = in ? x.sv[j / 4][j % 4] : 0.0f;
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) x.v[n][j][w] = in ? x.v[n][j][w] : 0u;
+        }
+      }
+      float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      mx = quarters_max(mx);
+      // The subtracted maximum follows the true one only when it has grown by 2^SLACK: weights stay below
+      // 2^SLACK, and the outputs are rescaled a few times in a sequence instead of at every step.
+      constexpr float SLACK = 8.0f;
+      if (__any(mx > m + SLACK)) {
+        const float to = mx > m ? mx : m;
+        const float alpha = hw_exp2(m - (to == -INFINITY ? 0.0f : to));
+        m = to;
+        l *= alpha;
+#pragma unroll
+        for (int c = 0; c < NB * VE; ++c) o[c] *= alpha;
+      }
+      const float mc = m == -INFINITY ? 0.0f : m;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = 8 * w4 + 4 * t + i;
+          const float p = hw_exp2(s[t][i] - mc);
+          l += p;  // this quarter's keys only; joined at the end
+          s[t][i] = KV != SSM_KV_IO ? p * x.sv[t][i] : p;
+        }
+      if constexpr (BF) {
+        const u32x4 pf = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                          pack_bf16(s[1][2], s[1][3])};
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const char* p = vt + (row * DP + d * 16 + col) * CS;
-            float x;
-            if constexpr (CS == 4) x = *reinterpret_cast<const float*>(p);
-            else x = widen_f32<KV>(*reinterpret_cast<const uint8_t*>(p))[0];
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, s[t][i], o[d], 0, 0, 0);
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int c = 0; c < VE; c += 2) {
+            u32x4 v0, v1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const unsigned* ra = x.v[n][2 * j];
+              const unsigned* rb = x.v[n][2 * j + 1];
+              if constexpr (KV == SSM_KV_I8) {
+                v0[j] = pack_bf16(widen_one<KV>(ra[c / 4], c % 4), widen_one<KV>(rb[c / 4], c % 4));
+                v1[j] = pack_bf16(widen_one<KV>(ra[c / 4], c % 4 + 1), widen_one<KV>(rb[c / 4], c % 4 + 1));
+              } else {
+                const unsigned wa = CS == 1 ? widen_pair<KV>(ra[c / 4], c % 4 / 2) : ra[c / 2];
+                const unsigned wb = CS == 1 ? widen_pair<KV>(rb[c / 4], c % 4 / 2) : rb[c / 2];
+                v0[j] = pair_lo(wa, wb);
+                v1[j] = pair_hi(wa, wb);
+              }
+            }
+            f32x4& o0 = o[n * VE + c];
+            f32x4& o1 = o[n * VE + c + 1];
+            o0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v0), __builtin_bit_cast(bf16x8, pf), o0,
+                                                         0, 0, 0);
+            o1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v1), __builtin_bit_cast(bf16x8, pf), o1,
+                                                         0, 0, 0);
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < VE; ++c)
+              o[n * VE + c] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(x.v[n][j], c), s[j / 4][j % 4],
+                                                                   o[n * VE + c], 0, 0, 0);
+      }
+    };
+
+    int step = chunk * share + wave;
+    if (step < s_end) {
+      int p0 = page_of(step, 0), p1 = page_of(step, 1);
+      if constexpr (AHEAD) {
+        Keys x;
+        load(x, step, p0, p1);
+        int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
+        for (; step < s_end; step += NW) {
+          Keys y;
+          if (step + NW < s_end) load(y, step + NW, n0, n1);
+          const int f0 = page_of(step + 2 * NW, 0), f1 = page_of(step + 2 * NW, 1);
+          work(x, step, p0, p1);
+          x = y;
+          p0 = n0, p1 = n1, n0 = f0, n1 = f1;
+        }
+      } else {
+        for (; step < s_end; step += NW) {
+          Keys x;
+          load(x, step, p0, p1);
+          const int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
+          work(x, step, p0, p1);
+          p0 = n0, p1 = n1;
+        }
+      }
+    }
+
+    // Join the waves: their outputs on one maximum, then sums in wave order.
+    l = quarters_sum(l);
+    __syncthreads();
+    if (w4 == 0) wml[wave][col][0] = m;
+    __syncthreads();
+    float top = wml[0][col][0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) top = fmaxf(top, wml[w][col][0]);
+    const float f = hw_exp2(m - (top == -INFINITY ? 0.0f : top));
+    if (w4 == 0) wml[wave][col][1] = l * f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      constexpr int BC = 16 * VE;  // channels of a block
+      if (n > 0) __syncthreads();
+      if (col < ng) {
+        float* at = wo + ((size_t)wave * ng + col) * BC + 4 * w4 * VE;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < VE; c += 4)
+            *reinterpret_cast<f32x4*>(at + i * VE + c) =
+                f32x4{o[n * VE + c][i], o[n * VE + c + 1][i], o[n * VE + c + 2][i], o[n * VE + c + 3][i]} * f;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < ng * (BC / 4); i += NW * 64) {
+        const int g = i / (BC / 4), e = n * BC + (i - g * (BC / 4)) * 4;
+        if (e >= D) continue;
+        f32x4 y = {};
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          y += *reinterpret_cast<const f32x4*>(wo + ((size_t)w * ng + g) * BC + (e - n * BC));
+          sum += wml[w][g][1];
+        }
+        const int hd = kh * a.G + g0 + g;
+        if (a.chunks == 1) {
+          y *= sum > 0.0f ? 1.0f / sum : 0.0f;
+          char* op = a.out.p + (int64_t)b * a.out.ts + (int64_t)hd * a.out.hs;
+          if constexpr (BF) *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+          else *reinterpret_cast<f32x4*>(op + e * 4) = y;
+        } else {
+          *reinterpret_cast<f32x4*>(a.po + (((int64_t)b * a.Hq + hd) * a.chunks + chunk) * D + e) = y;
+        }
+        if (e == 0) {
+          float hm = wml[0][g][0];
+#pragma unroll
+          for (int w = 1; w < NW; ++w) hm = fmaxf(hm, wml[w][g][0]);
+          const int64_t at = (int64_t)b * a.Hq + hd;
+          if (a.chunks > 1) {
+            a.ml[2 * (at * a.chunks + chunk)] = hm;
+            a.ml[2 * (at * a.chunks + chunk) + 1] = sum;
+          } else if (a.lse) {
+            a.lse[at] = sum > 0.0f ? (hm + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
           }
         }
-    }
-    wave_lds_fence();
-  }
-
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  if (!live) return;
-  if (a.splits == 1) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    char* op = a.out.p + (int64_t)b * a.out.ts + (int64_t)head * a.out.hs;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const int e = d * 16 + 4 * w4;
-      if (e >= D) continue;
-      const f32x4 x = o[d] * inv;
-      if constexpr (BF) *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-      else *reinterpret_cast<f32x4*>(op + e * 4) = x;
-    }
-    if (a.lse && w4 == 0)
-      a.lse[(int64_t)b * a.Hq + head] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-  } else {
-    const int64_t at = ((int64_t)b * a.Hq + head) * a.splits + split;
-    if (l > 0.0f) {
-      float* op = a.po + at * D;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-        if (d * 16 + 4 * w4 < D) *reinterpret_cast<f32x4*>(op + d * 16 + 4 * w4) = o[d];
-    }
-    if (w4 == 0) {
-      a.ml[2 * at] = m;
-      a.ml[2 * at + 1] = l;
+      }
     }
   }
 }
 
-// Joins the splits of one (sequence, head): a workgroup of 256 threads, thread e of the first D owning
-// channel e, the splits in order.
-template <typename IO>
-__global__ __launch_bounds__(256) void attn_decode_join(DecodeArgs a) {
-  const int64_t row = blockIdx.x;  // b * Hq + head
-  const float* ml = a.ml + row * a.splits * 2;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[2 * s]);
-  const float mc = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, x = 0.0f;
-  const int e = threadIdx.x;
-  for (int s = 0; s < a.splits; ++s) {
-    const float ls = ml[2 * s + 1];
-    if (!(ls > 0.0f)) continue;  // no key: no output was written
-    const float w = hw_exp2(ml[2 * s] - mc);
-    l += w * ls;
-    if (e < a.c.D) x += w * a.po[(row * a.splits + s) * a.c.D + e];
+constexpr int MAX_CHUNKS = 1024;
+constexpr int JOIN = 256;  // threads of a join
+
+// Joins the chunks of one (sequence, head): their weights first, then LP lanes for the row's channels
+// (4 each), JOIN / LP slices of the chunks, the slices added in order.
+template <typename IO, int LP>
+__global__ __launch_bounds__(JOIN) void attn_decode_join(DecodeArgs a) {
+  __shared__ float w[MAX_CHUNKS];
+  __shared__ float part[JOIN / 64][2];
+  __shared__ f32x4 acc[JOIN];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lp = tid % LP, slice = tid / LP, D = a.c.D;
+  for (int64_t row = blockIdx.x; row < (int64_t)a.B * a.Hq; row += gridDim.x) {
+    const int b = (int)(row / a.Hq), head = (int)(row - (int64_t)b * a.Hq);
+    const int steps = (sequence_length(a, b) + STEP - 1) / STEP, share = share_of(a, steps);
+    const int n = (steps + share - 1) / share;
+    const float* ml = a.ml + row * a.chunks * 2;
+    float m = -INFINITY;
+    for (int c = tid; c < n; c += JOIN) m = fmaxf(m, ml[2 * c]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    __syncthreads();  // the last row's use of the shared arrays is over
+    if (lane == 0) part[wave][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < JOIN / 64; ++x) m = fmaxf(m, part[x][0]);
+    const float mc = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    for (int c = tid; c < n; c += JOIN) {
+      const float f = hw_exp2(ml[2 * c] - mc);
+      w[c] = f;
+      l += f * ml[2 * c + 1];
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+    if (lane == 0) part[wave][1] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int x = 0; x < JOIN / 64; ++x) l += part[x][1];
+    f32x4 y = {};
+    if (lp * 4 < D) {
+      const float* po = a.po + row * a.chunks * D + lp * 4;
+#pragma unroll 4
+      for (int c = slice; c < n; c += JOIN / LP) y += *reinterpret_cast<const f32x4*>(po + (int64_t)c * D) * w[c];
+    }
+    acc[tid] = y;
+    __syncthreads();
+    if (slice == 0 && lp * 4 < D) {
+#pragma unroll
+      for (int x = 1; x < JOIN / LP; ++x) y += acc[x * LP + lp];
+      y *= l > 0.0f ? 1.0f / l : 0.0f;
+      char* op = a.out.p + (int64_t)b * a.out.ts + (int64_t)head * a.out.hs;
+      if constexpr (sizeof(IO) == 2)
+        *reinterpret_cast<u32x2*>(op + lp * 8) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+      else
+        *reinterpret_cast<f32x4*>(op + lp * 16) = y;
+    }
+    if (a.lse && tid == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
   }
-  const int b = (int)(row / a.Hq), head = (int)(row - (int64_t)b * a.Hq);
-  if (e < a.c.D) {
-    char* op = a.out.p + (int64_t)b * a.out.ts + (int64_t)head * a.out.hs;
-    const float y = l > 0.0f ? x / l : 0.0f;
-    if constexpr (sizeof(IO) == 2) reinterpret_cast<uint16_t*>(op)[e] = (uint16_t)pack_bf16(y, 0.0f);
-    else reinterpret_cast<float*>(op)[e] = y;
-  }
-  if (a.lse && e == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-constexpr int TARGET_WAVES = 4096;  // 16 waves for each of the 256 CUs
-constexpr int MIN_SHARE = 64;       // keys of a split that are worth one
-constexpr int MAX_SPLITS = 1024;
+constexpr int64_t TARGET = 8192;                // workgroups: several for each place on the chip, so uneven lengths even out
+constexpr int64_t MAX_GRID = int64_t(1) << 22;  // keeps a launch within 2^31 work-items
 
-int splits_of(int64_t batch, int q_heads, const ssm_kv_cache* c, int64_t table_width) {
+// Most chunks of a sequence, from what the host knows: the table's width, not the lengths.
+int chunks_of(int64_t batch, int q_heads, const ssm_kv_cache* c, int64_t table_width) {
   const int64_t groups = (q_heads / c->kv_heads + COLS - 1) / COLS;
-  const int64_t have = batch * c->kv_heads * groups, longest = table_width * c->page_size;
-  int64_t s = (TARGET_WAVES + have - 1) / have;
-  const int64_t most = (longest + MIN_SHARE - 1) / MIN_SHARE;
-  if (s > most) s = most;
-  if (s > MAX_SPLITS) s = MAX_SPLITS;
-  return (int)(s < 1 ? 1 : s);
+  const int64_t units = batch * c->kv_heads * groups, longest = table_width * c->page_size;
+  int64_t n = (TARGET + units - 1) / units;
+  const int64_t most = (longest + MIN_SHARE * STEP - 1) / (MIN_SHARE * STEP);
+  if (n > most) n = most;
+  if (n > MAX_CHUNKS) n = MAX_CHUNKS;
+  return (int)(n < 1 ? 1 : n);
 }
 
 template <typename IO, int KV, int DP>
 hipError_t launch_dp(const DecodeArgs& a, hipStream_t s) {
-  constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1;
-  constexpr int NW = STEP * DP * CS * 4 <= 65536 ? 4 : 2;  // 64 KB of LDS
-  const dim3 grid((a.splits + NW - 1) / NW, a.c.heads * a.groups, a.B), tb(NW * 64);
-  attn_decode<IO, KV, DP, NW><<<grid, tb, 0, s>>>(a);
+  constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1, VE = CS == 4 || DP % 128 ? 4 : 8;
+  const int ng = a.G < COLS ? a.G : COLS;
+  const dim3 grid((unsigned)(a.work < MAX_GRID ? a.work : MAX_GRID)), tb(NW * 64);
+  attn_decode<IO, KV, DP><<<grid, tb, NW * ng * 16 * VE * sizeof(float), s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && a.splits > 1) {
-    attn_decode_join<IO><<<dim3((unsigned)((int64_t)a.B * a.Hq)), dim3(256), 0, s>>>(a);
+  if (e == hipSuccess && a.chunks > 1) {
+    const int64_t rows = (int64_t)a.B * a.Hq;
+    const dim3 jgrid((unsigned)(rows < MAX_GRID ? rows : MAX_GRID));
+    attn_decode_join<IO, DP <= 64 ? 16 : DP <= 128 ? 32 : 64><<<jgrid, dim3(JOIN), 0, s>>>(a);
     e = hipGetLastError();
   }
   return e;
@@ -376,8 +522,8 @@ size_t ssm_attn_decode_workspace_bytes(int64_t batch, int32_t q_heads, const ssm
                                        int64_t table_width) {
   using namespace ssm::attn;
   if (!cache || check_decode_sizes(batch, q_heads, cache, table_width) != SSM_OK) return 0;
-  const int s = splits_of(batch, q_heads, cache, table_width);
-  return s == 1 ? 0 : (size_t)batch * q_heads * s * (cache->head_dim + 2) * sizeof(float);
+  const int n = chunks_of(batch, q_heads, cache, table_width);
+  return n == 1 ? 0 : (size_t)batch * q_heads * n * (cache->head_dim + 2) * sizeof(float);
 }
 
 int ssm_attn_decode_step(int64_t batch, int32_t q_heads, int32_t io_dtype, float scale, const ssm_kv_cache* cache,
@@ -418,11 +564,12 @@ int ssm_attn_decode_step(int64_t batch, int32_t q_heads, int32_t io_dtype, float
   a.Hq = q_heads;
   a.G = q_heads / cache->kv_heads;
   a.groups = (a.G + COLS - 1) / COLS;
-  a.splits = splits_of(batch, q_heads, cache, table_width);
+  a.chunks = chunks_of(batch, q_heads, cache, table_width);
+  a.work = batch * cache->kv_heads * a.groups * a.chunks;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!isfinite(a.scale_log2) || !(a.scale_log2 > 0.0f)) return SSM_ERR_SHAPE;
   a.po = static_cast<float*>(workspace);
-  a.ml = a.po + (int64_t)batch * q_heads * a.splits * cache->head_dim;
+  a.ml = a.po + (int64_t)batch * q_heads * a.chunks * cache->head_dim;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = io_dtype == SSM_BF16 ? launch_decode_attn<ssm::bf16_t>(a, cache->kv_dtype, s)
                                             : launch_decode_attn<float>(a, cache->kv_dtype, s);
