@@ -13,7 +13,9 @@
 //      reads its 8 keys, lane m of it VE neighbouring channels of each, and the 8 x VE block is turned in
 //      registers while it is widened; tile c of the output then is channels m VE + c, and a
 //      lane ends with 4 VE neighbouring channels of one head.
-// The next 32 keys are loaded while these are worked on, the page numbers one step earlier still.
+// Loads are hidden by the other waves of a SIMD: three of them, with registers for one set of keys each, measured
+// better than two that load 32 keys ahead (64 sequences of up to 8192 int8 tokens, 8 key heads of 128: 137 us
+// against 171).  The page numbers are read a step ahead.
 //
 // The long axis is split into chunks, one workgroup each; its waves take 32 keys in turn and join their
 // results in LDS.  With more than one chunk the partial results (maximum, sum, unnormalised output, fp32)
@@ -37,7 +39,6 @@ struct DecodeArgs {
   int64_t W;  // table width
   int B, Hq, G, groups;  // groups: 16-head groups of a key head
   int chunks;            // most chunks of a sequence
-  int64_t work;          // workgroups
   float scale_log2;
   float* po;  // [B, Hq, chunks, D]
   float* ml;  // [B, Hq, chunks, 2]: maximum (of scores * log2 e), sum
@@ -111,25 +112,25 @@ __device__ __forceinline__ void load_words(unsigned* w, const char* p) {
 
 // A workgroup is one (chunk, 16 heads of a key head, sequence).
 template <typename IO, int KV, int DP>
-__global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
+__global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SSM_KV_IO ? 2 : 3) void attn_decode(DecodeArgs a) {
   constexpr bool BF = sizeof(IO) == 2;
   constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1;
   // K: pieces of KB bytes; 16, but 8 of 8-bit codes where a row may be that short
   constexpr int KB = CS == 1 && DP == 64 ? 8 : 16, KE = KB / CS, NK = DP / (4 * KE), KW = KB / 4;
   // V: VE channels of a lane, NB blocks of 16 VE channels
   constexpr int VE = CS == 4 || DP % 128 ? 4 : 8, NB = DP / (16 * VE), VW = VE * CS / 4;
-  constexpr bool AHEAD = CS == 1 || (CS == 2 && DP <= 128);  // the next keys' registers fit beside these
+  constexpr bool HOLD_V = CS * DP < 1024;  // V's registers fit beside K's; if not, its rows are read as they are used
   __shared__ float wml[NW][COLS][2];
   extern __shared__ __attribute__((aligned(16))) float wo[];  // [NW][heads][16 VE]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, w4 = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, w4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = a.c.D, row_bytes = D * CS, page_mask = (1 << a.c.page_shift) - 1;
   const int pages = (int)(a.c.slots >> a.c.page_shift);
 
-  for (int64_t unit = blockIdx.x; unit < a.work; unit += gridDim.x) {
-    const int chunk = (int)(unit % a.chunks);
-    const int64_t uh = unit / a.chunks;
-    const int heads = a.c.heads * a.groups, b = (int)(uh / heads), kg = (int)(uh - (int64_t)b * heads);
-    const int kh = kg / a.groups, g0 = (kg - kh * a.groups) * COLS, ng = min(a.G - g0, COLS);
+  const int chunk = blockIdx.x, kh = blockIdx.y / a.groups;
+  const int g0 = (blockIdx.y - kh * a.groups) * COLS, ng = min(a.G - g0, COLS);
+
+  for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
     const int len = sequence_length(a, b), steps = (len + STEP - 1) / STEP, share = share_of(a, steps);
     const int s_end = min(chunk * (int64_t)share + share, (int64_t)steps);
     if (chunk > 0 && chunk * (int64_t)share >= steps) continue;
@@ -163,7 +164,8 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
 
     struct Keys {
       unsigned k[2][NK][KW];
-      unsigned v[NB][8][VW];
+      unsigned v[HOLD_V ? NB : 1][HOLD_V ? 8 : 1][VW];
+      const char* vp;
       f32x4 sk[2], sv[2];
     };
     // Pages of the two 16-key groups of a step (pages hold 16 tokens or more); -1 where there are no keys.
@@ -191,11 +193,13 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
           x.sv[t] = *reinterpret_cast<const f32x4*>(a.c.vs + rv + 4 * t);
         }
       }
-      const char* vp = a.c.v + rv * row_bytes;
+      x.vp = a.c.v + rv * row_bytes;
+      if constexpr (HOLD_V) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) load_words<VE * CS>(x.v[n][j], vp + j * row_bytes + voff[n]);
+          for (int j = 0; j < 8; ++j) load_words<VE * CS>(x.v[n][j], x.vp + j * row_bytes + voff[n]);
+      }
     };
     const auto work = [&](Keys& x, int step, int p0, int p1) {
       f32x4 s[2] = {};
@@ -229,6 +233,7 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
         s[t] *= a.scale_log2;
       }
       const bool whole = step * STEP + STEP <= len && p0 >= 0 && p0 < pages && p1 >= 0 && p1 < pages;
+      unsigned unseen = 0;
       if (!whole) {  // what lies in unseen places counts for nothing, whatever it holds
         const int p = w4 & 2 ? p1 : p0, seen = p >= 0 && p < pages ? len - step * STEP - 8 * w4 : 0;
 #pragma unroll
@@ -236,10 +241,14 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
           const bool in = j < seen;
           s[j / 4][j % 4] = in ? s[j / 4][j % 4] : -INFINITY;
           if constexpr (KV != SSM_KV_IO) x.sv[j / 4][j % 4] = in ? x.sv[j / 4][j % 4] : 0.0f;
+          if constexpr (HOLD_V) {
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int w = 0; w < VW; ++w) x.v[n][j][w] = in ? x.v[n][j][w] : 0u;
+              for (int w = 0; w < VW; ++w) x.v[n][j][w] = in ? x.v[n][j][w] : 0u;
+          } else {
+            unseen |= in ? 0u : 1u << j;
+          }
         }
       }
       float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
@@ -298,37 +307,31 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+          for (int n = 0; n < NB; ++n) {
+            unsigned own[VW];
+            if constexpr (!HOLD_V) {
+              load_words<VE * CS>(own, x.vp + j * row_bytes + voff[n]);
+#pragma unroll
+              for (int w = 0; w < VW; ++w) own[w] = unseen >> j & 1 ? 0u : own[w];
+            }
+            const unsigned* v = HOLD_V ? x.v[HOLD_V ? n : 0][HOLD_V ? j : 0] : own;
 #pragma unroll
             for (int c = 0; c < VE; ++c)
-              o[n * VE + c] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(x.v[n][j], c), s[j / 4][j % 4],
+              o[n * VE + c] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(v, c), s[j / 4][j % 4],
                                                                    o[n * VE + c], 0, 0, 0);
+          }
       }
     };
 
     int step = chunk * share + wave;
     if (step < s_end) {
       int p0 = page_of(step, 0), p1 = page_of(step, 1);
-      if constexpr (AHEAD) {
+      for (; step < s_end; step += NW) {
         Keys x;
         load(x, step, p0, p1);
-        int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
-        for (; step < s_end; step += NW) {
-          Keys y;
-          if (step + NW < s_end) load(y, step + NW, n0, n1);
-          const int f0 = page_of(step + 2 * NW, 0), f1 = page_of(step + 2 * NW, 1);
-          work(x, step, p0, p1);
-          x = y;
-          p0 = n0, p1 = n1, n0 = f0, n1 = f1;
-        }
-      } else {
-        for (; step < s_end; step += NW) {
-          Keys x;
-          load(x, step, p0, p1);
-          const int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
-          work(x, step, p0, p1);
-          p0 = n0, p1 = n1;
-        }
+        const int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
+        work(x, step, p0, p1);
+        p0 = n0, p1 = n1;
       }
     }
 
@@ -395,66 +398,79 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(DecodeArgs a) {
 constexpr int MAX_CHUNKS = 1024;
 constexpr int JOIN = 256;  // threads of a join
 
-// Joins the chunks of one (sequence, head): their weights first, then LP lanes for the row's channels
-// (4 each), JOIN / LP slices of the chunks, the slices added in order.
+// Joins the chunks of one (sequence, head), LP * 4 of its channels: JOIN / LP slices of the chunks, each
+// with a running maximum and sum of its own, then the slices in order.
 template <typename IO, int LP>
 __global__ __launch_bounds__(JOIN) void attn_decode_join(DecodeArgs a) {
-  __shared__ float w[MAX_CHUNKS];
-  __shared__ float part[JOIN / 64][2];
+  constexpr int S = JOIN / LP, AT_ONCE = 4;
+  __shared__ float part[S][2];
   __shared__ f32x4 acc[JOIN];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lp = tid % LP, slice = tid / LP, D = a.c.D;
+  const int tid = threadIdx.x, lp = tid % LP, slice = tid / LP, D = a.c.D;
+  const int e = (blockIdx.y * LP + lp) * 4;
   for (int64_t row = blockIdx.x; row < (int64_t)a.B * a.Hq; row += gridDim.x) {
     const int b = (int)(row / a.Hq), head = (int)(row - (int64_t)b * a.Hq);
     const int steps = (sequence_length(a, b) + STEP - 1) / STEP, share = share_of(a, steps);
     const int n = (steps + share - 1) / share;
     const float* ml = a.ml + row * a.chunks * 2;
-    float m = -INFINITY;
-    for (int c = tid; c < n; c += JOIN) m = fmaxf(m, ml[2 * c]);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    __syncthreads();  // the last row's use of the shared arrays is over
-    if (lane == 0) part[wave][0] = m;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < JOIN / 64; ++x) m = fmaxf(m, part[x][0]);
-    const float mc = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    for (int c = tid; c < n; c += JOIN) {
-      const float f = hw_exp2(ml[2 * c] - mc);
-      w[c] = f;
-      l += f * ml[2 * c + 1];
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-    if (lane == 0) part[wave][1] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int x = 0; x < JOIN / 64; ++x) l += part[x][1];
+    const float* po = a.po + row * a.chunks * D + (e < D ? e : 0);
+    float m = -INFINITY, l = 0.0f;
     f32x4 y = {};
-    if (lp * 4 < D) {
-      const float* po = a.po + row * a.chunks * D + lp * 4;
-#pragma unroll 4
-      for (int c = slice; c < n; c += JOIN / LP) y += *reinterpret_cast<const f32x4*>(po + (int64_t)c * D) * w[c];
+    for (int c0 = slice; c0 < n; c0 += AT_ONCE * S) {
+      float cm[AT_ONCE], cl[AT_ONCE];
+      f32x4 cy[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int c = c0 + i * S, at = c < n ? c : c0;
+        cm[i] = c < n ? ml[2 * at] : -INFINITY;
+        cl[i] = c < n ? ml[2 * at + 1] : 0.0f;
+        cy[i] = *reinterpret_cast<const f32x4*>(po + (int64_t)at * D);
+      }
+      float to = m;
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) to = fmaxf(to, cm[i]);
+      const float by = to == -INFINITY ? 0.0f : to, f = hw_exp2(m - by);
+      y *= f;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const float w = hw_exp2(cm[i] - by);
+        y += cy[i] * w;
+        l += cl[i] * w;
+      }
+      m = to;
     }
+    __syncthreads();  // the last row's use of the shared arrays is over
+    if (lp == 0) part[slice][0] = m, part[slice][1] = l;
     acc[tid] = y;
     __syncthreads();
-    if (slice == 0 && lp * 4 < D) {
+    if (slice == 0) {
 #pragma unroll
-      for (int x = 1; x < JOIN / LP; ++x) y += acc[x * LP + lp];
+      for (int i = 1; i < S; ++i) m = fmaxf(m, part[i][0]);
+      const float by = m == -INFINITY ? 0.0f : m;
+      y = f32x4{};
+      l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const float w = hw_exp2(part[i][0] - by);
+        y += acc[i * LP + lp] * w;
+        l += part[i][1] * w;
+      }
       y *= l > 0.0f ? 1.0f / l : 0.0f;
       char* op = a.out.p + (int64_t)b * a.out.ts + (int64_t)head * a.out.hs;
-      if constexpr (sizeof(IO) == 2)
-        *reinterpret_cast<u32x2*>(op + lp * 8) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-      else
-        *reinterpret_cast<f32x4*>(op + lp * 16) = y;
+      if (e < D) {
+        if constexpr (sizeof(IO) == 2)
+          *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        else
+          *reinterpret_cast<f32x4*>(op + e * 4) = y;
+      }
+      if (a.lse && e == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     }
-    if (a.lse && tid == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
   }
 }
 
-constexpr int64_t TARGET = 8192;                // workgroups: several for each place on the chip, so uneven lengths even out
+// Workgroups: several for each place on the chip, so that uneven lengths even out; more cost more starts than they
+// even out (the same 64 sequences: 134 us with 2048, 137 with 4096, 154 with 8192; 16384 250 with two waves a SIMD).
+constexpr int64_t TARGET = 4096;
 constexpr int64_t MAX_GRID = int64_t(1) << 22;  // keeps a launch within 2^31 work-items
 
 // Most chunks of a sequence, from what the host knows: the table's width, not the lengths.
@@ -462,7 +478,9 @@ int chunks_of(int64_t batch, int q_heads, const ssm_kv_cache* c, int64_t table_w
   const int64_t groups = (q_heads / c->kv_heads + COLS - 1) / COLS;
   const int64_t units = batch * c->kv_heads * groups, longest = table_width * c->page_size;
   int64_t n = (TARGET + units - 1) / units;
-  const int64_t most = (longest + MIN_SHARE * STEP - 1) / (MIN_SHARE * STEP);
+  // Up to twice the least share one chunk does, and no second launch: 5 sequences of up to 300 tokens
+  // 15.5 us a call against 20 with two.
+  const int64_t least = MIN_SHARE * STEP, most = longest <= 2 * least ? 1 : (longest + least - 1) / least;
   if (n > most) n = most;
   if (n > MAX_CHUNKS) n = MAX_CHUNKS;
   return (int)(n < 1 ? 1 : n);
@@ -472,13 +490,18 @@ template <typename IO, int KV, int DP>
 hipError_t launch_dp(const DecodeArgs& a, hipStream_t s) {
   constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1, VE = CS == 4 || DP % 128 ? 4 : 8;
   const int ng = a.G < COLS ? a.G : COLS;
-  const dim3 grid((unsigned)(a.work < MAX_GRID ? a.work : MAX_GRID)), tb(NW * 64);
+  const int heads = a.c.heads * a.groups;
+  const int64_t room = MAX_GRID / ((int64_t)a.chunks * heads);  // sequences of a launch's grid
+  const dim3 grid(a.chunks, heads, (unsigned)(a.B < room ? a.B : room < 1 ? 1 : room)), tb(NW * 64);
   attn_decode<IO, KV, DP><<<grid, tb, NW * ng * 16 * VE * sizeof(float), s>>>(a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.chunks > 1) {
-    const int64_t rows = (int64_t)a.B * a.Hq;
-    const dim3 jgrid((unsigned)(rows < MAX_GRID ? rows : MAX_GRID));
-    attn_decode_join<IO, DP <= 64 ? 16 : DP <= 128 ? 32 : 64><<<jgrid, dim3(JOIN), 0, s>>>(a);
+    // Many chunks: more slices of them, and fewer channels of a workgroup.
+    const int lp = a.chunks >= 64 ? 8 : 32;
+    const int64_t rows = (int64_t)a.B * a.Hq, jroom = MAX_GRID / 8;
+    const dim3 jgrid((unsigned)(rows < jroom ? rows : jroom), (a.c.D + 4 * lp - 1) / (4 * lp));
+    if (lp == 8) attn_decode_join<IO, 8><<<jgrid, dim3(JOIN), 0, s>>>(a);
+    else attn_decode_join<IO, 32><<<jgrid, dim3(JOIN), 0, s>>>(a);
     e = hipGetLastError();
   }
   return e;
@@ -565,7 +588,6 @@ int ssm_attn_decode_step(int64_t batch, int32_t q_heads, int32_t io_dtype, float
   a.G = q_heads / cache->kv_heads;
   a.groups = (a.G + COLS - 1) / COLS;
   a.chunks = chunks_of(batch, q_heads, cache, table_width);
-  a.work = batch * cache->kv_heads * a.groups * a.chunks;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!isfinite(a.scale_log2) || !(a.scale_log2 > 0.0f)) return SSM_ERR_SHAPE;
   a.po = static_cast<float*>(workspace);
