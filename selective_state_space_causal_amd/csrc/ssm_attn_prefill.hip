@@ -78,40 +78,68 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// One key tile in LDS: KT rows of DP elements, in 16-byte chunks whose place in the row is exchanged
-// by the row number so that lanes reading the same chunk of neighbouring rows use different banks.
-template <typename IO, int DP>
-struct Tile;
-
+// A key tile in LDS: rows of CH 16-byte chunks, whose places in the row are exchanged by the row
+// number so that lanes reading one chunk of neighbouring rows use different banks.
 template <int DP>
-struct Tile<bf16_t, DP> {
-  static constexpr int CH = DP / 8;  // chunks of a row
-  __device__ static int k_at(int row, int ch) { return (row * CH + (ch ^ (row & 7))) * 16; }
-  __device__ static int v_at(int row, int ch) { return (row * CH + (ch ^ ((row & 3) << 1))) * 16; }
-};
-template <int DP>
-struct Tile<float, DP> {
-  static constexpr int CH = DP / 4;
-  __device__ static int k_at(int row, int ch) { return (row * CH + (ch ^ (row & 7))) * 16; }
-  __device__ static int v_at(int row, int ch) { return (row * CH + ch) * 16; }
+struct Tile {
+  static constexpr int PITCH = DP == 96 ? 128 : DP;  // elements of a row: the exchange works on 8 chunks
+  static constexpr int CH = PITCH / 8;
+  __device__ static int k_swap(int row) { return row & 7; }
+  __device__ static int v_swap(int row) { return (row & 3) << 1; }
+  __device__ static int k_at(int row, int ch) { return (row * CH + (ch ^ k_swap(row))) * 16; }
+  __device__ static int v_at(int row, int ch) { return (row * CH + (ch ^ v_swap(row))) * 16; }
 };
 
-template <typename IO, int DP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(IO) == 2 ? 2 : 1) void attn_prefill(PrefillArgs a) {
-  constexpr bool BF = sizeof(IO) == 2;
-  constexpr int ES = sizeof(IO), QT = NW * 32, T = Tile<IO, DP>::CH, EPC = 16 / ES, NS = KT / 32, ND = DP / 32;
-  typedef Tile<IO, DP> L;
-  __shared__ __attribute__((aligned(16))) char kt[KT * DP * ES];
-  __shared__ __attribute__((aligned(16))) char vt[KT * DP * ES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+// A thread's NL pieces of a tile: rows row[] at byte ts * row + off[], straight into LDS (a wave's 64 pieces in
+// a row, NW waves in turn); rows past the last one repeat it.  32-bit offsets: a tile's rows are within 2 GiB.
+template <int NL, int NW>
+__device__ __forceinline__ void load_tile(const char* p, int ts, const int* row, const int* off, int last, int wave,
+                                          char* lds) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < NL; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16,
+                                             min(row[i], last) * ts + off[i], 0, 0, 0);
+}
+
+#ifndef NWP
+#define NWP 4
+#endif
+#ifndef LBP
+#define LBP 2
+#endif
+// bf16: a workgroup of NW waves has 32 rows a wave; key tiles of KT keys go straight into one of two LDS buffers
+// while the other is worked on.
+template <int DP, int NW, int KT>
+__global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(PrefillArgs a) {
+  typedef Tile<DP> L;
+  constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH;
+  constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
+  // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
+  __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
+  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // This thread's places of a tile, and the chunks of memory that belong there (the first one past a row's end:
+  // K's meets zeros of Q, V's gives channels that are not stored).
+  int lrow[NL], kch[NL], vch[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int c = (i * NW + wave) * 64 + lane, row = c / CH, pos = c - row * CH;
+    lrow[i] = row;
+    kch[i] = (pos ^ L::k_swap(row)) * 16;
+    vch[i] = (pos ^ L::v_swap(row)) * 16;
+    if (kch[i] >= a.D * 2) kch[i] = 0;
+    if (vch[i] >= a.D * 2) vch[i] = 0;
+  }
 
   for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
     const int h = (int)(idx % a.Hkv);
     int b, tile, tiles, q0, lq;
     if (!find_tile(a, QT, idx / a.Hkv, b, tile, tiles, q0, lq)) break;  // later ones are past the end too
     tile = tiles - 1 - tile;  // causal: the tiles with the most keys first
-    const int k0 = min(max(a.cu_k[b], 0), a.Tk);
-    const int lk = max(min(a.cu_k[b + 1], a.Tk) - k0, 0);
+    const int k0 = __builtin_amdgcn_readfirstlane(min(max(a.cu_k[b], 0), a.Tk));
+    const int lk = __builtin_amdgcn_readfirstlane(max(min(a.cu_k[b + 1], a.Tk) - k0, 0));
     const int rows = lq * a.G, r0 = tile * QT + wave * 32;
     const int r = r0 + col, rc = min(r, rows - 1);
     const int tok = rc / a.G, g = rc - tok * a.G;
@@ -123,34 +151,26 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(IO) == 2 ? 2 : 1) void
     const int block_last = seen_by(min(tile * QT + QT - 1, rows - 1) / a.G);
 
     // Q as the right operand: a lane's row, in the order that the K reads below use.
-    constexpr int NQ = BF ? DP / 16 : DP / 8;
     u32x4 qf[NQ];
     const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int ch = 2 * i + half;
-      qf[i] = ch * EPC < a.D ? *reinterpret_cast<const u32x4*>(qp + ch * 16) : u32x4{0, 0, 0, 0};
+      qf[i] = ch * 8 < a.D ? *reinterpret_cast<const u32x4*>(qp + ch * 16) : u32x4{0, 0, 0, 0};
     }
     f32x16 o[ND] = {};
     float m = -INFINITY, l = 0.0f;
 
     const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
     const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
-    for (int j0 = 0; j0 < block_last; j0 += KT) {
-      __syncthreads();
-      for (int c = threadIdx.x; c < KT * T; c += NW * 64) {
-        const int row = c / T, ch = c - row * T;
-        const int64_t key = min(j0 + row, lk - 1);  // rows past the end repeat the last key: finite, masked below
-        const bool in = ch * EPC < a.D;
-        const u32x4 z = {0, 0, 0, 0};
-        *reinterpret_cast<u32x4*>(kt + L::k_at(row, ch)) =
-            in ? *reinterpret_cast<const u32x4*>(kp + key * a.k.ts + ch * 16) : z;
-        *reinterpret_cast<u32x4*>(vt + L::v_at(row, ch)) =
-            in ? *reinterpret_cast<const u32x4*>(vp + key * a.v.ts + ch * 16) : z;
-      }
-      __syncthreads();
-      if (j0 >= wave_last) continue;
-
+    const int kts = (int)a.k.ts, vts = (int)a.v.ts;
+    // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
+    const auto load = [&](int j0, char* kt, char* vt) {
+      const int last = min(lk - 1 - j0, KT - 1);
+      load_tile<NL, NW>(kp + (int64_t)j0 * a.k.ts, kts, lrow, kch, last, wave, kt);
+      load_tile<NL, NW>(vp + (int64_t)j0 * a.v.ts, vts, lrow, vch, last, wave, vt);
+    };
+    const auto work = [&](int j0, const char* kt, const char* vt) {
       f32x16 s[NS];
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
@@ -158,14 +178,8 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(IO) == 2 ? 2 : 1) void
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + L::k_at(n * 32 + col, 2 * i + half));
-          if constexpr (BF) {
-            s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf),
-                                                           __builtin_bit_cast(bf16x8, qf[i]), s[n], 0, 0, 0);
-          } else {
-            const f32x4 kx = __builtin_bit_cast(f32x4, kf), qx = __builtin_bit_cast(f32x4, qf[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[n] = __builtin_amdgcn_mfma_f32_32x32x2f32(kx[j], qx[j], s[n], 0, 0, 0);
-          }
+          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf), __builtin_bit_cast(bf16x8, qf[i]),
+                                                         s[n], 0, 0, 0);
         }
       }
       if (j0 + KT > wave_first) {  // some row of the wave does not see some key of the tile
@@ -177,64 +191,68 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(IO) == 2 ? 2 : 1) void
             s[n][i] = key < seen ? s[n][i] : -INFINITY;
           }
       }
-      float mx = m;
+      float mx = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[n][i]);
-      mx = half_max(mx);
-      const float mc = mx == -INFINITY ? 0.0f : mx * a.scale_log2;  // a row that has seen nothing yet: all weights 0
-      const float alpha = hw_exp2(fmaf(m, a.scale_log2, -mc));
-      m = mx;
-      float sum = 0.0f;
+      mx = half_max(mx) * a.scale_log2;
+      // The subtracted maximum follows the true one only when it has grown by 2^SLACK: weights stay below 2^SLACK,
+      // and the output is rescaled a few times in a sequence instead of at every tile.
+      constexpr float SLACK = 8.0f;
+      if (__any(mx > m + SLACK)) {
+        const float to = mx > m ? mx : m;
+        const float alpha = hw_exp2(m - (to == -INFINITY ? 0.0f : to));
+        m = to;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+      }
+      const float mc = m == -INFINITY ? 0.0f : m;  // a row that has seen nothing yet: all weights 0
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           s[n][i] = hw_exp2(fmaf(s[n][i], a.scale_log2, -mc));
-          sum += s[n][i];
+          l += s[n][i];  // this half's keys only; joined at the end
         }
-      l = l * alpha + sum;  // this half's keys only; joined at the end
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+        for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
+          u32x4 pf;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[n][8 * t + 2 * i], s[n][8 * t + 2 * i + 1]);
+          // The transposing read: 16 lanes give 4 rows of 16 channels and get 4 rows of one channel each.
+          const int row = n * 32 + 16 * t + 4 * half + (lane & 15) / 4;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const int e = d * 32 + (col & 16) + (lane & 3) * 4;
+            union {
+              s16x4 x[2];
+              bf16x8 v;
+            } vf;
+            vf.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row, e / 8) + (e & 4) * 2));
+            vf.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row + 8, e / 8) + (e & 4) * 2));
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.v, __builtin_bit_cast(bf16x8, pf), o[d], 0, 0, 0);
+          }
+        }
+    };
 
-      if constexpr (BF) {
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
-            u32x4 pf;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[n][8 * t + 2 * i], s[n][8 * t + 2 * i + 1]);
-            // The transposing read: 16 lanes give 4 rows of 16 channels and get 4 rows of one channel each.
-            const int row = n * 32 + 16 * t + 4 * half + (lane & 15) / 4;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              const int e = d * 32 + (col & 16) + (lane & 3) * 4;
-              union {
-                s16x4 x[2];
-                bf16x8 v;
-              } vf;
-              vf.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row, e / 8) + (e & 4) * 2));
-              vf.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row + 8, e / 8) + (e & 4) * 2));
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.v, __builtin_bit_cast(bf16x8, pf), o[d], 0, 0, 0);
-            }
-          }
-      } else {
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int row = n * 32 + 8 * (i / 4) + 4 * half + i % 4;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              const int e = d * 32 + col;
-              const float vx = *reinterpret_cast<const float*>(vt + L::v_at(row, e / 4) + (e & 3) * 4);
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vx, s[n][i], o[d], 0, 0, 0);
-            }
-          }
+    if (block_last > 0) {
+      __syncthreads();  // the last tile's reads of the buffers are over
+      load(0, kt0, vt0);
+      __syncthreads();
+      for (int j0 = 0; j0 < block_last; j0 += 2 * KT) {
+        if (j0 + KT < block_last) load(j0 + KT, kt1, vt1);
+        if (j0 < wave_last) work(j0, kt0, vt0);
+        __syncthreads();
+        if (j0 + KT >= block_last) break;
+        if (j0 + 2 * KT < block_last) load(j0 + 2 * KT, kt0, vt0);
+        if (j0 + KT < wave_last) work(j0 + KT, kt1, vt1);
+        __syncthreads();
       }
     }
 
@@ -249,37 +267,174 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 && sizeof(IO) == 2 ? 2 : 1) void
         for (int i = 0; i < 4; ++i) {
           const int e = d * 32 + 8 * i + 4 * half;
           if (e >= a.D) continue;
-          const float x0 = o[d][4 * i] * inv, x1 = o[d][4 * i + 1] * inv, x2 = o[d][4 * i + 2] * inv,
-                      x3 = o[d][4 * i + 3] * inv;
-          if constexpr (BF)
-            *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(x0, x1), pack_bf16(x2, x3)};
-          else
-            *reinterpret_cast<f32x4*>(op + e * 4) = f32x4{x0, x1, x2, x3};
+          *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                                                       pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
         }
       if (a.lse && half == 0)
-        a.lse[(int64_t)(q0 + tok) * a.Hq + head] =
-            l > 0.0f ? (m * a.scale_log2 + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        a.lse[(int64_t)(q0 + tok) * a.Hq + head] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+constexpr int F32_NW = 4;
+
+// fp32, on the fp32 matrix instructions (a sixteenth of bf16's rate, which bounds it): a wave reads its
+// operands straight from memory, no LDS.  A workgroup has 32 rows; its waves take 32 keys in turn, so
+// that few rows still fill the chip, and join their results at the end.  K's channels may come in any
+// order if Q's do too: 16-byte reads of both.  Lane m of V's operand holds channels 4 m .. 4 m + 3 of
+// one key, for four output tiles; a lane ends with 16 neighbouring channels of one row.
+template <int DP>
+__global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
+  constexpr int NW = F32_NW, QT = 32, NQ = DP / 8;
+  constexpr int VE = DP % 128 == 0 ? 4 : DP % 64 == 0 ? 2 : 1, NB = DP / (32 * VE);  // channels of a lane, blocks of 32 VE
+  __shared__ float wml[NW][32][2];
+  __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
+  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
+    const int h = (int)(idx % a.Hkv);
+    int b, tile, tiles, q0, lq;
+    if (!find_tile(a, QT, idx / a.Hkv, b, tile, tiles, q0, lq)) break;
+    tile = tiles - 1 - tile;
+    const int k0 = __builtin_amdgcn_readfirstlane(min(max(a.cu_k[b], 0), a.Tk));
+    const int lk = __builtin_amdgcn_readfirstlane(max(min(a.cu_k[b + 1], a.Tk) - k0, 0));
+    const int rows = lq * a.G, r0 = tile * QT;
+    const int r = r0 + col, rc = min(r, rows - 1);
+    const int tok = rc / a.G, g = rc - tok * a.G;
+    const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
+    const int seen = seen_by(tok);
+    const int first = __builtin_amdgcn_readfirstlane(seen_by(r0 / a.G));
+    const int last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
+
+    f32x4 qf[NQ];
+    int ko[NQ];  // bytes into a row: its first ones, against zeros, past its end
+    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int e = (2 * i + half) * 4;
+      qf[i] = e < a.D ? *reinterpret_cast<const f32x4*>(qp + e * 4) : f32x4{};
+      ko[i] = e < a.D ? e * 4 : 0;
+    }
+    int vo[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) vo[n] = (n * 32 + col) * VE < a.D ? (n * 32 + col) * VE * 4 : 0;
+    f32x16 o[NB * VE] = {};
+    float m = -INFINITY, l = 0.0f;
+    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
+    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
+
+    for (int j0 = wave * 32; j0 < last; j0 += NW * 32) {
+      // keys past the end repeat the last one (finite, masked below)
+      const char* kr = kp + (int64_t)min(j0 + col, lk - 1) * a.k.ts;
+      f32x16 s = {};
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const f32x4 kx = *reinterpret_cast<const f32x4*>(kr + ko[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_32x32x2f32(kx[j], qf[i][j], s, 0, 0, 0);
+      }
+      if (j0 + 32 > first) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = j0 + 8 * (i / 4) + 4 * half + i % 4 < seen ? s[i] : -INFINITY;
+      }
+      float mx = m;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i] * a.scale_log2);
+      mx = half_max(mx);
+      const float mc = mx == -INFINITY ? 0.0f : mx, alpha = hw_exp2(m - mc);
+      m = mx;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = hw_exp2(fmaf(s[i], a.scale_log2, -mc));
+        l += s[i];
+      }
+#pragma unroll
+      for (int c = 0; c < NB * VE; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const char* vr = vp + (int64_t)min(j0 + 8 * (i / 4) + 4 * half + i % 4, lk - 1) * a.v.ts;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          typedef float vec __attribute__((ext_vector_type(VE)));
+          const vec x = *reinterpret_cast<const vec*>(vr + vo[n]);
+#pragma unroll
+          for (int c = 0; c < VE; ++c)
+            o[n * VE + c] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[c], s[i], o[n * VE + c], 0, 0, 0);
+        }
+      }
+    }
+
+    // Join the waves, as the decode kernel does: one maximum, then sums in wave order.
+    l = half_sum(l);
+    __syncthreads();
+    if (half == 0) wml[wave][col][0] = m;
+    __syncthreads();
+    float top = wml[0][col][0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) top = fmaxf(top, wml[w][col][0]);
+    const float f = hw_exp2(m - (top == -INFINITY ? 0.0f : top));
+    if (half == 0) wml[wave][col][1] = l * f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      constexpr int BC = 32 * VE;
+      if (n > 0) __syncthreads();
+      // rows of the product: channel lane m of V = 8 (i / 4) + 4 half + i % 4
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int c = 0; c < VE; ++c) wo[wave][col][(8 * (i / 4) + 4 * half + i % 4) * VE + c] = o[n * VE + c][i] * f;
+      __syncthreads();
+      for (int i = threadIdx.x; i < 32 * (BC / 4); i += NW * 64) {
+        const int row = i / (BC / 4), e = (i - row * (BC / 4)) * 4, rr = r0 + row;
+        if (n * BC + e >= a.D || rr >= rows) continue;
+        f32x4 y = {};
+        float sum = 0.0f, hm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          y += *reinterpret_cast<const f32x4*>(&wo[w][row][e]);
+          sum += wml[w][row][1];
+          hm = fmaxf(hm, wml[w][row][0]);
+        }
+        const int t = rr / a.G, head = h * a.G + rr - t * a.G;
+        *reinterpret_cast<f32x4*>(a.out.p + (int64_t)(q0 + t) * a.out.ts + (int64_t)head * a.out.hs + (n * BC + e) * 4) =
+            y * (sum > 0.0f ? 1.0f / sum : 0.0f);
+        if (a.lse && n == 0 && e == 0)
+          a.lse[(int64_t)(q0 + t) * a.Hq + head] = sum > 0.0f ? (hm + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+      }
     }
   }
 }
 
 constexpr int64_t MAX_GRID = int64_t(1) << 22;  // keeps a launch within 2^31 work-items
 
-template <typename IO, int DP, int NW, int KT>
-hipError_t launch(PrefillArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)a.Tq * a.G / (NW * 32) + a.B;  // sum of ceil(rows / QT) over the sequences
-  a.work = tiles * a.Hkv;
-  const dim3 grid((unsigned)(a.work < MAX_GRID ? a.work : MAX_GRID)), tb(NW * 64);
-  attn_prefill<IO, DP, NW, KT><<<grid, tb, 0, s>>>(a);
-  return hipGetLastError();
+// Tiles of all key heads, at most (the sum of ceil(rows / QT) over the sequences), as a grid.
+dim3 tiles_grid(PrefillArgs& a, int QT) {
+  a.work = ((int64_t)a.Tq * a.G / QT + a.B) * a.Hkv;
+  return dim3((unsigned)(a.work < MAX_GRID ? a.work : MAX_GRID));
 }
 
-template <typename IO, int KT>
-hipError_t launch_dim(PrefillArgs& a, hipStream_t s) {
-  if (a.D <= 64) return launch<IO, 64, 4, KT>(a, s);
-  if (a.D <= 128) return launch<IO, 128, 4, KT>(a, s);
-  if (a.D <= 192) return launch<IO, 192, 4, KT>(a, s);
-  return launch<IO, 256, 4, KT>(a, s);
+template <int DP>
+void launch_bf16(PrefillArgs& a, hipStream_t s) {
+  constexpr int NW = NWP, KT = 64;
+  attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32), dim3(NW * 64), 0, s>>>(a);
+}
+
+template <int DP>
+void launch_f32(PrefillArgs& a, hipStream_t s) {
+  attn_prefill_f32<DP><<<tiles_grid(a, 32), dim3(F32_NW * 64), 0, s>>>(a);
+}
+
+hipError_t launch(PrefillArgs& a, bool bf16, hipStream_t s) {
+  if (a.D <= 64) bf16 ? launch_bf16<64>(a, s) : launch_f32<64>(a, s);
+  else if (a.D <= 96) bf16 ? launch_bf16<96>(a, s) : launch_f32<96>(a, s);
+  else if (a.D <= 128) bf16 ? launch_bf16<128>(a, s) : launch_f32<128>(a, s);
+  else if (a.D <= 192) bf16 ? launch_bf16<192>(a, s) : launch_f32<192>(a, s);
+  else bf16 ? launch_bf16<256>(a, s) : launch_f32<256>(a, s);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -342,6 +497,6 @@ extern "C" int ssm_attn_prefill(const ssm_attn_dims* d, const ssm_view* q, const
   a.scale_log2 = d->scale * 1.4426950408889634f;
   if (!isfinite(a.scale_log2) || !(a.scale_log2 > 0.0f)) return SSM_ERR_SHAPE;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = d->io_dtype == SSM_BF16 ? launch_dim<ssm::bf16_t, 64>(a, s) : launch_dim<float, 32>(a, s);
+  const hipError_t e = launch(a, d->io_dtype == SSM_BF16, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
