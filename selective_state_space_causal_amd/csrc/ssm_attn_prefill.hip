@@ -82,10 +82,13 @@ __device__ __forceinline__ float half_sum(float x) {
 // number so that lanes reading one chunk of neighbouring rows use different banks.
 template <int DP>
 struct Tile {
-  static constexpr int PITCH = DP == 96 ? 128 : DP;  // elements of a row: the exchange works on 8 chunks
+  static constexpr int PITCH = DP == 96 ? 128 : DP;  // elements of a row: the exchange works on 8 or 16 chunks
   static constexpr int CH = PITCH / 8;
-  __device__ static int k_swap(int row) { return row & 7; }
-  __device__ static int v_swap(int row) { return (row & 3) << 1; }
+  // Sixteen chunks fill the banks once.  Rows of 16 n chunks: any 16 rows' chunks in 16 places.  Rows of 16 n + 8
+  // start in the two halves of the banks in turn: 8 places for each half.
+  __device__ static int k_swap(int row) { return CH % 16 == 0 ? row & 15 : (row >> 1) & 7; }
+  // 32 lanes read 4 chunks of 4 rows each.
+  __device__ static int v_swap(int row) { return CH % 16 == 0 ? (row & 3) << 2 : (row & 2) << 1; }
   __device__ static int k_at(int row, int ch) { return (row * CH + (ch ^ k_swap(row))) * 16; }
   __device__ static int v_at(int row, int ch) { return (row * CH + (ch ^ v_swap(row))) * 16; }
 };
@@ -172,6 +175,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
     };
     const auto work = [&](int j0, const char* kt, const char* vt) {
       f32x16 s[NS];
+#ifdef PRIO
+      __builtin_amdgcn_s_setprio(1);
+#endif
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         s[n] = f32x16{};
@@ -200,6 +206,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
       // The subtracted maximum follows the true one only when it has grown by 2^SLACK: weights stay below 2^SLACK,
       // and the output is rescaled a few times in a sequence instead of at every tile.
       constexpr float SLACK = 8.0f;
+#ifdef PRIO
+      __builtin_amdgcn_s_setprio(0);
+#endif
       if (__any(mx > m + SLACK)) {
         const float to = mx > m ? mx : m;
         const float alpha = hw_exp2(m - (to == -INFINITY ? 0.0f : to));
