@@ -32,35 +32,47 @@ struct PrefillArgs {
   int64_t work;      // upper bound of tiles of all key heads
 };
 
+// Inclusive prefix sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // the 16 lanes of a row: 1, 2, 4, 8 to the right
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row 0's sum into row 1, row 2's into 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // the lower half's into the upper half
+  return x;
+}
+
+struct Work {
+  int tile, tiles;     // of the sequence's rows
+  int q0, lq, k0, lk;  // its queries and keys
+};
+
 // The sequence and tile that hold tile `idx` of the packed batch (false past the end).  Each wave finds
 // it by itself: 64 sequences at a time, a prefix sum of their tile counts over the lanes.
-__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int QT, int64_t idx, int& b, int& tile, int& tiles,
-                                          int& q0, int& lq) {
+__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int QT, int64_t idx, Work& w) {
   const int lane = threadIdx.x & 63;
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     const int bb = b0 + lane;
-    int start = 0, len = 0;
+    int q0 = 0, lq = 0, k0 = 0, lk = 0;
     if (bb < a.B) {
-      start = min(max(a.cu_q[bb], 0), a.Tq);
-      len = max(min(a.cu_q[bb + 1], a.Tq) - start, 0);
+      q0 = min(max(a.cu_q[bb], 0), a.Tq);
+      lq = max(min(a.cu_q[bb + 1], a.Tq) - q0, 0);
+      k0 = min(max(a.cu_k[bb], 0), a.Tk);
+      lk = max(min(a.cu_k[bb + 1], a.Tk) - k0, 0);
     }
-    const int n = (int)(((int64_t)len * a.G + QT - 1) / QT);
-    int incl = n;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int up = __shfl_up(incl, m);
-      if (lane >= m) incl += up;
-    }
-    const int total = __shfl(incl, 63);
+    const int n = (int)(((int64_t)lq * a.G + QT - 1) / QT), incl = wave_scan(n);
+    const int total = __builtin_amdgcn_readlane(incl, 63);
     if (idx < base + total) {
       const int want = (int)(idx - base);
-      const int first = __ffsll((unsigned long long)__ballot(incl > want)) - 1;
-      b = __builtin_amdgcn_readfirstlane(b0 + first);
-      tiles = __builtin_amdgcn_readfirstlane(__shfl(n, first));
-      tile = __builtin_amdgcn_readfirstlane(want - (__shfl(incl, first) - tiles));
-      q0 = __builtin_amdgcn_readfirstlane(__shfl(start, first));
-      lq = __builtin_amdgcn_readfirstlane(__shfl(len, first));
+      const int at = __ffsll((unsigned long long)__ballot(incl > want)) - 1;
+      w.tiles = __builtin_amdgcn_readlane(n, at);
+      w.tile = want - (__builtin_amdgcn_readlane(incl, at) - w.tiles);
+      w.q0 = __builtin_amdgcn_readlane(q0, at);
+      w.lq = __builtin_amdgcn_readlane(lq, at);
+      w.k0 = __builtin_amdgcn_readlane(k0, at);
+      w.lk = __builtin_amdgcn_readlane(lk, at);
       return true;
     }
     base += total;
@@ -93,16 +105,24 @@ struct Tile {
   __device__ static int v_at(int row, int ch) { return (row * CH + (ch ^ v_swap(row))) * 16; }
 };
 
-// A thread's NL pieces of a tile: rows row[] at byte ts * row + off[], straight into LDS (a wave's 64 pieces in
-// a row, NW waves in turn); rows past the last one repeat it.  32-bit offsets: a tile's rows are within 2 GiB.
-template <int NL, int NW>
-__device__ __forceinline__ void load_tile(const char* p, int ts, const int* row, const int* off, int last, int wave,
-                                          char* lds) {
+// A thread's NL pieces of a tile, at byte off[] of its rows, straight into LDS: a wave's 64 pieces in a row, NW
+// waves in turn.  Rows past the last one repeat it (CH pieces to a row, ts bytes between rows).  32-bit
+// offsets: a tile's rows are within 2 GiB.
+template <int NL, int NW, int CH, int KT>
+__device__ __forceinline__ void load_tile(const char* p, int ts, const int* off, int last, int wave, char* lds) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
+  if (last >= KT - 1) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16,
-                                             min(row[i], last) * ts + off[i], 0, 0, 0);
+    for (int i = 0; i < NL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16, off[i], 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int row = ((i * NW + wave) * 64 + (int)(threadIdx.x & 63)) / CH;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16,
+                                               off[i] - max(row - last, 0) * ts, 0, 0, 0);
+    }
+  }
 }
 
 #ifndef NWP
@@ -123,26 +143,24 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // This thread's places of a tile, and the chunks of memory that belong there (the first one past a row's end:
+  // This thread's pieces of a tile: the chunk of memory that belongs at each place (the first one past a row's end:
   // K's meets zeros of Q, V's gives channels that are not stored).
-  int lrow[NL], kch[NL], vch[NL];
+  const int kts = (int)a.k.ts, vts = (int)a.v.ts;
+  int koff[NL], voff[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int c = (i * NW + wave) * 64 + lane, row = c / CH, pos = c - row * CH;
-    lrow[i] = row;
-    kch[i] = (pos ^ L::k_swap(row)) * 16;
-    vch[i] = (pos ^ L::v_swap(row)) * 16;
-    if (kch[i] >= a.D * 2) kch[i] = 0;
-    if (vch[i] >= a.D * 2) vch[i] = 0;
+    const int kc = pos ^ L::k_swap(row), vc = pos ^ L::v_swap(row);
+    koff[i] = row * kts + (kc * 8 < a.D ? kc : 0) * 16;
+    voff[i] = row * vts + (vc * 8 < a.D ? vc : 0) * 16;
   }
 
   for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
     const int h = (int)(idx % a.Hkv);
-    int b, tile, tiles, q0, lq;
-    if (!find_tile(a, QT, idx / a.Hkv, b, tile, tiles, q0, lq)) break;  // later ones are past the end too
-    tile = tiles - 1 - tile;  // causal: the tiles with the most keys first
-    const int k0 = __builtin_amdgcn_readfirstlane(min(max(a.cu_k[b], 0), a.Tk));
-    const int lk = __builtin_amdgcn_readfirstlane(max(min(a.cu_k[b + 1], a.Tk) - k0, 0));
+    Work w;
+    if (!find_tile(a, QT, idx / a.Hkv, w)) break;  // later ones are past the end too
+    const int tile = w.tiles - 1 - w.tile;  // causal: the tiles with the most keys first
+    const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
     const int rows = lq * a.G, r0 = tile * QT + wave * 32;
     const int r = r0 + col, rc = min(r, rows - 1);
     const int tok = rc / a.G, g = rc - tok * a.G;
@@ -150,8 +168,19 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
     const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
     const int seen = seen_by(tok);
     const int wave_first = __builtin_amdgcn_readfirstlane(seen_by(min(r0, rows - 1) / a.G));
-    const int wave_last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
+    const int wave_last = r0 >= rows ? 0 : __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
     const int block_last = seen_by(min(tile * QT + QT - 1, rows - 1) / a.G);
+
+    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
+    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
+    // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
+    const auto load = [&](int j0, char* kt, char* vt) {
+      const int last = min(lk - 1 - j0, KT - 1);
+      load_tile<NL, NW, CH, KT>(kp + (int64_t)j0 * a.k.ts, kts, koff, last, wave, kt);
+      load_tile<NL, NW, CH, KT>(vp + (int64_t)j0 * a.v.ts, vts, voff, last, wave, vt);
+    };
+    __syncthreads();  // the last tile's reads of the buffers are over
+    if (block_last > 0) load(0, kt0, vt0);
 
     // Q as the right operand: a lane's row, in the order that the K reads below use.
     u32x4 qf[NQ];
@@ -164,15 +193,6 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
     f32x16 o[ND] = {};
     float m = -INFINITY, l = 0.0f;
 
-    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
-    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
-    const int kts = (int)a.k.ts, vts = (int)a.v.ts;
-    // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
-    const auto load = [&](int j0, char* kt, char* vt) {
-      const int last = min(lk - 1 - j0, KT - 1);
-      load_tile<NL, NW>(kp + (int64_t)j0 * a.k.ts, kts, lrow, kch, last, wave, kt);
-      load_tile<NL, NW>(vp + (int64_t)j0 * a.v.ts, vts, lrow, vch, last, wave, vt);
-    };
     const auto work = [&](int j0, const char* kt, const char* vt) {
       f32x16 s[NS];
 #ifdef PRIO
@@ -251,8 +271,6 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
     };
 
     if (block_last > 0) {
-      __syncthreads();  // the last tile's reads of the buffers are over
-      load(0, kt0, vt0);
       __syncthreads();
       for (int j0 = 0; j0 < block_last; j0 += 2 * KT) {
         if (j0 + KT < block_last) load(j0 + KT, kt1, vt1);
@@ -303,11 +321,10 @@ __global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
 
   for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
     const int h = (int)(idx % a.Hkv);
-    int b, tile, tiles, q0, lq;
-    if (!find_tile(a, QT, idx / a.Hkv, b, tile, tiles, q0, lq)) break;
-    tile = tiles - 1 - tile;
-    const int k0 = __builtin_amdgcn_readfirstlane(min(max(a.cu_k[b], 0), a.Tk));
-    const int lk = __builtin_amdgcn_readfirstlane(max(min(a.cu_k[b + 1], a.Tk) - k0, 0));
+    Work w;
+    if (!find_tile(a, QT, idx / a.Hkv, w)) break;
+    const int tile = w.tiles - 1 - w.tile;
+    const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
     const int rows = lq * a.G, r0 = tile * QT;
     const int r = r0 + col, rc = min(r, rows - 1);
     const int tok = rc / a.G, g = rc - tok * a.G;
