@@ -29,7 +29,6 @@ struct PrefillArgs {
   int B, Tq, Tk, Hq, Hkv, G, D;
   int causal;
   float scale_log2;  // scale * log2(e)
-  int64_t work;      // upper bound of tiles of all key heads
 };
 
 // Inclusive prefix sum over the wave's lanes.
@@ -125,16 +124,10 @@ __device__ __forceinline__ void load_tile(const char* p, int ts, const int* off,
   }
 }
 
-#ifndef NWP
-#define NWP 4
-#endif
-#ifndef LBP
-#define LBP 2
-#endif
 // bf16: a workgroup of NW waves has 32 rows a wave; key tiles of KT keys go straight into one of two LDS buffers
 // while the other is worked on.
 template <int DP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(PrefillArgs a) {
+__global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(PrefillArgs a) {
   typedef Tile<DP> L;
   constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH;
   constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
@@ -155,10 +148,9 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
     voff[i] = row * vts + (vc * 8 < a.D ? vc : 0) * 16;
   }
 
-  for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
-    const int h = (int)(idx % a.Hkv);
-    Work w;
-    if (!find_tile(a, QT, idx / a.Hkv, w)) break;  // later ones are past the end too
+  const int h = blockIdx.x;
+  Work w;
+  for (int64_t idx = blockIdx.y; find_tile(a, QT, idx, w); idx += gridDim.y) {
     const int tile = w.tiles - 1 - w.tile;  // causal: the tiles with the most keys first
     const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
     const int rows = lq * a.G, r0 = tile * QT + wave * 32;
@@ -195,9 +187,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
 
     const auto work = [&](int j0, const char* kt, const char* vt) {
       f32x16 s[NS];
-#ifdef PRIO
-      __builtin_amdgcn_s_setprio(1);
-#endif
+      __builtin_amdgcn_s_setprio(1);  // the matrix instructions first: the other wave of a SIMD has the vector unit
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         s[n] = f32x16{};
@@ -226,9 +216,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? LBP : 1) void attn_prefill(Pre
       // The subtracted maximum follows the true one only when it has grown by 2^SLACK: weights stay below 2^SLACK,
       // and the output is rescaled a few times in a sequence instead of at every tile.
       constexpr float SLACK = 8.0f;
-#ifdef PRIO
       __builtin_amdgcn_s_setprio(0);
-#endif
       if (__any(mx > m + SLACK)) {
         const float to = mx > m ? mx : m;
         const float alpha = hw_exp2(m - (to == -INFINITY ? 0.0f : to));
@@ -308,21 +296,61 @@ constexpr int F32_NW = 4;
 // fp32, on the fp32 matrix instructions (a sixteenth of bf16's rate, which bounds it): a wave reads its
 // operands straight from memory, no LDS.  A workgroup has 32 rows; its waves take 32 keys in turn, so
 // that few rows still fill the chip, and join their results at the end.  K's channels may come in any
-// order if Q's do too: 16-byte reads of both.  Lane m of V's operand holds channels 4 m .. 4 m + 3 of
-// one key, for four output tiles; a lane ends with 16 neighbouring channels of one row.
+// order if Q's do too: 16-byte reads of both.  Lane m of V's operand holds VE neighbouring channels of
+// one key, for VE output tiles.  A step's V is loaded while its scores are computed, the next step's K while
+// its output is.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const char* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, bytes, 0x00020000);
+}
+
+// Pieces 32 i + 16 half of a lane's row (at: its first byte); the first one again past D.
+template <int NQ>
+__device__ __forceinline__ void load_k32(f32x4* k, const char* p, int bytes, int at, int D) {
+  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+    k[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, i * 8 < D ? i * 32 : 0, 0));
+}
+
+template <int NB, int VE>
+__device__ __forceinline__ void load_v32(float (*v)[NB * VE], const char* p, int bytes, const int* at, int ts) {
+  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int row = (8 * (i / 4) + i % 4) * ts;
+      float* x = v[i] + n * VE;
+      if constexpr (VE == 4) {
+        const f32x4 t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at[n], row, 0));
+        x[0] = t[0], x[1] = t[1], x[2] = t[2], x[3] = t[3];
+      } else if constexpr (VE == 2) {
+        const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at[n], row, 0));
+        x[0] = __uint_as_float(t[0]), x[1] = __uint_as_float(t[1]);
+      } else {
+        x[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at[n], row, 0));
+      }
+    }
+}
+
 template <int DP>
-__global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
+__global__ __launch_bounds__(F32_NW * 64, 1) void attn_prefill_f32(PrefillArgs a) {
   constexpr int NW = F32_NW, QT = 32, NQ = DP / 8;
   constexpr int VE = DP % 128 == 0 ? 4 : DP % 64 == 0 ? 2 : 1, NB = DP / (32 * VE);  // channels of a lane, blocks of 32 VE
+  constexpr bool QREG = DP <= 128;  // Q in registers beside a step's K, V and output, else in LDS
   __shared__ float wml[NW][32][2];
   __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
+  __shared__ __attribute__((aligned(16))) f32x4 ql[QREG ? 1 : NQ][64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kts = (int)a.k.ts, vts = (int)a.v.ts;
+  int vo[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) vo[n] = 4 * half * vts + ((n * 32 + col) * VE < a.D ? (n * 32 + col) * VE * 4 : 0);
 
-  for (int64_t idx = blockIdx.x; idx < a.work; idx += gridDim.x) {
-    const int h = (int)(idx % a.Hkv);
-    Work w;
-    if (!find_tile(a, QT, idx / a.Hkv, w)) break;
+  const int h = blockIdx.x;
+  Work w;
+  for (int64_t idx = blockIdx.y; find_tile(a, QT, idx, w); idx += gridDim.y) {
     const int tile = w.tiles - 1 - w.tile;
     const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
     const int rows = lq * a.G, r0 = tile * QT;
@@ -333,33 +361,42 @@ __global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
     const int first = __builtin_amdgcn_readfirstlane(seen_by(r0 / a.G));
     const int last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
 
-    f32x4 qf[NQ];
-    int ko[NQ];  // bytes into a row: its first ones, against zeros, past its end
-    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int e = (2 * i + half) * 4;
-      qf[i] = e < a.D ? *reinterpret_cast<const f32x4*>(qp + e * 4) : f32x4{};
-      ko[i] = e < a.D ? e * 4 : 0;
-    }
-    int vo[NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) vo[n] = (n * 32 + col) * VE < a.D ? (n * 32 + col) * VE * 4 : 0;
-    f32x16 o[NB * VE] = {};
-    float m = -INFINITY, l = 0.0f;
     const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
     const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
+    // Bytes of a step's rows: past them, keys read as zeros (masked below).
+    const auto span = [&](int j0, int ts) { return (min(lk - j0, 32) - 1) * ts + a.D * 4; };
+    f32x4 kx[NQ];
+    int j0 = wave * 32;
+    if (j0 < last) load_k32<NQ>(kx, kp + (int64_t)j0 * a.k.ts, span(j0, kts), col * kts + half * 16, a.D);
+    f32x4 qf[QREG ? NQ : 1];
+    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
+    if constexpr (!QREG) __syncthreads();
+#pragma unroll
+    for (int i = QREG ? 0 : wave; i < NQ; i += QREG ? 1 : NW) {
+      const int e = (2 * i + half) * 4;
+      const f32x4 x = e < a.D ? *reinterpret_cast<const f32x4*>(qp + e * 4) : f32x4{};
+      if constexpr (QREG) qf[i] = x;
+      else ql[i][lane] = x;
+    }
+    if constexpr (!QREG) __syncthreads();
+    f32x16 o[NB * VE] = {};
+    float m = -INFINITY, l = 0.0f;
 
-    for (int j0 = wave * 32; j0 < last; j0 += NW * 32) {
-      // keys past the end repeat the last one (finite, masked below)
-      const char* kr = kp + (int64_t)min(j0 + col, lk - 1) * a.k.ts;
+    for (; j0 < last; j0 += NW * 32) {
+      float vx[16][NB * VE];
+      load_v32<NB, VE>(vx, vp + (int64_t)j0 * a.v.ts, span(j0, vts), vo, vts);
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 s = {};
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const f32x4 kx = *reinterpret_cast<const f32x4*>(kr + ko[i]);
+        const f32x4 qx = QREG ? qf[QREG ? i : 0] : ql[QREG ? 0 : i][lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_32x32x2f32(kx[j], qf[i][j], s, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_32x32x2f32(kx[i][j], qx[j], s, 0, 0, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      const int jn = j0 + NW * 32;
+      if (jn < last) load_k32<NQ>(kx, kp + (int64_t)jn * a.k.ts, span(jn, kts), col * kts + half * 16, a.D);
+      __builtin_amdgcn_sched_barrier(0);
       if (j0 + 32 > first) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = j0 + 8 * (i / 4) + 4 * half + i % 4 < seen ? s[i] : -INFINITY;
@@ -381,17 +418,9 @@ __global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const char* vr = vp + (int64_t)min(j0 + 8 * (i / 4) + 4 * half + i % 4, lk - 1) * a.v.ts;
+      for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          typedef float vec __attribute__((ext_vector_type(VE)));
-          const vec x = *reinterpret_cast<const vec*>(vr + vo[n]);
-#pragma unroll
-          for (int c = 0; c < VE; ++c)
-            o[n * VE + c] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[c], s[i], o[n * VE + c], 0, 0, 0);
-        }
-      }
+        for (int c = 0; c < NB * VE; ++c) o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(vx[i][c], s[i], o[c], 0, 0, 0);
     }
 
     // Join the waves, as the decode kernel does: one maximum, then sums in wave order.
@@ -435,17 +464,16 @@ __global__ __launch_bounds__(F32_NW * 64) void attn_prefill_f32(PrefillArgs a) {
   }
 }
 
-constexpr int64_t MAX_GRID = int64_t(1) << 22;  // keeps a launch within 2^31 work-items
-
-// Tiles of all key heads, at most (the sum of ceil(rows / QT) over the sequences), as a grid.
-dim3 tiles_grid(PrefillArgs& a, int QT) {
-  a.work = ((int64_t)a.Tq * a.G / QT + a.B) * a.Hkv;
-  return dim3((unsigned)(a.work < MAX_GRID ? a.work : MAX_GRID));
+// Key heads and tiles (at most: the sum of ceil(rows / QT) over the sequences), heads first: the eight XCDs take
+// workgroups in turn, so that with eight heads each XCD's L2 holds the keys of one.
+dim3 tiles_grid(const PrefillArgs& a, int QT) {
+  const int64_t tiles = (int64_t)a.Tq * a.G / QT + a.B, most = 65535;
+  return dim3(a.Hkv, (unsigned)(tiles < most ? tiles : most));  // 65535 * 1024 heads * 256 threads: below 2^35
 }
 
 template <int DP>
 void launch_bf16(PrefillArgs& a, hipStream_t s) {
-  constexpr int NW = NWP, KT = 64;
+  constexpr int NW = 4, KT = DP > 128 ? 32 : 64;  // two buffers of K and V: 64 KB, two workgroups on a CU up to 128
   attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32), dim3(NW * 64), 0, s>>>(a);
 }
 
