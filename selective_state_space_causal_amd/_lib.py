@@ -160,8 +160,11 @@ def _check_params(params: dict, D: int, N: int, device):
 def stream_handle(stream=None, device=None) -> int:
     """The HIP stream to enqueue on: `stream`, else the current stream of `device` (the
     tensors' device), so kernels run where the tensors live."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream  # ctypes passes the integer as a void*
+    if stream is not None:
+        return stream.cuda_stream  # ctypes passes the integer as a void*
+    if device is not None and device.index is not None:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # the same handle, without a Stream object around it
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def workspace_bytes(batch, seqlen, d_inner, d_state, io_dtype=torch.bfloat16, chunk_hint=0) -> int:

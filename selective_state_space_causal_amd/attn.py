@@ -8,7 +8,9 @@ heads of a packed q/k/v projection are used in place); the D values of a head ar
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -64,6 +66,42 @@ def declare(lib):
                                          ctypes.c_size_t, vp]
 
 
+class _Calls:
+    """The entry points, taking the structures above by address: a call packs its structures into one buffer of
+    its own (_pack) instead of building an object for each, a third of the time a small call takes."""
+
+    def __init__(self, lib):
+        vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+        def entry(name, *args):
+            return ctypes.CFUNCTYPE(ctypes.c_int, *args)((name, lib))
+        self.rope = entry("ssm_rope", i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp)
+        self.kv_write = entry("ssm_kv_write", i64, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp)
+        self.kv_read = entry("ssm_kv_read", i64, i32, vp, vp, vp, vp, vp)
+        self.attn_prefill = entry("ssm_attn_prefill", vp, vp, vp, vp, vp, vp, vp, vp, vp)
+        self.attn_decode_step = entry("ssm_attn_decode_step", i64, i32, i32, ctypes.c_float, vp, vp, vp, i64, vp, vp, vp,
+                                      vp, ctypes.c_size_t, vp)
+
+
+_calls = None
+
+
+def _entry() -> _Calls:
+    global _calls
+    if _calls is None:
+        _calls = _Calls(_lib.load())
+    return _calls
+
+
+_VIEW = 24  # bytes of a _View
+_Buffer = ctypes.c_char * 192
+_two_views = struct.Struct("QqqQqq").pack_into
+_views_rope = struct.Struct("QqqQqqQqqQqqQQiif4x").pack_into
+_five_views_rope = struct.Struct("QqqQqqQqqQqqQqqQQiif4x").pack_into
+_four_views_dims = struct.Struct("QqqQqqQqqQqqqqqiiiiif").pack_into
+_no_view = (0, 0, 0)
+
+
 def _io(t: torch.Tensor) -> int:
     code = _IO.get(t.dtype)
     if code is None:
@@ -71,19 +109,27 @@ def _io(t: torch.Tensor) -> int:
     return code
 
 
-def _view(t: torch.Tensor, name: str, shape, dtype, device) -> _View:
+def _view(t: torch.Tensor, name: str, shape, dtype, device):
     """A [T, H, D] tensor's view, checked for shape, dtype, GPU device and contiguous heads."""
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.device != device or device.type != "cuda":
         raise ValueError(f"{name} must be on {device} (a GPU)")
-    st = t.stride()
-    if st[2] != 1 and shape[2] != 1:
-        raise ValueError(f"{name}: the values of a head must be contiguous (stride {st[2]})")
+    ts, hs, one = t.stride()
+    if one != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous (stride {one})")
     # the stride of an axis of length 1 is never used, and torch leaves it arbitrary
-    return _View(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+
+
+def _new(like: torch.Tensor, shape, stream):
+    """A contiguous output [T, H, D] and its view."""
+    t = like.new_empty(shape)
+    if stream is not None:  # allocated for the current stream, used on another: not to be handed out before that is done
+        t.record_stream(stream)
+    return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _three(t, name):
@@ -99,18 +145,8 @@ def _index(t: torch.Tensor, name: str, shape, dtype, device):
                      f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _status(lib, name, st):
-    if st != 0:
-        raise SsmError(name, st, lib.ssm_status_str(st).decode())
-
-
-def _own(stream, *tensors):
-    """Tensors allocated here and used on a stream that is not the current one: the allocator must
-    not hand them out again before that stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _fail(name, st):
+    raise SsmError(name, st, _lib.load().ssm_status_str(st).decode())
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -151,38 +187,44 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[s
     return freq.to(device), mscale
 
 
-def _rope_desc(positions, freq, interleaved, mscale, T, device) -> _Rope:
-    return _Rope(_index(positions, "positions", (T,), torch.int64, device),
-                 _index(freq, "freq", (freq.numel(),), torch.float64, device), freq.numel(), bool(interleaved), mscale)
+def _rope_fields(positions, freq, interleaved, mscale, T, device):
+    pairs = freq.numel()
+    return (_index(positions, "positions", (T,), torch.int64, device), _index(freq, "freq", (pairs,), torch.float64, device),
+            pairs, bool(interleaved), mscale)
 
 
 def rope(q, k, positions, freq, *, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None,
          stream=None):
     """ssm_rope: q [T, Hq, D] and k [T, Hkv, D] (or None) rotated by positions [T] int64; freq (and
     mscale) as rope_frequencies gives them.  Returns (q_out, k_out); pass q_out=q, k_out=k for in place."""
-    lib = _lib.load()
-    T, Hq, D = _three(q, "q")
-    dev = q.device
+    call = _entry().rope
+    T, Hq, D = shape = _three(q, "q")
+    dev, dtype = q.device, q.dtype
     io = _io(q)
-    vq = _view(q, "q", (T, Hq, D), q.dtype, dev)
-    desc = _rope_desc(positions, freq, interleaved, mscale, T, dev)
-    new = []
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        new.append(q_out)
-    vqo = _view(q_out, "q_out", (T, Hq, D), q.dtype, dev)
-    Hk, vk, vko = 0, None, None
+    vq = _view(q, "q", shape, dtype, dev)
+    desc = _rope_fields(positions, freq, interleaved, mscale, T, dev)
+    Hk, vk, vko = 0, _no_view, _no_view
     if k is not None:
         Hk = _three(k, "k")[1]
-        vk = _view(k, "k", (T, Hk, D), q.dtype, dev)
+        kshape = (T, Hk, D)
+        vk = _view(k, "k", kshape, dtype, dev)
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-            new.append(k_out)
-        vko = _view(k_out, "k_out", (T, Hk, D), q.dtype, dev)
+            k_out, vko = _new(q, kshape, stream)
+        else:
+            vko = _view(k_out, "k_out", kshape, dtype, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _status(lib, "ssm_rope", lib.ssm_rope(T, Hq, Hk, D, io, desc, vq, vqo, vk, vko, stream_handle(stream, dev)))
-    _own(stream, *new)
+    if q_out is None:
+        q_out, vqo = _new(q, shape, stream)
+    else:
+        vqo = _view(q_out, "q_out", shape, dtype, dev)
+    buf = _Buffer()
+    _views_rope(buf, 0, *vq, *vqo, *vk, *vko, *desc)
+    at = ctypes.addressof(buf)
+    st = call(T, Hq, Hk, D, io, at + 4 * _VIEW, at, at + _VIEW, at + 2 * _VIEW if Hk else None,
+              at + 3 * _VIEW if Hk else None, stream_handle(stream, dev))
+    if st != 0:
+        _fail("ssm_rope", st)
     return q_out, k_out
 
 
@@ -193,36 +235,42 @@ class KVCache:
     float8_e4m3fn, and for the 8-bit types k_scale and v_scale [pages, Hkv, page_size] fp32.  The
     tensors are the caller's; this holds them and their description."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "device", "kv_heads", "head_dim", "page_size", "pages")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "address", "device", "kv_heads", "head_dim", "page_size", "pages",
+                 "io_only")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4:
             raise ValueError(f"k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
-        kind = _CODES.get(k.dtype)
-        if kind is None:
-            if k.dtype not in _IO:
-                raise TypeError(f"a cache holds float32, bfloat16, int8 or float8_e4m3fn, got {k.dtype}")
-            kind = KV_IO
-        dev = k.device
-        for t, name, shape, dtype in ((k, "k", k.shape, k.dtype), (v, "v", k.shape, k.dtype),
-                                      (k_scale, "k_scale", k.shape[:3], torch.float32),
-                                      (v_scale, "v_scale", k.shape[:3], torch.float32)):
-            scale = name.endswith("scale")
-            if scale and kind == KV_IO:
-                if t is not None:
-                    raise ValueError(f"{name}: only the 8-bit types have scales")
-                continue
-            if t is None:
-                raise ValueError(f"{name} is required")
-            if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a GPU),"
-                                 f" got {t.dtype} {tuple(t.shape)} on {t.device}")
+        shape, dtype, dev = k.shape, k.dtype, k.device
+        kind = _CODES.get(dtype, KV_IO)
+        if kind == KV_IO:
+            if dtype not in _IO:
+                raise TypeError(f"a cache holds float32, bfloat16, int8 or float8_e4m3fn, got {dtype}")
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("k_scale and v_scale: only the 8-bit types have scales")
+            pks = pvs = None
+        else:
+            pks = self._address(k_scale, "k_scale", shape[:3], torch.float32, dev)
+            pvs = self._address(v_scale, "v_scale", shape[:3], torch.float32, dev)
+        pk, pv = self._address(k, "k", shape, dtype, dev), self._address(v, "v", shape, dtype, dev)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.pages, self.kv_heads, self.page_size, self.head_dim = shape
         self.device = dev
-        self.desc = _Cache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-                           None if v_scale is None else v_scale.data_ptr(), self.pages, self.page_size, self.kv_heads,
-                           self.head_dim, kind)
+        self.io_only = dtype if kind == KV_IO else None  # the io dtype that a cache of that dtype is tied to
+        self.desc = _Cache(pk, pv, pks, pvs, *self._sizes(), kind)
+        self.address = ctypes.addressof(self.desc)
+
+    def _sizes(self):
+        return self.pages, self.page_size, self.kv_heads, self.head_dim
+
+    @staticmethod
+    def _address(t, name, shape, dtype, dev):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a GPU),"
+                             f" got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
 
     @classmethod
     def allocate(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,
@@ -233,7 +281,7 @@ class KVCache:
         return cls(k, torch.empty_like(k), *scale)
 
     def check_io(self, dtype):
-        if self.k.dtype in _IO and self.k.dtype != dtype:
+        if self.io_only is not None and self.io_only != dtype:
             raise TypeError(f"a cache of {self.k.dtype} is written and read in that type, got {dtype}")
 
 
@@ -242,61 +290,80 @@ def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, 
     """ssm_kv_write: keys and values k, v [T, Hkv, D] into the cache rows slots [T] int64 (page *
     page_size + place; out of range: skipped).  With positions and freq the keys are rotated on the way, and q
     [T, Hq, D] too where given; a k_out tensor receives the rotated keys.  Returns q_out (None without q)."""
-    lib = _lib.load()
-    T, Hk, D = _three(k, "k")
-    dev = cache.device
+    call = _entry().kv_write
+    T = _three(k, "k")[0]
+    dev, dtype = cache.device, k.dtype
     shape = (T, cache.kv_heads, cache.head_dim)
-    cache.check_io(k.dtype)
+    cache.check_io(dtype)
     io = _io(k)
-    vk, vv = _view(k, "k", shape, k.dtype, dev), _view(v, "v", shape, k.dtype, dev)
+    vk, vv = _view(k, "k", shape, dtype, dev), _view(v, "v", shape, dtype, dev)
     ps = _index(slots, "slots", (T,), torch.int64, dev)
-    desc, vq, vqo, vko, Hq, new = None, None, None, None, 0, None
+    Hq, vq, vqo, vko, desc = 0, _no_view, _no_view, _no_view, None
     if (positions is None) != (freq is None):
         raise ValueError("positions and freq go together")
     if positions is not None:
-        desc = _rope_desc(positions, freq, interleaved, mscale, T, dev)
+        desc = _rope_fields(positions, freq, interleaved, mscale, T, dev)
         if k_out is not None:
-            vko = _view(k_out, "k_out", shape, k.dtype, dev)
+            vko = _view(k_out, "k_out", shape, dtype, dev)
         if q is not None:
             Hq = _three(q, "q")[1]
-            vq = _view(q, "q", (T, Hq, D), k.dtype, dev)
+            qshape = (T, Hq, cache.head_dim)
+            vq = _view(q, "q", qshape, dtype, dev)
             if q_out is None:
-                q_out = new = torch.empty((T, Hq, D), dtype=k.dtype, device=dev)
-            vqo = _view(q_out, "q_out", (T, Hq, D), k.dtype, dev)
+                q_out, vqo = _new(q, qshape, stream)
+            else:
+                vqo = _view(q_out, "q_out", qshape, dtype, dev)
     elif q is not None or k_out is not None:
         raise ValueError("q and k_out are for a call with positions and freq")
     if q is None and q_out is not None:
         raise ValueError("q_out without q")
-    _status(lib, "ssm_kv_write", lib.ssm_kv_write(T, io, cache.desc, ps, vk, vv, desc, Hq, vq, vqo, vko,
-                                                  stream_handle(stream, dev)))
-    _own(stream, new)
+    buf = _Buffer()
+    at = ctypes.addressof(buf)
+    if desc is None:
+        _two_views(buf, 0, *vk, *vv)
+        st = call(T, io, cache.address, ps, at, at + _VIEW, None, 0, None, None, None, stream_handle(stream, dev))
+    else:
+        _five_views_rope(buf, 0, *vk, *vv, *vq, *vqo, *vko, *desc)
+        st = call(T, io, cache.address, ps, at, at + _VIEW, at + 5 * _VIEW, Hq, at + 2 * _VIEW if Hq else None,
+                  at + 3 * _VIEW if Hq else None, at + 4 * _VIEW if k_out is not None else None,
+                  stream_handle(stream, dev))
+    if st != 0:
+        _fail("ssm_kv_write", st)
     return q_out
 
 
 def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream=None):
     """ssm_kv_read: the rows at slots [T] int64 as (k, v) [T, Hkv, D] in dtype (the cache's own, or bfloat16
     for the 8-bit types, where not given); slots out of range read as zeros."""
-    lib = _lib.load()
+    call = _entry().kv_read
     dev = cache.device
     if slots.dim() != 1:
         raise ValueError(f"slots must have one axis, got {tuple(slots.shape)}")
     T = slots.shape[0]
     if dtype is None:
-        dtype = k_out.dtype if k_out is not None else cache.k.dtype if cache.k.dtype in _IO else torch.bfloat16
+        dtype = k_out.dtype if k_out is not None else cache.io_only or torch.bfloat16
     cache.check_io(dtype)
+    if dtype not in _IO:
+        raise TypeError(f"io tensors must be float32 or bfloat16, got {dtype}")
     shape = (T, cache.kv_heads, cache.head_dim)
     ps = _index(slots, "slots", (T,), torch.int64, dev)
-    new = []
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
-        new.append(k_out)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-        new.append(v_out)
-    vk, vv = _view(k_out, "k_out", shape, dtype, dev), _view(v_out, "v_out", shape, dtype, dev)
-    _status(lib, "ssm_kv_read", lib.ssm_kv_read(T, _io(k_out), cache.desc, ps, vk, vv, stream_handle(stream, dev)))
-    _own(stream, *new)
-    return k_out, v_out
+    views, outs = [], []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+            if stream is not None:
+                t.record_stream(stream)
+            views.append((t.data_ptr(), shape[1] * shape[2], shape[2]))
+        else:
+            views.append(_view(t, name, shape, dtype, dev))
+        outs.append(t)
+    buf = _Buffer()
+    _two_views(buf, 0, *views[0], *views[1])
+    at = ctypes.addressof(buf)
+    st = call(T, _IO[dtype], cache.address, ps, at, at + _VIEW, stream_handle(stream, dev))
+    if st != 0:
+        _fail("ssm_kv_read", st)
+    return outs[0], outs[1]
 
 
 # ---------------------------------------------------------------- attention
@@ -308,31 +375,42 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, *, causal: bool = True, scale: Option
     defaults to cu_q); causal lets its last query see all its keys, the one before one less, and so on.  scale
     defaults to 1 / sqrt(D).  A query that sees no key gives zeros.  Returns out [Tq, Hq, D]; an lse tensor
     [Tq, Hq] fp32 receives the log of the softmax sums."""
-    lib = _lib.load()
-    Tq, Hq, D = _three(q, "q")
+    call = _entry().attn_prefill
+    Tq, Hq, D = shape = _three(q, "q")
     Tk, Hkv, _ = _three(k, "k")
-    dev = q.device
+    dev, dtype = q.device, q.dtype
     io = _io(q)
     cu_k = cu_q if cu_k is None else cu_k
     if cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError(f"cu_q must be [batch + 1] with batch >= 1, got {tuple(cu_q.shape)}")
-    B = cu_q.shape[0] - 1
-    vq = _view(q, "q", (Tq, Hq, D), q.dtype, dev)
-    vk, vv = _view(k, "k", (Tk, Hkv, D), q.dtype, dev), _view(v, "v", (Tk, Hkv, D), q.dtype, dev)
-    pq, pk = (_index(t, n, (B + 1,), torch.int32, dev) for t, n in ((cu_q, "cu_q"), (cu_k, "cu_k")))
-    new = None
+    ends = cu_q.shape
+    kshape = (Tk, Hkv, D)
+    vq = _view(q, "q", shape, dtype, dev)
+    vk, vv = _view(k, "k", kshape, dtype, dev), _view(v, "v", kshape, dtype, dev)
+    pq, pk = _index(cu_q, "cu_q", ends, torch.int32, dev), _index(cu_k, "cu_k", ends, torch.int32, dev)
     if out is None:
-        out = new = torch.empty((Tq, Hq, D), dtype=q.dtype, device=dev)
-    vo = _view(out, "out", (Tq, Hq, D), q.dtype, dev)
+        out, vo = _new(q, shape, stream)
+    else:
+        vo = _view(out, "out", shape, dtype, dev)
     pl = None if lse is None else _index(lse, "lse", (Tq, Hq), torch.float32, dev)
-    d = _Dims(B, Tq, Tk, Hq, Hkv, D, io, bool(causal), D ** -0.5 if scale is None else scale)
-    _status(lib, "ssm_attn_prefill", lib.ssm_attn_prefill(d, vq, vk, vv, pq, pk, vo, pl, stream_handle(stream, dev)))
-    _own(stream, new)
+    buf = _Buffer()
+    _four_views_dims(buf, 0, *vq, *vk, *vv, *vo, ends[0] - 1, Tq, Tk, Hq, Hkv, D, io, bool(causal),
+                     D ** -0.5 if scale is None else scale)
+    at = ctypes.addressof(buf)
+    st = call(at + 4 * _VIEW, at, at + _VIEW, at + 2 * _VIEW, pq, pk, at + 3 * _VIEW, pl, stream_handle(stream, dev))
+    if st != 0:
+        _fail("ssm_attn_prefill", st)
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(batch, q_heads, pages, page_size, kv_heads, head_dim, table_width):
+    sizes = _Cache(None, None, None, None, pages, page_size, kv_heads, head_dim, KV_IO)
+    return int(_lib.load().ssm_attn_decode_workspace_bytes(batch, q_heads, sizes, table_width))
+
+
 def attn_decode_workspace_bytes(batch: int, q_heads: int, cache: KVCache, table_width: int) -> int:
-    return int(_lib.load().ssm_attn_decode_workspace_bytes(batch, q_heads, cache.desc, table_width))
+    return _decode_workspace(batch, q_heads, *cache._sizes(), table_width)
 
 
 def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] = None, out=None, lse=None,
@@ -341,30 +419,39 @@ def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] =
     among them: write it first).  table [B, width] int32: the pages of each sequence; lens [B] int32.  scale defaults
     to 1 / sqrt(D).  workspace: attn_decode_workspace_bytes() bytes, allocated where not given.  Returns out
     [B, Hq, D]; an lse tensor [B, Hq] fp32 receives the log of the softmax sums."""
-    lib = _lib.load()
+    call = _entry().attn_decode_step
     B, Hq, D = _three(q, "q")
-    dev = cache.device
-    cache.check_io(q.dtype)
+    dev, dtype = cache.device, q.dtype
+    cache.check_io(dtype)
     io = _io(q)
     if table.dim() != 2:
         raise ValueError(f"table must be [batch, width], got {tuple(table.shape)}")
     W = table.shape[1]
     shape = (B, Hq, cache.head_dim)
-    vq = _view(q, "q", shape, q.dtype, dev)
+    vq = _view(q, "q", shape, dtype, dev)
     pt, pn = _index(table, "table", (B, W), torch.int32, dev), _index(lens, "lens", (B,), torch.int32, dev)
-    new, ws = None, None
     if out is None:
-        out = new = torch.empty(shape, dtype=q.dtype, device=dev)
-    vo = _view(out, "out", shape, q.dtype, dev)
+        out, vo = _new(q, shape, stream)
+    else:
+        vo = _view(out, "out", shape, dtype, dev)
     pl = None if lse is None else _index(lse, "lse", (B, Hq), torch.float32, dev)
+    pw, size = None, 0
     if workspace is None:
-        need = lib.ssm_attn_decode_workspace_bytes(B, Hq, cache.desc, W)
-        workspace = ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        size = _decode_workspace(B, Hq, *cache._sizes(), W)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+            pw = workspace.data_ptr()
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _status(lib, "ssm_attn_decode_step", lib.ssm_attn_decode_step(
-        B, Hq, io, D ** -0.5 if scale is None else scale, cache.desc, vq, pt, W, pn, vo, pl,
-        None if workspace is None else workspace.data_ptr(), size, stream_handle(stream, dev)))
-    _own(stream, new, ws)
+    else:
+        pw, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    buf = _Buffer()
+    _two_views(buf, 0, *vq, *vo)
+    at = ctypes.addressof(buf)
+    st = call(B, Hq, io, D ** -0.5 if scale is None else scale, cache.address, at, pt, W, pn, at + _VIEW, pl, pw, size,
+              stream_handle(stream, dev))
+    if st != 0:
+        _fail("ssm_attn_decode_step", st)
     return out

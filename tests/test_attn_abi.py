@@ -18,7 +18,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "ssm_attn.h")
 OK, NULL, SHAPE, DTYPE, ALIGN, ALIAS, WORKSPACE = range(7)
 BASE, STEP = 0x7F0000000000, 1 << 36
-T, HQ, HK, D, PAGE, PAGES, B, W = 10, 4, 2, 64, 16, 8, 3, 5
+T, HQ, HK, D, PAGE, PAGES, B, W = 10, 4, 2, 64, 16, 8, 3, 500  # 8000 tokens: several chunks, with a workspace
 
 
 def at(i, off=0):
