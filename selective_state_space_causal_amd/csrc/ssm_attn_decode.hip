@@ -275,8 +275,14 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
           s[t][i] = KV != SSM_KV_IO ? p * x.sv[t][i] : p;
         }
       if constexpr (BF) {
-        const u32x4 pf = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                          pack_bf16(s[1][2], s[1][3])};
+        // A weight as the sum of two bf16 (2^-17): one alone would be as inexact as the output's own rounding.
+        u32x4 pf, pr;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = s[j / 2][j % 2 * 2], x1 = s[j / 2][j % 2 * 2 + 1];
+          pf[j] = pack_bf16(x0, x1);
+          pr[j] = pack_bf16(x0 - __uint_as_float(pf[j] << 16), x1 - __uint_as_float(pf[j] & 0xFFFF0000u));
+        }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -298,10 +304,12 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
             }
             f32x4& o0 = o[n * VE + c];
             f32x4& o1 = o[n * VE + c + 1];
-            o0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v0), __builtin_bit_cast(bf16x8, pf), o0,
-                                                         0, 0, 0);
-            o1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v1), __builtin_bit_cast(bf16x8, pf), o1,
-                                                         0, 0, 0);
+#pragma unroll
+            for (const u32x4& p : {pf, pr}) {
+              const bf16x8 w = __builtin_bit_cast(bf16x8, p);
+              o0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v0), w, o0, 0, 0, 0);
+              o1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v1), w, o1, 0, 0, 0);
+            }
           }
       } else {
 #pragma unroll
