@@ -131,6 +131,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(Prefi
   typedef Tile<DP> L;
   constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH;
   constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
+  static_assert(NW == 4 && KT >= 32, "a buffer for each wave's 32 rows of output");
   // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
   __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
@@ -271,23 +272,28 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(Prefi
       }
     }
 
+    // The output through LDS (one of the buffers for each wave; their reads ended at the last barrier), so that
+    // memory gets whole rows and not 8 bytes of each.
     l = half_sum(l);
-    if (r < rows) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const int head = h * a.G + g;
-      char* op = a.out.p + (int64_t)(q0 + tok) * a.out.ts + (int64_t)head * a.out.hs;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    char* stage = wave == 0 ? kt0 : wave == 1 ? kt1 : wave == 2 ? vt0 : vt1;
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = d * 32 + 8 * i + 4 * half;
-          if (e >= a.D) continue;
-          *reinterpret_cast<u32x2*>(op + e * 2) = u32x2{pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
-                                                       pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
-        }
-      if (a.lse && half == 0)
-        a.lse[(int64_t)(q0 + tok) * a.Hq + head] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(stage + L::k_at(col, d * 4 + i) + half * 8) =
+            u32x2{pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+    const int64_t row_at = (int64_t)(q0 + tok) * a.out.ts + (int64_t)(h * a.G + g) * a.out.hs;
+    constexpr int PIECES = DP / 8;
+#pragma unroll
+    for (int i = 0; i < 32 * PIECES / 64; ++i) {
+      const int c = i * 64 + lane, row = c / PIECES, ch = c - row * PIECES;
+      const int64_t at = __shfl(row_at, row);
+      if (r0 + row < rows && ch * 8 < a.D)
+        *reinterpret_cast<u32x4*>(a.out.p + at + ch * 16) = *reinterpret_cast<const u32x4*>(stage + L::k_at(row, ch));
     }
+    if (a.lse && half == 0 && r < rows)
+      a.lse[(int64_t)(q0 + tok) * a.Hq + h * a.G + g] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
   }
 }
 
