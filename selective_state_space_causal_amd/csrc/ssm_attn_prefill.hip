@@ -47,36 +47,86 @@ struct Work {
   int q0, lq, k0, lk;  // its queries and keys
 };
 
+// The same value, of which the compiler knows nothing: what is computed from it stays where it stands, instead of
+// being kept in registers through the loop over keys, which needs them all.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// (q0, lq, k0, lk) of sequence b; empty past the last.
+__device__ __forceinline__ int4 bounds(const PrefillArgs& a, int b) {
+  int4 s = {0, 0, 0, 0};
+  if (b < a.B) {
+    s.x = min(max(a.cu_q[b], 0), a.Tq);
+    s.y = max(min(a.cu_q[b + 1], a.Tq) - s.x, 0);
+    s.z = min(max(a.cu_k[b], 0), a.Tk);
+    s.w = max(min(a.cu_k[b + 1], a.Tk) - s.z, 0);
+  }
+  return s;
+}
+
+__device__ __forceinline__ int tiles_of(const PrefillArgs& a, int QT, int lq) {
+  return (int)(((unsigned)(lq * a.G) + QT - 1) / QT);
+}
+
 // The sequence and tile that hold tile `idx` of the packed batch (false past the end).  Each wave finds
 // it by itself: 64 sequences at a time, a prefix sum of their tile counts over the lanes.
 __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int QT, int64_t idx, Work& w) {
   const int lane = threadIdx.x & 63;
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int bb = b0 + lane;
-    int q0 = 0, lq = 0, k0 = 0, lk = 0;
-    if (bb < a.B) {
-      q0 = min(max(a.cu_q[bb], 0), a.Tq);
-      lq = max(min(a.cu_q[bb + 1], a.Tq) - q0, 0);
-      k0 = min(max(a.cu_k[bb], 0), a.Tk);
-      lk = max(min(a.cu_k[bb + 1], a.Tk) - k0, 0);
-    }
-    const int n = (int)(((int64_t)lq * a.G + QT - 1) / QT), incl = wave_scan(n);
+    const int4 q = bounds(a, b0 + lane);
+    const int n = tiles_of(a, QT, q.y), incl = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (idx < base + total) {
       const int want = (int)(idx - base);
       const int at = __ffsll((unsigned long long)__ballot(incl > want)) - 1;
       w.tiles = __builtin_amdgcn_readlane(n, at);
       w.tile = want - (__builtin_amdgcn_readlane(incl, at) - w.tiles);
-      w.q0 = __builtin_amdgcn_readlane(q0, at);
-      w.lq = __builtin_amdgcn_readlane(lq, at);
-      w.k0 = __builtin_amdgcn_readlane(k0, at);
-      w.lk = __builtin_amdgcn_readlane(lk, at);
+      w.q0 = __builtin_amdgcn_readlane(q.x, at);
+      w.lq = __builtin_amdgcn_readlane(q.y, at);
+      w.k0 = __builtin_amdgcn_readlane(q.z, at);
+      w.lk = __builtin_amdgcn_readlane(q.w, at);
       return true;
     }
     base += total;
   }
   return false;
+}
+
+// Tile `idx` in the order of falling work (key tiles of KT): up to 64 sequences, one a lane (q: its bounds).  The
+// tiles with at least c key tiles are counted for a c found by bisection.
+__device__ __forceinline__ bool find_sorted(const PrefillArgs& a, int QT, int KT, int4 q, int64_t idx, Work& w) {
+  const int tiles = tiles_of(a, QT, q.y);
+  // Tiles of this lane's sequence whose last row sees more than (c - 1) KT keys.
+  const auto at_least = [&](int c) {
+    const int64_t x = (int64_t)(c - 1) * KT;
+    if (c <= 0) return tiles;
+    if (!a.causal) return q.w > x ? tiles : 0;
+    const int64_t token = x - (q.w - q.y);  // the first token that sees so many
+    if (token >= q.y) return 0;
+    return tiles - (token <= 0 ? 0 : (int)(((unsigned)((int)token * a.G) + QT) / QT) - 1);
+  };
+  const auto total = [&](int n) { return __builtin_amdgcn_readlane(wave_scan(n), 63); };
+  if (idx >= total(tiles)) return false;
+  const int want = (int)idx;
+  int lo = 0, hi = (int)(((unsigned)a.Tk + KT - 1) / KT);  // more than lo's tiles hold it, no more than hi + 1's
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (total(at_least(mid)) > want) lo = mid;
+    else hi = mid - 1;
+  }
+  const int more = at_least(lo + 1), n = at_least(lo) - more, incl = wave_scan(n);
+  const int rank = want - total(more);
+  const int at = __ffsll((unsigned long long)__ballot(incl > rank)) - 1;
+  w.tiles = __builtin_amdgcn_readlane(tiles, at);
+  w.tile = w.tiles - __builtin_amdgcn_readlane(more + incl, at) + rank;  // the class's tiles end where `more` begin
+  w.q0 = __builtin_amdgcn_readlane(q.x, at);
+  w.lq = __builtin_amdgcn_readlane(q.y, at);
+  w.k0 = __builtin_amdgcn_readlane(q.z, at);
+  w.lk = __builtin_amdgcn_readlane(q.w, at);
+  return true;
 }
 
 // The two halves' values of one row joined: max / sum over lane and lane ^ 32.
@@ -125,17 +175,23 @@ __device__ __forceinline__ void load_tile(const char* p, int ts, const int* off,
 }
 
 // bf16: a workgroup of NW waves has 32 rows a wave; key tiles of KT keys go straight into one of two LDS buffers
-// while the other is worked on.
+// while the other is worked on.  A workgroup takes tiles of rows in turn until there are none, and the key
+// tiles of one follow those of the last without a break: the next one's first keys are loaded under the
+// last key tile of this one, its queries under that tile's softmax, and the output is stored under what comes then.
+// Each head's tiles are dealt out in the order of falling work, forwards and backwards in turn.
 template <int DP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(PrefillArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(DP <= 192 ? 2 : 1, DP <= 192 ? 2 : 1)))
+void attn_prefill(PrefillArgs a) {
   typedef Tile<DP> L;
-  constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH;
+  constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH, AHEAD = 4;
   constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
-  static_assert(NW == 4 && KT >= 32, "a buffer for each wave's 32 rows of output");
   // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
   __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
+  __shared__ __attribute__((aligned(16))) char stage[NW][8 * CH * 16];  // 8 rows of a wave's output
+  __shared__ int4 seqs[64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (threadIdx.x < 64) seqs[threadIdx.x] = bounds(a, threadIdx.x);
 
   // This thread's pieces of a tile: the chunk of memory that belongs at each place (the first one past a row's end:
   // K's meets zeros of Q, V's gives channels that are not stored).
@@ -148,57 +204,89 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(Prefi
     koff[i] = row * kts + (kc * 8 < a.D ? kc : 0) * 16;
     voff[i] = row * vts + (vc * 8 < a.D ? vc : 0) * 16;
   }
+  __syncthreads();
 
-  const int h = blockIdx.x;
-  Work w;
-  for (int64_t idx = blockIdx.y; find_tile(a, QT, idx, w); idx += gridDim.y) {
-    const int tile = w.tiles - 1 - w.tile;  // causal: the tiles with the most keys first
-    const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
-    const int rows = lq * a.G, r0 = tile * QT + wave * 32;
-    const int r = r0 + col, rc = min(r, rows - 1);
-    const int tok = rc / a.G, g = rc - tok * a.G;
-    // Keys that a row sees: [0, seen).
-    const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
-    const int seen = seen_by(tok);
-    const int wave_first = __builtin_amdgcn_readfirstlane(seen_by(min(r0, rows - 1) / a.G));
-    const int wave_last = r0 >= rows ? 0 : __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
-    const int block_last = seen_by(min(tile * QT + QT - 1, rows - 1) / a.G);
-
-    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
-    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
-    // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
-    const auto load = [&](int j0, char* kt, char* vt) {
-      const int last = min(lk - 1 - j0, KT - 1);
-      load_tile<NL, NW, CH, KT>(kp + (int64_t)j0 * a.k.ts, kts, koff, last, wave, kt);
-      load_tile<NL, NW, CH, KT>(vp + (int64_t)j0 * a.v.ts, vts, voff, last, wave, vt);
-    };
-    __syncthreads();  // the last tile's reads of the buffers are over
-    if (block_last > 0) load(0, kt0, vt0);
-
-    // Q as the right operand: a lane's row, in the order that the K reads below use.
-    u32x4 qf[NQ];
-    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
+  const int h = blockIdx.x, places = gridDim.y, place = blockIdx.y;
+  int64_t dealt = 0;  // tiles dealt to all places before this round
+  bool forwards = true;
+  // The next tile of rows; false when there are no more.
+  const auto next = [&](Work& w) {
+    const int64_t idx = dealt + (forwards ? place : places - 1 - place);
+    dealt += places;
+    forwards = !forwards;
+    if (a.B <= 64) return find_sorted(a, QT, KT, seqs[here(lane)], idx, w);
+    const bool found = find_tile(a, QT, idx, w);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) of its loads here, not under the products
+    if (!found) return false;
+    w.tile = w.tiles - 1 - w.tile;  // causal: a sequence's tiles with the most keys first
+    return true;
+  };
+  // Keys that a token of a sequence sees: [0, seen_by).
+  const auto seen_by = [&](const Work& w, int token) {
+    return a.causal ? min(max(token + 1 + w.lk - w.lq, 0), w.lk) : w.lk;
+  };
+  const auto keys_of = [&](const Work& w) {  // of a tile's last row
+    return seen_by(w, min(w.tile * QT + QT - 1, w.lq * a.G - 1) / a.G);
+  };
+  // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
+  const auto load = [&](const Work& w, int j0, char* kt, char* vt) {
+    const int last = min(w.lk - 1 - j0, KT - 1);
+    load_tile<NL, NW, CH, KT>(a.k.p + (int64_t)(w.k0 + j0) * a.k.ts + (int64_t)h * a.k.hs, kts, koff, last, wave, kt);
+    load_tile<NL, NW, CH, KT>(a.v.p + (int64_t)(w.k0 + j0) * a.v.ts + (int64_t)h * a.v.hs, vts, voff, last, wave, vt);
+  };
+  // Q as the right operand: a lane's row, in the order that the K reads below use.
+  u32x4 qf[NQ];
+  const auto load_q = [&](const Work& w) {
+    const int c = here(lane), half = c >> 5;
+    const int r = min(w.tile * QT + wave * 32 + (c & 31), w.lq * a.G - 1), tok = r / a.G;
+    const char* qp = a.q.p + (int64_t)(w.q0 + tok) * a.q.ts + (int64_t)(h * a.G + r - tok * a.G) * a.q.hs;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int ch = 2 * i + half;
       qf[i] = ch * 8 < a.D ? *reinterpret_cast<const u32x4*>(qp + ch * 16) : u32x4{0, 0, 0, 0};
     }
-    f32x16 o[ND] = {};
-    float m = -INFINITY, l = 0.0f;
+  };
 
-    const auto work = [&](int j0, const char* kt, const char* vt) {
+  Work w, nx = {};
+  if (!next(w)) return;
+  bool more = false, fresh = true;  // more: nx is the next tile; fresh: not yet looked for
+  int r0, seen, wave_first, wave_last, block_last, j0;
+  f32x16 o[ND];
+  float m, l;
+  const auto begin = [&] {
+    const int rows = w.lq * a.G;
+    r0 = w.tile * QT + wave * 32;
+    seen = seen_by(w, min(r0 + col, rows - 1) / a.G);
+    wave_first = seen_by(w, min(r0, rows - 1) / a.G);
+    wave_last = r0 >= rows ? 0 : seen_by(w, min(r0 + 31, rows - 1) / a.G);
+    block_last = keys_of(w);
+    j0 = 0;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16{};
+  };
+
+  const auto work = [&](const char* kt, const char* vt, bool last) {
+      // Operands are read some products ahead; the barriers hold each read in its place.
+      const auto read_k = [&](int i) {
+        return *reinterpret_cast<const bf16x8*>(kt + L::k_at(i / NQ * 32 + col, 2 * (i % NQ) + half));
+      };
       f32x16 s[NS];
+      bf16x8 kf[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) kf[i] = read_k(i);
       __builtin_amdgcn_s_setprio(1);  // the matrix instructions first: the other wave of a SIMD has the vector unit
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        s[n] = f32x16{};
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + L::k_at(n * 32 + col, 2 * i + half));
-          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf), __builtin_bit_cast(bf16x8, qf[i]),
-                                                         s[n], 0, 0, 0);
-        }
+      for (int i = 0; i < NS * NQ; ++i) {
+        f32x16& sn = s[i / NQ];
+        if (i % NQ == 0) sn = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
+        sn = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % AHEAD], __builtin_bit_cast(bf16x8, qf[i % NQ]), sn, 0, 0, 0);
+        if (i + AHEAD < NS * NQ) kf[i % AHEAD] = read_k(i + AHEAD);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (last) load_q(nx);
       if (j0 + KT > wave_first) {  // some row of the wave does not see some key of the tile
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -229,71 +317,118 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void attn_prefill(Prefi
           for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
       }
       const float mc = m == -INFINITY ? 0.0f : m;  // a row that has seen nothing yet: all weights 0
+      // 16 keys at a time: this half holds keys 4 half + {0..3, 8..11} of them.  Under each product of 16 keys go the
+      // reads of V for the same product of the next 16, and a share of their weights.
+      const auto weight = [&](int i) {
+        const float x = hw_exp2(fmaf(s[i / 16][i % 16], a.scale_log2, -mc));
+        s[i / 16][i % 16] = x;
+        l += x;  // this half's keys only; joined at the end
+      };
+      const auto packed = [&](int g) {
+        u32x4 p;
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
+        for (int i = 0; i < 4; ++i) p[i] = pack_bf16(s[g / 2][8 * (g & 1) + 2 * i], s[g / 2][8 * (g & 1) + 2 * i + 1]);
+        return __builtin_bit_cast(bf16x8, p);
+      };
+      const auto read_v = [&](int g, int d) {
+        // The transposing read: 16 lanes give 4 rows of 16 channels and get 4 rows of one channel each.
+        const int row = g * 16 + 4 * half + (lane & 15) / 4, e = d * 32 + (col & 16) + (lane & 3) * 4;
+        union {
+          s16x4 x[2];
+          bf16x8 v;
+        } vf;
+        vf.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row, e / 8) + (e & 4) * 2));
+        vf.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row + 8, e / 8) + (e & 4) * 2));
+        return vf.v;
+      };
+      constexpr int GROUPS = 2 * NS;
+      bf16x8 vf[ND];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[n][i] = hw_exp2(fmaf(s[n][i], a.scale_log2, -mc));
-          l += s[n][i];  // this half's keys only; joined at the end
-        }
+      for (int d = 0; d < ND; ++d) vf[d] = read_v(0, d);
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
+      for (int i = 0; i < 8; ++i) weight(i);
+      bf16x8 pf = packed(0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
-          u32x4 pf;
+      for (int g = 0; g < GROUPS; ++g) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[n][8 * t + 2 * i], s[n][8 * t + 2 * i + 1]);
-          // The transposing read: 16 lanes give 4 rows of 16 channels and get 4 rows of one channel each.
-          const int row = n * 32 + 16 * t + 4 * half + (lane & 15) / 4;
+        for (int d = 0; d < ND; ++d) {
+          __builtin_amdgcn_sched_barrier(0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[d], pf, o[d], 0, 0, 0);
+          if (g + 1 < GROUPS) {
+            vf[d] = read_v(g + 1, d);
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const int e = d * 32 + (col & 16) + (lane & 3) * 4;
-            union {
-              s16x4 x[2];
-              bf16x8 v;
-            } vf;
-            vf.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row, e / 8) + (e & 4) * 2));
-            vf.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, vt + L::v_at(row + 8, e / 8) + (e & 4) * 2));
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.v, __builtin_bit_cast(bf16x8, pf), o[d], 0, 0, 0);
+            for (int i = 0; i < 8; ++i)
+              if (i * ND / 8 == d) weight((g + 1) * 8 + i);
           }
         }
+        if (g + 1 < GROUPS) pf = packed(g + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     };
 
-    if (block_last > 0) {
-      __syncthreads();
-      for (int j0 = 0; j0 < block_last; j0 += 2 * KT) {
-        if (j0 + KT < block_last) load(j0 + KT, kt1, vt1);
-        if (j0 < wave_last) work(j0, kt0, vt0);
-        __syncthreads();
-        if (j0 + KT >= block_last) break;
-        if (j0 + 2 * KT < block_last) load(j0 + 2 * KT, kt0, vt0);
-        if (j0 + KT < wave_last) work(j0 + KT, kt1, vt1);
-        __syncthreads();
-      }
-    }
-
-    // The output through LDS (one of the buffers for each wave; their reads ended at the last barrier), so that
-    // memory gets whole rows and not 8 bytes of each.
+  // The output through LDS, 8 rows at a time, so that memory gets whole rows and not 8 bytes of each.
+  const auto store = [&] {
     l = half_sum(l);
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    char* stage = wave == 0 ? kt0 : wave == 1 ? kt1 : wave == 2 ? vt0 : vt1;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2*>(stage + L::k_at(col, d * 4 + i) + half * 8) =
-            u32x2{pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
-    const int64_t row_at = (int64_t)(q0 + tok) * a.out.ts + (int64_t)(h * a.G + g) * a.out.hs;
+    const int lane = here(threadIdx.x & 63), col = lane & 31, half = lane >> 5;
+    const int rows = w.lq * a.G, r = min(r0 + col, rows - 1), tok = r / a.G, head = h * a.G + r - tok * a.G;
+    const int64_t row_at = (int64_t)(w.q0 + tok) * a.out.ts + (int64_t)head * a.out.hs;
+    if (a.lse && half == 0 && r0 + col < rows)
+      a.lse[(int64_t)(w.q0 + tok) * a.Hq + head] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     constexpr int PIECES = DP / 8;
+    char* st = stage[wave];
 #pragma unroll
-    for (int i = 0; i < 32 * PIECES / 64; ++i) {
-      const int c = i * 64 + lane, row = c / PIECES, ch = c - row * PIECES;
-      const int64_t at = __shfl(row_at, row);
-      if (r0 + row < rows && ch * 8 < a.D)
-        *reinterpret_cast<u32x4*>(a.out.p + at + ch * 16) = *reinterpret_cast<const u32x4*>(stage + L::k_at(row, ch));
+    for (int x = 0; x < 4; ++x) {
+      if (r0 + 8 * x >= rows) break;
+      if (col >> 3 == x) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x2*>(st + L::k_at(col & 7, d * 4 + i) + half * 8) = u32x2{
+                pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < (8 * PIECES + 63) / 64; ++i) {
+        const int c = i * 64 + lane, row = c / PIECES, ch = c - row * PIECES;
+        const int64_t at = __shfl(row_at, 8 * x + row);
+        if (c < 8 * PIECES && r0 + 8 * x + row < rows && ch * 8 < a.D)
+          *reinterpret_cast<u32x4*>(a.out.p + at + ch * 16) = *reinterpret_cast<const u32x4*>(st + L::k_at(row, ch));
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-    if (a.lse && half == 0 && r < rows)
-      a.lse[(int64_t)(q0 + tok) * a.Hq + h * a.G + g] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  };
+
+  // One key tile, from (kc, vc), while the next one comes into (kn, vn); false when all is done.
+  const auto advance = [&](char* kc, char* vc, char* kn, char* vn) {
+    const bool ends = j0 + KT >= block_last;
+    if (!ends) load(w, j0 + KT, kn, vn);
+    if (fresh) more = next(nx), fresh = false;
+    if (ends && more && keys_of(nx) > 0) load(nx, 0, kn, vn);
+    const bool sees = j0 < wave_last;
+    if (sees) work(kc, vc, ends && more);
+    if (!sees && ends && more) load_q(nx);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), said here: the compiler then waits for no load under the products
+    __syncthreads();  // the reads of (kc, vc) are over, (kn, vn) and a next tile's Q are there
+    if (!ends) {
+      j0 += KT;
+      return true;
+    }
+    store();
+    if (!more) return false;
+    w = nx;
+    begin();
+    fresh = true;
+    return true;
+  };
+
+  begin();
+  if (block_last > 0) load(w, 0, kt0, vt0);
+  load_q(w);
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  __syncthreads();
+  while (advance(kt0, vt0, kt1, vt1) && advance(kt1, vt1, kt0, vt0)) {
   }
 }
 
@@ -472,20 +607,22 @@ __global__ __launch_bounds__(F32_NW * 64, 1) void attn_prefill_f32(PrefillArgs a
 
 // Key heads and tiles (at most: the sum of ceil(rows / QT) over the sequences), heads first: the eight XCDs take
 // workgroups in turn, so that with eight heads each XCD's L2 holds the keys of one.
-dim3 tiles_grid(const PrefillArgs& a, int QT) {
-  const int64_t tiles = (int64_t)a.Tq * a.G / QT + a.B, most = 65535;
-  return dim3(a.Hkv, (unsigned)(tiles < most ? tiles : most));  // 65535 * 1024 heads * 256 threads: below 2^35
+dim3 tiles_grid(const PrefillArgs& a, int QT, int places) {
+  const int64_t tiles = (int64_t)a.Tq * a.G / QT + a.B;
+  int64_t most = places / a.Hkv;
+  most = most < 1 ? 1 : most > 65535 ? 65535 : most;
+  return dim3(a.Hkv, (unsigned)(tiles < most ? tiles : most));
 }
 
 template <int DP>
 void launch_bf16(PrefillArgs& a, hipStream_t s) {
-  constexpr int NW = 4, KT = DP > 128 ? 32 : 64;  // two buffers of K and V: 64 KB, two workgroups on a CU up to 128
-  attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32), dim3(NW * 64), 0, s>>>(a);
+  constexpr int NW = 4, KT = DP > 128 ? 32 : 64, PER_CU = DP > 192 ? 1 : 2;  // two buffers of K and V: 64 KB, two workgroups on a CU up to 128
+  attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32, 256 * PER_CU), dim3(NW * 64), 0, s>>>(a);
 }
 
 template <int DP>
 void launch_f32(PrefillArgs& a, hipStream_t s) {
-  attn_prefill_f32<DP><<<tiles_grid(a, 32), dim3(F32_NW * 64), 0, s>>>(a);
+  attn_prefill_f32<DP><<<tiles_grid(a, 32, INT32_MAX), dim3(F32_NW * 64), 0, s>>>(a);
 }
 
 hipError_t launch(PrefillArgs& a, bool bf16, hipStream_t s) {
