@@ -96,8 +96,9 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int QT, int64_t 
 }
 
 // Tile `idx` in the order of falling work (key tiles of KT): up to 64 sequences, one a lane (q: its bounds).  The
-// tiles with at least c key tiles are counted for a c found by bisection.
-__device__ __forceinline__ bool find_sorted(const PrefillArgs& a, int QT, int KT, int4 q, int64_t idx, Work& w) {
+// tiles with at least c key tiles are counted for a c found by bisection.  top: a c that no tile from here on exceeds,
+// made smaller for the calls that follow (with larger idx).
+__device__ __forceinline__ bool find_sorted(const PrefillArgs& a, int QT, int KT, int4 q, int64_t idx, int& top, Work& w) {
   const int tiles = tiles_of(a, QT, q.y);
   // Tiles of this lane's sequence whose last row sees more than (c - 1) KT keys.
   const auto at_least = [&](int c) {
@@ -111,12 +112,13 @@ __device__ __forceinline__ bool find_sorted(const PrefillArgs& a, int QT, int KT
   const auto total = [&](int n) { return __builtin_amdgcn_readlane(wave_scan(n), 63); };
   if (idx >= total(tiles)) return false;
   const int want = (int)idx;
-  int lo = 0, hi = (int)(((unsigned)a.Tk + KT - 1) / KT);  // more than lo's tiles hold it, no more than hi + 1's
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
+  int lo = 0, hi = top;  // more than `want` tiles have lo key tiles or more, no more than `want` have hi + 1
+  for (int step = 1; lo < hi; step *= 2) {  // the last call's c is near: in growing steps down, then halves
+    const int mid = max(hi - step + 1, (lo + hi + 1) >> 1);
     if (total(at_least(mid)) > want) lo = mid;
     else hi = mid - 1;
   }
+  top = lo;
   const int more = at_least(lo + 1), n = at_least(lo) - more, incl = wave_scan(n);
   const int rank = want - total(more);
   const int at = __ffsll((unsigned long long)__ballot(incl > rank)) - 1;
@@ -187,7 +189,6 @@ void attn_prefill(PrefillArgs a) {
   constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
   // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
   __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
-  __shared__ __attribute__((aligned(16))) char stage[NW][8 * CH * 16];  // 8 rows of a wave's output
   __shared__ int4 seqs[64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -209,12 +210,13 @@ void attn_prefill(PrefillArgs a) {
   const int h = blockIdx.x, places = gridDim.y, place = blockIdx.y;
   int64_t dealt = 0;  // tiles dealt to all places before this round
   bool forwards = true;
+  int top = (int)(((unsigned)a.Tk + KT - 1) / KT);
   // The next tile of rows; false when there are no more.
   const auto next = [&](Work& w) {
     const int64_t idx = dealt + (forwards ? place : places - 1 - place);
     dealt += places;
     forwards = !forwards;
-    if (a.B <= 64) return find_sorted(a, QT, KT, seqs[here(lane)], idx, w);
+    if (a.B <= 64) return find_sorted(a, QT, KT, seqs[here(lane)], idx, top, w);
     const bool found = find_tile(a, QT, idx, w);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) of its loads here, not under the products
     if (!found) return false;
@@ -366,38 +368,30 @@ void attn_prefill(PrefillArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     };
 
-  // The output through LDS, 8 rows at a time, so that memory gets whole rows and not 8 bytes of each.
+  // The halves of a row hold 4 channels of 8 in turn: exchanged, each has whole 16-byte pieces.
   const auto store = [&] {
     l = half_sum(l);
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int lane = here(threadIdx.x & 63), col = lane & 31, half = lane >> 5;
-    const int rows = w.lq * a.G, r = min(r0 + col, rows - 1), tok = r / a.G, head = h * a.G + r - tok * a.G;
-    const int64_t row_at = (int64_t)(w.q0 + tok) * a.out.ts + (int64_t)head * a.out.hs;
-    if (a.lse && half == 0 && r0 + col < rows)
+    const int lane = here(threadIdx.x & 63), half = lane >> 5;
+    const int rows = w.lq * a.G, r = r0 + (lane & 31), rc = min(r, rows - 1), tok = rc / a.G, head = h * a.G + rc - tok * a.G;
+    char* op = a.out.p + (int64_t)(w.q0 + tok) * a.out.ts + (int64_t)head * a.out.hs + half * 16;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        u32x2 x[2];  // channels 32 d + 8 (i + 0, 1) + 4 half + {0..3}
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          x[j] = u32x2{pack_bf16(o[d][4 * (i + j)] * inv, o[d][4 * (i + j) + 1] * inv),
+                       pack_bf16(o[d][4 * (i + j) + 2] * inv, o[d][4 * (i + j) + 3] * inv)};
+        // the upper half's piece i for the lower half's piece i + 1
+        const auto lo = __builtin_amdgcn_permlane32_swap(x[0][0], x[1][0], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(x[0][1], x[1][1], false, false);
+        if (r < rows && d * 32 + (i + half) * 8 < a.D)
+          *reinterpret_cast<u32x4*>(op + (d * 4 + i) * 16) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+      }
+    if (a.lse && half == 0 && r < rows)
       a.lse[(int64_t)(w.q0 + tok) * a.Hq + head] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-    constexpr int PIECES = DP / 8;
-    char* st = stage[wave];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (r0 + 8 * x >= rows) break;
-      if (col >> 3 == x) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x2*>(st + L::k_at(col & 7, d * 4 + i) + half * 8) = u32x2{
-                pack_bf16(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack_bf16(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
-      }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int i = 0; i < (8 * PIECES + 63) / 64; ++i) {
-        const int c = i * 64 + lane, row = c / PIECES, ch = c - row * PIECES;
-        const int64_t at = __shfl(row_at, 8 * x + row);
-        if (c < 8 * PIECES && r0 + 8 * x + row < rows && ch * 8 < a.D)
-          *reinterpret_cast<u32x4*>(a.out.p + at + ch * 16) = *reinterpret_cast<const u32x4*>(st + L::k_at(row, ch));
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
   };
 
   // One key tile, from (kc, vc), while the next one comes into (kn, vn); false when all is done.
