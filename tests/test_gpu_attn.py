@@ -436,3 +436,76 @@ def test_attn_decode_graph_replays():
         assert torch.equal(out, got), i
         assert torch.equal(c.k.view(torch.uint8), c2.k.view(torch.uint8))
         n += 1
+
+
+# ---------------------------------------------------------------- many tiles, many chunks
+
+def whole_sequences(q, k, v, cu_q, cu_k, causal, scale):
+    """O.prefill by whole matrices of each sequence and head (the same five results)."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out, lse, mag = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf), np.zeros((T, Hq, D))
+    smax, qkmax = np.zeros((T, Hq)), np.zeros((T, Hq))
+    for b in range(len(cu_q) - 1):
+        lq, lk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        if lq <= 0 or lk <= 0:
+            continue
+        seen = np.minimum(np.maximum(np.arange(lq) + 1 + lk - lq, 0), lk) if causal else np.full(lq, lk)
+        mask = np.arange(lk)[None, :] < seen[:, None]
+        some = seen > 0
+        rows = slice(cu_q[b], cu_q[b + 1])
+        for h in range(Hq):
+            kk, vv, qq = k[cu_k[b]:cu_k[b + 1], h // G], v[cu_k[b]:cu_k[b + 1], h // G], q[rows, h]
+            s = np.where(mask, scale * (qq @ kk.T), -np.inf)
+            m = np.where(some, s.max(-1, initial=-np.inf), 0.0)
+            p = np.exp(s - m[:, None])
+            l = np.where(some, p.sum(-1), 1.0)
+            w = p / l[:, None]
+            out[rows, h], mag[rows, h] = w @ vv, w @ np.abs(vv)
+            lse[rows, h] = np.where(some, m + np.log(l), -np.inf)
+            smax[rows, h] = np.where(some, np.abs(np.where(mask, s, 0.0)).max(-1), 0.0)
+            qkmax[rows, h] = np.where(some, np.where(mask, scale * (np.abs(qq) @ np.abs(kk).T), 0.0).max(-1), 0.0)
+    return out, lse, mag, smax, qkmax
+
+
+def test_whole_sequences_is_the_oracle():
+    q, k, v, cu_q, cu_k = prefill_case([5, 0, 9, 4], [3, 2, -4, -9], 4, 2, 16, "f32")
+    for causal in (True, False):
+        for a, b in zip(whole_sequences(f64(q), f64(k), f64(v), cu_q, cu_k, causal, 0.25),
+                        O.prefill(f64(q), f64(k), f64(v), cu_q, cu_k, causal, 0.25)):
+            np.testing.assert_allclose(a, b, atol=1e-12)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,longest,Hq,Hkv,D,causal", [
+    (61, 150, 32, 1, 64, True), (64, 120, 32, 1, 128, True), (200, 60, 32, 1, 96, True), (7, 700, 64, 2, 72, False),
+    (30, 260, 32, 1, 256, True), (40, 180, 40, 2, 192, True)])
+def test_attn_prefill_many_tiles(B, longest, Hq, Hkv, D, causal, io):
+    """More tiles of rows than workgroups, of sequences of all lengths (none among them), some with past keys, some
+    with fewer keys than queries: each workgroup goes from tile to tile."""
+    g = np.random.default_rng(B)
+    lens = [int(n) for n in g.integers(0, longest, B)]
+    past = [int(n) for n in g.choice([0, 0, 0, 1, 50, -20], B)]
+    q, k, v, cu_q, cu_k = prefill_case(lens, past, Hq, Hkv, D, io)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    out = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), torch.from_numpy(cu_q).to(DEV), torch.from_numpy(cu_k).to(DEV),
+                           causal=causal, lse=lse)
+    ref = whole_sequences(f64(q), f64(k), f64(v), cu_q, cu_k, causal, D ** -0.5)
+    check_attn(out, lse, ref, io, D, "many tiles")
+
+
+@pytest.mark.parametrize("io,kind", [("bf16", "int8"), ("bf16", "e4m3"), ("f32", "io")])
+def test_attn_decode_many_chunks(io, kind):
+    """A sequence in more than 64 chunks, beside short ones in the same call."""
+    lens, Hq, Hkv, D, page = [20011, 5, 0, 16640], 6, 2, 72, 32
+    c, table, n, q = decode_case(lens, Hq, Hkv, D, page, kind, io)
+    lse = torch.empty(len(lens), Hq, device=DEV)
+    out = ssm.attn_decode_step(q, c, table, n, lse=lse)
+    ref = O.decode(f64(q), values(c, "k"), values(c, "v"), table.cpu().numpy(), lens, D ** -0.5)
+    o, rlse, mag, smax, qkmax = ref
+    tol, ltol = O.attention_tolerance(HALF[io], HALF["bf16"] if io == "bf16" else 0.0, o, mag, smax, qkmax, D, 1 << 15)
+    close(out, o, tol, "many chunks")
+    got, empty = f64(lse), np.isinf(rlse)
+    assert np.array_equal(np.isneginf(got), empty)
+    assert np.all(np.abs(np.where(empty, 0, got) - np.where(empty, 0, rlse)) <= ltol + 2.0 ** -22 * np.abs(np.where(empty, 0, rlse)))
+    assert torch.equal(ssm.attn_decode_step(q, c, table, n), out)
