@@ -46,9 +46,14 @@ struct DecodeArgs {
 
 constexpr int MIN_SHARE = 8;   // steps of a chunk, at least: two for each wave
 
+// Tables that no kernel writes, as constant memory: entries that a whole wave shares are read by the scalar unit, whose
+// loads do not wait for the vector loads of keys and values.
+typedef const __attribute__((address_space(4))) int32_t* ConstInts;
+__device__ __forceinline__ ConstInts constant(const int32_t* p) { return (ConstInts)(uintptr_t)p; }
+
 __device__ __forceinline__ int sequence_length(const DecodeArgs& a, int b) {
   const int64_t cap = a.W << a.c.page_shift;
-  const int64_t n = a.lens[b];
+  const int64_t n = constant(a.lens)[b];
   return (int)(n < 0 ? 0 : n > cap ? cap : n);
 }
 
@@ -160,7 +165,7 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
 
     f32x4 o[NB * VE] = {};
     float m = -INFINITY, l = 0.0f;
-    const int32_t* table = a.table + (int64_t)b * a.W;
+    const ConstInts table = constant(a.table) + (int64_t)b * a.W;
 
     struct Keys {
       unsigned k[2][NK][KW];
@@ -336,8 +341,8 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
       int p0 = page_of(step, 0), p1 = page_of(step, 1);
       for (; step < s_end; step += NW) {
         Keys x;
-        load(x, step, p0, p1);
         const int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
+        load(x, step, p0, p1);
         work(x, step, p0, p1);
         p0 = n0, p1 = n1;
       }
