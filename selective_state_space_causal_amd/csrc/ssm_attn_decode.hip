@@ -343,6 +343,7 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
         Keys x;
         const int n0 = page_of(step + NW, 0), n1 = page_of(step + NW, 1);
         load(x, step, p0, p1);
+        __builtin_amdgcn_sched_barrier(0);  // every load of the step before its first product
         work(x, step, p0, p1);
         p0 = n0, p1 = n1;
       }
