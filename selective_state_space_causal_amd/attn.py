@@ -93,12 +93,14 @@ def _entry() -> _Calls:
     return _calls
 
 
+_I32, _I64, _F32, _F64 = torch.int32, torch.int64, torch.float32, torch.float64
 _VIEW = 24  # bytes of a _View
 _Buffer = ctypes.c_char * 192
 _two_views = struct.Struct("QqqQqq").pack_into
 _views_rope = struct.Struct("QqqQqqQqqQqqQQiif4x").pack_into
 _five_views_rope = struct.Struct("QqqQqqQqqQqqQqqQQiif4x").pack_into
 _four_views_dims = struct.Struct("QqqQqqQqqQqqqqqiiiiif").pack_into
+_cache_fields = struct.Struct("QQQQqiiii").pack_into
 _no_view = (0, 0, 0)
 
 
@@ -115,7 +117,7 @@ def _view(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device or device.type != "cuda":
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be on {device} (a GPU)")
     ts, hs, one = t.stride()
     if one != 1 and shape[2] != 1:
@@ -189,7 +191,7 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[s
 
 def _rope_fields(positions, freq, interleaved, mscale, T, device):
     pairs = freq.numel()
-    return (_index(positions, "positions", (T,), torch.int64, device), _index(freq, "freq", (pairs,), torch.float64, device),
+    return (_index(positions, "positions", (T,), _I64, device), _index(freq, "freq", (pairs,), _F64, device),
             pairs, bool(interleaved), mscale)
 
 
@@ -235,7 +237,7 @@ class KVCache:
     float8_e4m3fn, and for the 8-bit types k_scale and v_scale [pages, Hkv, page_size] fp32.  The
     tensors are the caller's; this holds them and their description."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "address", "device", "kv_heads", "head_dim", "page_size", "pages",
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_desc", "address", "device", "kv_heads", "head_dim", "page_size", "pages",
                  "io_only")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
@@ -243,34 +245,42 @@ class KVCache:
             raise ValueError(f"k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
         shape, dtype, dev = k.shape, k.dtype, k.device
         kind = _CODES.get(dtype, KV_IO)
+        ks, vs = k_scale, v_scale
         if kind == KV_IO:
             if dtype not in _IO:
                 raise TypeError(f"a cache holds float32, bfloat16, int8 or float8_e4m3fn, got {dtype}")
-            if k_scale is not None or v_scale is not None:
+            if ks is not None or vs is not None:
                 raise ValueError("k_scale and v_scale: only the 8-bit types have scales")
-            pks = pvs = None
+            pks = pvs = 0
         else:
-            pks = self._address(k_scale, "k_scale", shape[:3], torch.float32, dev)
-            pvs = self._address(v_scale, "v_scale", shape[:3], torch.float32, dev)
-        pk, pv = self._address(k, "k", shape, dtype, dev), self._address(v, "v", shape, dtype, dev)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.kv_heads, self.page_size, self.head_dim = shape
-        self.device = dev
+            rows = shape[:3]
+            if ks is None or vs is None or ks.shape != rows or vs.shape != rows or ks.dtype != _F32 or vs.dtype != _F32 or \
+                    ks.device != dev or vs.device != dev or not ks.is_contiguous() or not vs.is_contiguous():
+                self._refuse(ks, "k_scale", rows, _F32, dev)
+                self._refuse(vs, "v_scale", rows, _F32, dev)
+            pks, pvs = ks.data_ptr(), vs.data_ptr()
+        if not k.is_cuda or v is None or v.shape != shape or v.dtype != dtype or v.device != dev or \
+                not k.is_contiguous() or not v.is_contiguous():
+            self._refuse(k, "k", shape, dtype, dev)
+            self._refuse(v, "v", shape, dtype, dev)
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, ks, vs, dev
+        pages, heads, page_size, dim = shape
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, dim
         self.io_only = dtype if kind == KV_IO else None  # the io dtype that a cache of that dtype is tied to
-        self.desc = _Cache(pk, pv, pks, pvs, *self._sizes(), kind)
-        self.address = ctypes.addressof(self.desc)
+        self._desc = desc = _Buffer()  # a _Cache
+        _cache_fields(desc, 0, k.data_ptr(), v.data_ptr(), pks, pvs, pages, page_size, heads, dim, kind)
+        self.address = ctypes.addressof(desc)
 
     def _sizes(self):
         return self.pages, self.page_size, self.kv_heads, self.head_dim
 
     @staticmethod
-    def _address(t, name, shape, dtype, dev):
+    def _refuse(t, name, shape, dtype, dev):
         if t is None:
             raise ValueError(f"{name} is required")
         if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a GPU),"
                              f" got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
 
     @classmethod
     def allocate(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,
@@ -297,7 +307,7 @@ def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, 
     cache.check_io(dtype)
     io = _io(k)
     vk, vv = _view(k, "k", shape, dtype, dev), _view(v, "v", shape, dtype, dev)
-    ps = _index(slots, "slots", (T,), torch.int64, dev)
+    ps = _index(slots, "slots", (T,), _I64, dev)
     Hq, vq, vqo, vko, desc = 0, _no_view, _no_view, _no_view, None
     if (positions is None) != (freq is None):
         raise ValueError("positions and freq go together")
@@ -346,7 +356,7 @@ def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream
     if dtype not in _IO:
         raise TypeError(f"io tensors must be float32 or bfloat16, got {dtype}")
     shape = (T, cache.kv_heads, cache.head_dim)
-    ps = _index(slots, "slots", (T,), torch.int64, dev)
+    ps = _index(slots, "slots", (T,), _I64, dev)
     views, outs = [], []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
@@ -387,12 +397,12 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, *, causal: bool = True, scale: Option
     kshape = (Tk, Hkv, D)
     vq = _view(q, "q", shape, dtype, dev)
     vk, vv = _view(k, "k", kshape, dtype, dev), _view(v, "v", kshape, dtype, dev)
-    pq, pk = _index(cu_q, "cu_q", ends, torch.int32, dev), _index(cu_k, "cu_k", ends, torch.int32, dev)
+    pq, pk = _index(cu_q, "cu_q", ends, _I32, dev), _index(cu_k, "cu_k", ends, _I32, dev)
     if out is None:
         out, vo = _new(q, shape, stream)
     else:
         vo = _view(out, "out", shape, dtype, dev)
-    pl = None if lse is None else _index(lse, "lse", (Tq, Hq), torch.float32, dev)
+    pl = None if lse is None else _index(lse, "lse", (Tq, Hq), _F32, dev)
     buf = _Buffer()
     _four_views_dims(buf, 0, *vq, *vk, *vv, *vo, ends[0] - 1, Tq, Tk, Hq, Hkv, D, io, bool(causal),
                      D ** -0.5 if scale is None else scale)
@@ -429,12 +439,12 @@ def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] =
     W = table.shape[1]
     shape = (B, Hq, cache.head_dim)
     vq = _view(q, "q", shape, dtype, dev)
-    pt, pn = _index(table, "table", (B, W), torch.int32, dev), _index(lens, "lens", (B,), torch.int32, dev)
+    pt, pn = _index(table, "table", (B, W), _I32, dev), _index(lens, "lens", (B,), _I32, dev)
     if out is None:
         out, vo = _new(q, shape, stream)
     else:
         vo = _view(out, "out", shape, dtype, dev)
-    pl = None if lse is None else _index(lse, "lse", (B, Hq), torch.float32, dev)
+    pl = None if lse is None else _index(lse, "lse", (B, Hq), _F32, dev)
     pw, size = None, 0
     if workspace is None:
         size = _decode_workspace(B, Hq, *cache._sizes(), W)

@@ -212,3 +212,38 @@ def test_rope_frequencies():
                 dict(rot_dim=8, scaling="cubic"), dict(rot_dim=2, scaling="ntk", factor=2.0)):
         with pytest.raises(ValueError):
             A.rope_frequencies(device="cpu", **bad)
+
+
+def test_binding_refuses_cpu_tensors_with_an_index():
+    q = torch.zeros(4, 2, 16, device="cpu:0")
+    pos, freq = torch.arange(4, device="cpu:0"), A.rope_frequencies(16, device="cpu:0")[0]
+    with pytest.raises(ValueError, match="GPU"):
+        A.rope(q, None, pos, freq)
+    k = torch.zeros(2, 1, 16, 8, device="cpu:0")
+    with pytest.raises(ValueError, match="GPU"):
+        A.KVCache(k, k)
+    with pytest.raises(ValueError, match="required"):
+        A.KVCache(k.to(torch.int8), k.to(torch.int8))
+
+
+def test_packed_structures_are_the_declared_ones():
+    """What the binding packs by hand has the layout of the structures."""
+    buf = A._Buffer()
+    A._cache_fields(buf, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9)
+    c = A._Cache.from_buffer(buf)
+    assert [getattr(c, n) for n, _ in A._Cache._fields_] == list(range(1, 10))
+    A._views_rope(buf, 0, *range(12), 21, 22, 23, 1, 0.5)
+    for i in range(4):
+        v = A._View.from_buffer(buf, i * A._VIEW)
+        assert (v.data or 0, v.token_stride, v.head_stride) == (3 * i, 3 * i + 1, 3 * i + 2)
+    r = A._Rope.from_buffer(buf, 4 * A._VIEW)
+    assert (r.positions, r.freq, r.pairs, r.interleaved, r.mscale) == (21, 22, 23, 1, 0.5)
+    A._five_views_rope(buf, 0, *range(15), 21, 22, 23, 1, 0.5)
+    r = A._Rope.from_buffer(buf, 5 * A._VIEW)
+    assert (r.positions, r.freq, r.pairs, r.interleaved, r.mscale) == (21, 22, 23, 1, 0.5)
+    A._four_views_dims(buf, 0, *range(12), 31, 32, 33, 34, 35, 36, 1, 0, 0.25)
+    d = A._Dims.from_buffer(buf, 4 * A._VIEW)
+    assert [getattr(d, n) for n, _ in A._Dims._fields_] == [31, 32, 33, 34, 35, 36, 1, 0, 0.25]
+    A._two_views(buf, 0, *range(40, 46))
+    v = A._View.from_buffer(buf, A._VIEW)
+    assert (v.data, v.token_stride, v.head_stride) == (43, 44, 45)
