@@ -13,9 +13,11 @@
 //      reads its 8 keys, lane m of it VE neighbouring channels of each, and the 8 x VE block is turned in
 //      registers while it is widened; tile c of the output then is channels m VE + c, and a
 //      lane ends with 4 VE neighbouring channels of one head.
-// Loads are hidden by the other waves of a SIMD: three of them, with registers for one set of keys each, measured
-// better than two that load 32 keys ahead (64 sequences of up to 8192 int8 tokens, 8 key heads of 128: 137 us
-// against 171).  The page numbers are read a step ahead.
+// All of a step's loads are issued before its first product, and are hidden by the other waves of a SIMD: three of
+// them up to head_dim 128, with registers for one set of keys each, measured better than two that load 32 keys ahead
+// (64 sequences of up to 8192 int8 tokens, 8 key heads of 128: 122 us, 4.6 TB/s, against 132); two above (32 sequences,
+// 4 key heads of 256: 45 us against 76 with one); one for a wide cache of fp32, whose keys take the registers.
+// The page numbers are read a step ahead, by the scalar unit.
 //
 // The long axis is split into chunks, one workgroup each; its waves take 32 keys in turn and join their
 // results in LDS.  With more than one chunk the partial results (maximum, sum, unnormalised output, fp32)
@@ -117,14 +119,13 @@ __device__ __forceinline__ void load_words(unsigned* w, const char* p) {
 
 // A workgroup is one (chunk, 16 heads of a key head, sequence).
 template <typename IO, int KV, int DP>
-__global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SSM_KV_IO ? 2 : 3) void attn_decode(DecodeArgs a) {
+__global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP > 128 ? 1 : 2) : DP > 128 ? 2 : 3) void attn_decode(DecodeArgs a) {
   constexpr bool BF = sizeof(IO) == 2;
   constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1;
   // K: pieces of KB bytes; 16, but 8 of 8-bit codes where a row may be that short
   constexpr int KB = CS == 1 && DP == 64 ? 8 : 16, KE = KB / CS, NK = DP / (4 * KE), KW = KB / 4;
   // V: VE channels of a lane, NB blocks of 16 VE channels
   constexpr int VE = CS == 4 || DP % 128 ? 4 : 8, NB = DP / (16 * VE), VW = VE * CS / 4;
-  constexpr bool HOLD_V = CS * DP < 1024;  // V's registers fit beside K's; if not, its rows are read as they are used
   __shared__ float wml[NW][COLS][2];
   extern __shared__ __attribute__((aligned(16))) float wo[];  // [NW][heads][16 VE]
   const int lane = threadIdx.x & 63, col = lane & 15, w4 = lane >> 4;
@@ -169,8 +170,7 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
 
     struct Keys {
       unsigned k[2][NK][KW];
-      unsigned v[HOLD_V ? NB : 1][HOLD_V ? 8 : 1][VW];
-      const char* vp;
+      unsigned v[NB][8][VW];
       f32x4 sk[2], sv[2];
     };
     // Pages of the two 16-key groups of a step (pages hold 16 tokens or more); -1 where there are no keys.
@@ -198,13 +198,11 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
           x.sv[t] = *reinterpret_cast<const f32x4*>(a.c.vs + rv + 4 * t);
         }
       }
-      x.vp = a.c.v + rv * row_bytes;
-      if constexpr (HOLD_V) {
+      const char* vp = a.c.v + rv * row_bytes;
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) load_words<VE * CS>(x.v[n][j], x.vp + j * row_bytes + voff[n]);
-      }
+        for (int j = 0; j < 8; ++j) load_words<VE * CS>(x.v[n][j], vp + j * row_bytes + voff[n]);
     };
     const auto work = [&](Keys& x, int step, int p0, int p1) {
       f32x4 s[2] = {};
@@ -238,7 +236,6 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
         s[t] *= a.scale_log2;
       }
       const bool whole = step * STEP + STEP <= len && p0 >= 0 && p0 < pages && p1 >= 0 && p1 < pages;
-      unsigned unseen = 0;
       if (!whole) {  // what lies in unseen places counts for nothing, whatever it holds
         const int p = w4 & 2 ? p1 : p0, seen = p >= 0 && p < pages ? len - step * STEP - 8 * w4 : 0;
 #pragma unroll
@@ -246,14 +243,10 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
           const bool in = j < seen;
           s[j / 4][j % 4] = in ? s[j / 4][j % 4] : -INFINITY;
           if constexpr (KV != SSM_KV_IO) x.sv[j / 4][j % 4] = in ? x.sv[j / 4][j % 4] : 0.0f;
-          if constexpr (HOLD_V) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
-              for (int w = 0; w < VW; ++w) x.v[n][j][w] = in ? x.v[n][j][w] : 0u;
-          } else {
-            unseen |= in ? 0u : 1u << j;
-          }
+            for (int w = 0; w < VW; ++w) x.v[n][j][w] = in ? x.v[n][j][w] : 0u;
         }
       }
       float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
@@ -320,19 +313,11 @@ __global__ __launch_bounds__(NW * 64, DP > 128 ? 1 : sizeof(IO) == 4 && KV == SS
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            unsigned own[VW];
-            if constexpr (!HOLD_V) {
-              load_words<VE * CS>(own, x.vp + j * row_bytes + voff[n]);
-#pragma unroll
-              for (int w = 0; w < VW; ++w) own[w] = unseen >> j & 1 ? 0u : own[w];
-            }
-            const unsigned* v = HOLD_V ? x.v[HOLD_V ? n : 0][HOLD_V ? j : 0] : own;
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int c = 0; c < VE; ++c)
-              o[n * VE + c] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(v, c), s[j / 4][j % 4],
+              o[n * VE + c] = __builtin_amdgcn_mfma_f32_16x16x4f32(element_f32<KV, CS>(x.v[n][j], c), s[j / 4][j % 4],
                                                                    o[n * VE + c], 0, 0, 0);
-          }
       }
     };
 
