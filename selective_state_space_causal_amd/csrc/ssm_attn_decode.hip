@@ -64,10 +64,6 @@ __device__ __forceinline__ int share_of(const DecodeArgs& a, int steps) {
   return max((steps + a.chunks - 1) / a.chunks, MIN_SHARE);
 }
 
-// The two 16-bit halves of a and b as pairs (a.lo, b.lo) and (a.hi, b.hi).
-__device__ __forceinline__ unsigned pair_lo(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ __forceinline__ unsigned pair_hi(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-
 // Code j of a word as fp32.
 template <int KV>
 __device__ __forceinline__ float widen_one(unsigned w, int j) {

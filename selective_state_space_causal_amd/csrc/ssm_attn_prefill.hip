@@ -1,10 +1,6 @@
 // ssm_attn_prefill.hip -- ssm_attn_prefill of include/ssm_attn.h: softmax attention over packed
 // prompts, one pass over the keys with the running maximum and sum of each row's softmax.
 //
-// Rows.  The query heads that share a key head are packed into the rows of a tile: row r of a sequence
-// is token r / G, query head kv_head * G + r % G (G = query heads per key head).  A key tile is then
-// read once for all G heads, and a short sequence fills a tile G times better.
-//
 // Products.  Scores are computed transposed, S^T = K Q^T, with 32x32 matrix instructions: a lane then
 // holds scores of ONE row (column lane & 31), 16 keys of every 32, the other 16 being in lane ^ 32.
 // Row maxima and sums are therefore taken inside a lane, with a single exchange of the two halves, and
@@ -12,88 +8,11 @@
 // order of the keys inside a product is free as long as V is read in the same order.  V's operand needs
 // keys along a lane's registers, and V is stored with channels along a row: bf16 uses the LDS read that
 // transposes 16-bit elements.
-#include "ssm_attn.h"
+#include "ssm_attn_prefill.h"
 
 namespace ssm {
 namespace attn {
 namespace {
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
-
-struct PrefillArgs {
-  View q, k, v, out;
-  float* lse;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
-  int B, Tq, Tk, Hq, Hkv, G, D;
-  int causal;
-  float scale_log2;  // scale * log2(e)
-};
-
-// Inclusive prefix sum over the wave's lanes.
-__device__ __forceinline__ int wave_scan(int x) {
-  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // the 16 lanes of a row: 1, 2, 4, 8 to the right
-  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row 0's sum into row 1, row 2's into 3
-  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // the lower half's into the upper half
-  return x;
-}
-
-struct Work {
-  int tile, tiles;     // of the sequence's rows
-  int q0, lq, k0, lk;  // its queries and keys
-};
-
-// The same value, of which the compiler knows nothing: what is computed from it stays where it stands, instead of
-// being kept in registers through the loop over keys, which needs them all.
-__device__ __forceinline__ int here(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
-// (q0, lq, k0, lk) of sequence b; empty past the last.
-__device__ __forceinline__ int4 bounds(const PrefillArgs& a, int b) {
-  int4 s = {0, 0, 0, 0};
-  if (b < a.B) {
-    s.x = min(max(a.cu_q[b], 0), a.Tq);
-    s.y = max(min(a.cu_q[b + 1], a.Tq) - s.x, 0);
-    s.z = min(max(a.cu_k[b], 0), a.Tk);
-    s.w = max(min(a.cu_k[b + 1], a.Tk) - s.z, 0);
-  }
-  return s;
-}
-
-__device__ __forceinline__ int tiles_of(const PrefillArgs& a, int QT, int lq) {
-  return (int)(((unsigned)(lq * a.G) + QT - 1) / QT);
-}
-
-// The sequence and tile that hold tile `idx` of the packed batch (false past the end).  Each wave finds
-// it by itself: 64 sequences at a time, a prefix sum of their tile counts over the lanes.
-__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int QT, int64_t idx, Work& w) {
-  const int lane = threadIdx.x & 63;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int4 q = bounds(a, b0 + lane);
-    const int n = tiles_of(a, QT, q.y), incl = wave_scan(n);
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    if (idx < base + total) {
-      const int want = (int)(idx - base);
-      const int at = __ffsll((unsigned long long)__ballot(incl > want)) - 1;
-      w.tiles = __builtin_amdgcn_readlane(n, at);
-      w.tile = want - (__builtin_amdgcn_readlane(incl, at) - w.tiles);
-      w.q0 = __builtin_amdgcn_readlane(q.x, at);
-      w.lq = __builtin_amdgcn_readlane(q.y, at);
-      w.k0 = __builtin_amdgcn_readlane(q.z, at);
-      w.lk = __builtin_amdgcn_readlane(q.w, at);
-      return true;
-    }
-    base += total;
-  }
-  return false;
-}
 
 // Tile `idx` in the order of falling work (key tiles of KT): up to 64 sequences, one a lane (q: its bounds).  The
 // tiles with at least c key tiles are counted for a c found by bisection.  top: a c that no tile from here on exceeds,
@@ -129,16 +48,6 @@ __device__ __forceinline__ bool find_sorted(const PrefillArgs& a, int QT, int KT
   w.k0 = __builtin_amdgcn_readlane(q.z, at);
   w.lk = __builtin_amdgcn_readlane(q.w, at);
   return true;
-}
-
-// The two halves' values of one row joined: max / sum over lane and lane ^ 32.
-__device__ __forceinline__ float half_max(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float half_sum(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // A key tile in LDS: rows of CH 16-byte chunks, whose places in the row are exchanged by the row
@@ -426,205 +335,27 @@ void attn_prefill(PrefillArgs a) {
   }
 }
 
-constexpr int F32_NW = 4;
-
-// fp32, on the fp32 matrix instructions (a sixteenth of bf16's rate, which bounds it): a wave reads its
-// operands straight from memory, no LDS.  A workgroup has 32 rows; its waves take 32 keys in turn, so
-// that few rows still fill the chip, and join their results at the end.  K's channels may come in any
-// order if Q's do too: 16-byte reads of both.  Lane m of V's operand holds VE neighbouring channels of
-// one key, for VE output tiles.  A step's V is loaded while its scores are computed, the next step's K while
-// its output is.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const char* p, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, bytes, 0x00020000);
-}
-
-// Pieces 32 i + 16 half of a lane's row (at: its first byte); the first one again past D.
-template <int NQ>
-__device__ __forceinline__ void load_k32(f32x4* k, const char* p, int bytes, int at, int D) {
-  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
-#pragma unroll
-  for (int i = 0; i < NQ; ++i)
-    k[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, i * 8 < D ? i * 32 : 0, 0));
-}
-
-template <int NB, int VE>
-__device__ __forceinline__ void load_v32(float (*v)[NB * VE], const char* p, int bytes, const int* at, int ts) {
-  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int row = (8 * (i / 4) + i % 4) * ts;
-      float* x = v[i] + n * VE;
-      if constexpr (VE == 4) {
-        const f32x4 t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at[n], row, 0));
-        x[0] = t[0], x[1] = t[1], x[2] = t[2], x[3] = t[3];
-      } else if constexpr (VE == 2) {
-        const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at[n], row, 0));
-        x[0] = __uint_as_float(t[0]), x[1] = __uint_as_float(t[1]);
-      } else {
-        x[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at[n], row, 0));
-      }
-    }
-}
-
-template <int DP>
-__global__ __launch_bounds__(F32_NW * 64, 1) void attn_prefill_f32(PrefillArgs a) {
-  constexpr int NW = F32_NW, QT = 32, NQ = DP / 8;
-  constexpr int VE = DP % 128 == 0 ? 4 : DP % 64 == 0 ? 2 : 1, NB = DP / (32 * VE);  // channels of a lane, blocks of 32 VE
-  constexpr bool QREG = DP <= 128;  // Q in registers beside a step's K, V and output, else in LDS
-  __shared__ float wml[NW][32][2];
-  __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
-  __shared__ __attribute__((aligned(16))) f32x4 ql[QREG ? 1 : NQ][64];
-  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kts = (int)a.k.ts, vts = (int)a.v.ts;
-  int vo[NB];
-#pragma unroll
-  for (int n = 0; n < NB; ++n) vo[n] = 4 * half * vts + ((n * 32 + col) * VE < a.D ? (n * 32 + col) * VE * 4 : 0);
-
-  const int h = blockIdx.x;
-  Work w;
-  for (int64_t idx = blockIdx.y; find_tile(a, QT, idx, w); idx += gridDim.y) {
-    const int tile = w.tiles - 1 - w.tile;
-    const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
-    const int rows = lq * a.G, r0 = tile * QT;
-    const int r = r0 + col, rc = min(r, rows - 1);
-    const int tok = rc / a.G, g = rc - tok * a.G;
-    const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
-    const int seen = seen_by(tok);
-    const int first = __builtin_amdgcn_readfirstlane(seen_by(r0 / a.G));
-    const int last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
-
-    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
-    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
-    // Bytes of a step's rows: past them, keys read as zeros (masked below).
-    const auto span = [&](int j0, int ts) { return (min(lk - j0, 32) - 1) * ts + a.D * 4; };
-    f32x4 kx[NQ];
-    int j0 = wave * 32;
-    if (j0 < last) load_k32<NQ>(kx, kp + (int64_t)j0 * a.k.ts, span(j0, kts), col * kts + half * 16, a.D);
-    f32x4 qf[QREG ? NQ : 1];
-    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
-    if constexpr (!QREG) __syncthreads();
-#pragma unroll
-    for (int i = QREG ? 0 : wave; i < NQ; i += QREG ? 1 : NW) {
-      const int e = (2 * i + half) * 4;
-      const f32x4 x = e < a.D ? *reinterpret_cast<const f32x4*>(qp + e * 4) : f32x4{};
-      if constexpr (QREG) qf[i] = x;
-      else ql[i][lane] = x;
-    }
-    if constexpr (!QREG) __syncthreads();
-    f32x16 o[NB * VE] = {};
-    float m = -INFINITY, l = 0.0f;
-
-    for (; j0 < last; j0 += NW * 32) {
-      float vx[16][NB * VE];
-      load_v32<NB, VE>(vx, vp + (int64_t)j0 * a.v.ts, span(j0, vts), vo, vts);
-      __builtin_amdgcn_sched_barrier(0);
-      f32x16 s = {};
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const f32x4 qx = QREG ? qf[QREG ? i : 0] : ql[QREG ? 0 : i][lane];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_32x32x2f32(kx[i][j], qx[j], s, 0, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      const int jn = j0 + NW * 32;
-      if (jn < last) load_k32<NQ>(kx, kp + (int64_t)jn * a.k.ts, span(jn, kts), col * kts + half * 16, a.D);
-      __builtin_amdgcn_sched_barrier(0);
-      if (j0 + 32 > first) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = j0 + 8 * (i / 4) + 4 * half + i % 4 < seen ? s[i] : -INFINITY;
-      }
-      float mx = m;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i] * a.scale_log2);
-      mx = half_max(mx);
-      const float mc = mx == -INFINITY ? 0.0f : mx, alpha = hw_exp2(m - mc);
-      m = mx;
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = hw_exp2(fmaf(s[i], a.scale_log2, -mc));
-        l += s[i];
-      }
-#pragma unroll
-      for (int c = 0; c < NB * VE; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int c = 0; c < NB * VE; ++c) o[c] = __builtin_amdgcn_mfma_f32_32x32x2f32(vx[i][c], s[i], o[c], 0, 0, 0);
-    }
-
-    // Join the waves, as the decode kernel does: one maximum, then sums in wave order.
-    l = half_sum(l);
-    __syncthreads();
-    if (half == 0) wml[wave][col][0] = m;
-    __syncthreads();
-    float top = wml[0][col][0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) top = fmaxf(top, wml[w][col][0]);
-    const float f = hw_exp2(m - (top == -INFINITY ? 0.0f : top));
-    if (half == 0) wml[wave][col][1] = l * f;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      constexpr int BC = 32 * VE;
-      if (n > 0) __syncthreads();
-      // rows of the product: channel lane m of V = 8 (i / 4) + 4 half + i % 4
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int c = 0; c < VE; ++c) wo[wave][col][(8 * (i / 4) + 4 * half + i % 4) * VE + c] = o[n * VE + c][i] * f;
-      __syncthreads();
-      for (int i = threadIdx.x; i < 32 * (BC / 4); i += NW * 64) {
-        const int row = i / (BC / 4), e = (i - row * (BC / 4)) * 4, rr = r0 + row;
-        if (n * BC + e >= a.D || rr >= rows) continue;
-        f32x4 y = {};
-        float sum = 0.0f, hm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          y += *reinterpret_cast<const f32x4*>(&wo[w][row][e]);
-          sum += wml[w][row][1];
-          hm = fmaxf(hm, wml[w][row][0]);
-        }
-        const int t = rr / a.G, head = h * a.G + rr - t * a.G;
-        *reinterpret_cast<f32x4*>(a.out.p + (int64_t)(q0 + t) * a.out.ts + (int64_t)head * a.out.hs + (n * BC + e) * 4) =
-            y * (sum > 0.0f ? 1.0f / sum : 0.0f);
-        if (a.lse && n == 0 && e == 0)
-          a.lse[(int64_t)(q0 + t) * a.Hq + head] = sum > 0.0f ? (hm + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
-      }
-    }
-  }
-}
-
-// Key heads and tiles (at most: the sum of ceil(rows / QT) over the sequences), heads first: the eight XCDs take
-// workgroups in turn, so that with eight heads each XCD's L2 holds the keys of one.
-dim3 tiles_grid(const PrefillArgs& a, int QT, int places) {
-  const int64_t tiles = (int64_t)a.Tq * a.G / QT + a.B;
-  int64_t most = places / a.Hkv;
-  most = most < 1 ? 1 : most > 65535 ? 65535 : most;
-  return dim3(a.Hkv, (unsigned)(tiles < most ? tiles : most));
-}
-
 template <int DP>
 void launch_bf16(PrefillArgs& a, hipStream_t s) {
   constexpr int NW = 4, KT = DP > 128 ? 32 : 64, PER_CU = DP > 192 ? 1 : 2;  // two buffers of K and V: 64 KB, two workgroups on a CU up to 128
   attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32, 256 * PER_CU), dim3(NW * 64), 0, s>>>(a);
 }
 
-template <int DP>
-void launch_f32(PrefillArgs& a, hipStream_t s) {
-  attn_prefill_f32<DP><<<tiles_grid(a, 32, INT32_MAX), dim3(F32_NW * 64), 0, s>>>(a);
+// Few rows: the keys split over waves, so that more of the chip is at work and a row's way along the keys is shorter
+// (8 query and 2 key heads of 128: 1000 tokens 19 us against 25, 2000 38 against 43).  With more tiles of rows the
+// keys, read again for every 32 rows, cost more than that saves (32 and 8 heads: 500 tokens 21 against 16.5).
+bool few_rows(const PrefillArgs& a) {
+  const int64_t work = tiles_at_most(a, 128) * a.Hkv;
+  return work <= 64 || (work <= 128 && a.Tk / a.B >= 1024);
 }
 
 hipError_t launch(PrefillArgs& a, bool bf16, hipStream_t s) {
-  if (a.D <= 64) bf16 ? launch_bf16<64>(a, s) : launch_f32<64>(a, s);
-  else if (a.D <= 96) bf16 ? launch_bf16<96>(a, s) : launch_f32<96>(a, s);
-  else if (a.D <= 128) bf16 ? launch_bf16<128>(a, s) : launch_f32<128>(a, s);
-  else if (a.D <= 192) bf16 ? launch_bf16<192>(a, s) : launch_f32<192>(a, s);
-  else bf16 ? launch_bf16<256>(a, s) : launch_f32<256>(a, s);
+  if (!bf16 || few_rows(a)) launch_split(a, bf16, s);
+  else if (a.D <= 64) launch_bf16<64>(a, s);
+  else if (a.D <= 96) launch_bf16<96>(a, s);
+  else if (a.D <= 128) launch_bf16<128>(a, s);
+  else if (a.D <= 192) launch_bf16<192>(a, s);
+  else launch_bf16<256>(a, s);
   return hipGetLastError();
 }
 

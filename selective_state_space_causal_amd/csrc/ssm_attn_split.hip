@@ -1,0 +1,246 @@
+// ssm_attn_split.hip -- prompt attention (ssm_attn_prefill of include/ssm_attn.h) with the keys split over a
+// workgroup's waves: all of fp32, and bf16 calls of few rows.
+//
+// A workgroup has 32 rows; its waves take 32 keys in turn and join their results at the end, so that few rows still
+// fill the chip and a row's way along the keys is a fraction of their number.  A wave reads its operands straight from
+// memory, no LDS.  Scores are computed transposed, S^T = K Q^T, with 32x32 matrix instructions: a lane holds 16 scores of
+// ONE row (column lane & 31), the other 16 being in lane ^ 32, in the order that the right operand of
+// O^T = V^T P^T wants.  K's channels may come in any order if Q's do too: 16-byte reads of both.  Lane m of V's
+// operand holds VE neighbouring channels of its keys, for VE output tiles (bf16: turned in registers into each
+// channel's keys).  A step's V is loaded while its scores are computed, the next step's K while its output is.
+// Past a sequence's end keys are read as zeros (the buffer's bounds) and masked.
+//
+// fp32 runs on the fp32 matrix instructions, a sixteenth of bf16's rate, which bounds it.
+#include "ssm_attn_prefill.h"
+
+namespace ssm {
+namespace attn {
+namespace {
+
+typedef unsigned u32;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const char* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, bytes, 0x00020000);
+}
+
+// 16-byte pieces 2 i + half of a lane's row (at `row`).  Past the row's end a piece of it that lies within: it meets zeros
+// of Q.  Both pieces of an i lie within or neither does, but for the last one of bf16 rows of 16 n + 8 values.
+template <int NQ, int ES>
+__device__ __forceinline__ void load_k(u32x4* k, const char* p, int bytes, int row, int half, int row_bytes) {
+  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
+  const int at = row + (ES == 4 || row_bytes > 16 ? half * 16 : 0);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const bool edge = ES == 2 && i * 32 < row_bytes && i * 32 + 16 == row_bytes;  // the upper half's is past the end
+    const int v = edge ? row + (half ? 0 : i * 32) : at, s = !edge && i * 32 < row_bytes ? i * 32 : 0;
+    k[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, s, 0));
+  }
+}
+
+// VW words of 16 keys (the ones of score i in a lane's order) of each of NB blocks.
+template <int NB, int VW>
+__device__ __forceinline__ void load_v(u32 (*v)[NB][VW], const char* p, int bytes, const int* at, int ts) {
+  const __amdgpu_buffer_rsrc_t r = rows_view(p, bytes);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int row = (8 * (i / 4) + i % 4) * ts;
+      if constexpr (VW == 4) {
+        const u32x4 t = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at[n], row, 0));
+        v[i][n][0] = t[0], v[i][n][1] = t[1], v[i][n][2] = t[2], v[i][n][3] = t[3];
+      } else if constexpr (VW == 2) {
+        const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at[n], row, 0));
+        v[i][n][0] = t[0], v[i][n][1] = t[1];
+      } else {
+        v[i][n][0] = __builtin_amdgcn_raw_buffer_load_b32(r, at[n], row, 0);
+      }
+    }
+}
+
+template <typename IO, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
+  constexpr bool BF = sizeof(IO) == 2;
+  constexpr int ES = sizeof(IO), QT = 32, NQ = DP * ES / 32;
+  // Channels of a lane, blocks of 32 VE, words of a lane's channels of one key
+  constexpr int VE = DP % 128 == 0 ? 4 : DP % 64 == 0 ? 2 : 1, NB = DP / (32 * VE), VW = VE * ES / 4;
+  static_assert(VW >= 1, "bf16 takes two channels at a time");
+  constexpr bool QREG = DP * ES <= 512;  // Q in registers beside a step's K, V and output, else in LDS
+  __shared__ float wml[NW][32][2];
+  __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
+  __shared__ __attribute__((aligned(16))) u32x4 ql[QREG ? 1 : NQ][64];
+  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kts = (int)a.k.ts, vts = (int)a.v.ts, row_bytes = a.D * ES;
+  int vo[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) vo[n] = 4 * half * vts + ((n * 32 + col) * VE < a.D ? (n * 32 + col) * VE * ES : 0);
+
+  const int h = blockIdx.x;
+  Work w;
+  for (int64_t idx = blockIdx.y; find_tile(a, QT, idx, w); idx += gridDim.y) {
+    const int tile = w.tiles - 1 - w.tile;  // causal: the tiles with the most keys first
+    const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
+    const int rows = lq * a.G, r0 = tile * QT;
+    const int r = r0 + col, rc = min(r, rows - 1);
+    const int tok = rc / a.G, g = rc - tok * a.G;
+    const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
+    const int seen = seen_by(tok);
+    const int first = __builtin_amdgcn_readfirstlane(seen_by(r0 / a.G));
+    const int last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
+
+    const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
+    const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
+    const auto span = [&](int j0, int ts) { return (min(lk - j0, 32) - 1) * ts + row_bytes; };  // bytes of a step's rows
+    u32x4 kx[NQ];
+    int j0 = wave * 32;
+    if (j0 < last) load_k<NQ, ES>(kx, kp + (int64_t)j0 * a.k.ts, span(j0, kts), col * kts, half, row_bytes);
+    u32x4 qf[QREG ? NQ : 1];
+    const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
+    if constexpr (!QREG) __syncthreads();
+#pragma unroll
+    for (int i = QREG ? 0 : wave; i < NQ; i += QREG ? 1 : NW) {
+      const int e = (2 * i + half) * 16;
+      const u32x4 x = e < row_bytes ? *reinterpret_cast<const u32x4*>(qp + e) : u32x4{0, 0, 0, 0};
+      if constexpr (QREG) qf[i] = x;
+      else ql[i][lane] = x;
+    }
+    if constexpr (!QREG) __syncthreads();
+    f32x16 o[NB * VE] = {};
+    float m = -INFINITY, l = 0.0f;
+
+    for (; j0 < last; j0 += NW * 32) {
+      u32 vx[16][NB][VW];
+      load_v<NB, VW>(vx, vp + (int64_t)j0 * a.v.ts, span(j0, vts), vo, vts);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x16 s = {};
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const u32x4 qx = QREG ? qf[QREG ? i : 0] : ql[QREG ? 0 : i][lane];
+        if constexpr (BF) {
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kx[i]), __builtin_bit_cast(bf16x8, qx), s,
+                                                      0, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kx[i][j]), __uint_as_float(qx[j]), s, 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const int jn = j0 + NW * 32;
+      if (jn < last) load_k<NQ, ES>(kx, kp + (int64_t)jn * a.k.ts, span(jn, kts), col * kts, half, row_bytes);
+      __builtin_amdgcn_sched_barrier(0);
+      if (j0 + 32 > first) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = j0 + 8 * (i / 4) + 4 * half + i % 4 < seen ? s[i] : -INFINITY;
+      }
+      float mx = m;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i] * a.scale_log2);
+      mx = half_max(mx);
+      const float mc = mx == -INFINITY ? 0.0f : mx, alpha = hw_exp2(m - mc);
+      m = mx;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = hw_exp2(fmaf(s[i], a.scale_log2, -mc));
+        l += s[i];
+      }
+#pragma unroll
+      for (int c = 0; c < NB * VE; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
+      if constexpr (BF) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
+          u32x4 pf;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < VE; ++c) {
+              u32x4 vf;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const u32 x = vx[8 * t + 2 * i][n][c / 2], y = vx[8 * t + 2 * i + 1][n][c / 2];
+                vf[i] = c % 2 == 0 ? pair_lo(x, y) : pair_hi(x, y);
+              }
+              f32x16& oc = o[n * VE + c];
+              oc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf), oc,
+                                                           0, 0, 0);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < VE; ++c)
+              o[n * VE + c] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(vx[i][n][c]), s[i], o[n * VE + c], 0, 0, 0);
+      }
+    }
+
+    // Join the waves: their outputs on one maximum, then sums in wave order.
+    l = half_sum(l);
+    __syncthreads();
+    if (half == 0) wml[wave][col][0] = m;
+    __syncthreads();
+    float top = wml[0][col][0];
+#pragma unroll
+    for (int x = 1; x < NW; ++x) top = fmaxf(top, wml[x][col][0]);
+    const float f = hw_exp2(m - (top == -INFINITY ? 0.0f : top));
+    if (half == 0) wml[wave][col][1] = l * f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      constexpr int BC = 32 * VE;
+      if (n > 0) __syncthreads();
+      // rows of the product: channel lane m of V = 8 (i / 4) + 4 half + i % 4
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int c = 0; c < VE; ++c) wo[wave][col][(8 * (i / 4) + 4 * half + i % 4) * VE + c] = o[n * VE + c][i] * f;
+      __syncthreads();
+      for (int i = threadIdx.x; i < 32 * (BC / 4); i += NW * 64) {
+        const int row = i / (BC / 4), e = (i - row * (BC / 4)) * 4, rr = r0 + row;
+        if (n * BC + e >= a.D || rr >= rows) continue;
+        f32x4 y = {};
+        float sum = 0.0f, hm = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < NW; ++x) {
+          y += *reinterpret_cast<const f32x4*>(&wo[x][row][e]);
+          sum += wml[x][row][1];
+          hm = fmaxf(hm, wml[x][row][0]);
+        }
+        y *= sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int t = rr / a.G, head = h * a.G + rr - t * a.G;
+        char* op = a.out.p + (int64_t)(q0 + t) * a.out.ts + (int64_t)head * a.out.hs + (n * BC + e) * ES;
+        if constexpr (BF) *reinterpret_cast<u32x2*>(op) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        else *reinterpret_cast<f32x4*>(op) = y;
+        if (a.lse && n == 0 && e == 0)
+          a.lse[(int64_t)(q0 + t) * a.Hq + head] = sum > 0.0f ? (hm + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+}
+
+// Waves of a workgroup: eight, two a SIMD, where registers allow.
+template <typename IO, int DP>
+void launch_dp(const PrefillArgs& a, hipStream_t s) {
+  constexpr int NW = sizeof(IO) == 2 && DP <= 128 ? 8 : 4;
+  attn_split<IO, DP, NW><<<tiles_grid(a, 32, INT32_MAX), dim3(NW * 64), 0, s>>>(a);
+}
+
+}  // namespace
+
+void launch_split(const PrefillArgs& a, bool bf16, hipStream_t s) {
+  if (a.D <= 64) bf16 ? launch_dp<bf16_t, 64>(a, s) : launch_dp<float, 64>(a, s);
+  else if (a.D <= 96 && !bf16) launch_dp<float, 96>(a, s);
+  else if (a.D <= 128) bf16 ? launch_dp<bf16_t, 128>(a, s) : launch_dp<float, 128>(a, s);
+  else if (a.D <= 192) bf16 ? launch_dp<bf16_t, 192>(a, s) : launch_dp<float, 192>(a, s);
+  else bf16 ? launch_dp<bf16_t, 256>(a, s) : launch_dp<float, 256>(a, s);
+}
+
+}  // namespace attn
+}  // namespace ssm

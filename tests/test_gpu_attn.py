@@ -509,3 +509,51 @@ def test_attn_decode_many_chunks(io, kind):
     assert np.array_equal(np.isneginf(got), empty)
     assert np.all(np.abs(np.where(empty, 0, got) - np.where(empty, 0, rlse)) <= ltol + 2.0 ** -22 * np.abs(np.where(empty, 0, rlse)))
     assert torch.equal(ssm.attn_decode_step(q, c, table, n), out)
+
+
+@pytest.mark.parametrize("B", [64, 150])
+@pytest.mark.parametrize("case", [c for c in PREFILL if sum(c[0]) <= 300])
+def test_attn_prefill_edges_in_large_calls(case, B):
+    """The edges of PREFILL in calls of many sequences, which run another kernel than a few rows do: the sequences
+    in turn until there are B, as views of a packed projection, into a strided output."""
+    lens, past, Hq, Hkv, D, causal = case
+    n = len(lens)
+    lq = [lens[i % n] for i in range(B)]
+    lk = [max(lens[i % n] + past[i % n], 0) for i in range(B)]
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lq, lk))
+    Tq, Tk = int(cu_q[-1]), int(cu_k[-1])
+    x = rnd(50, Tq + 3, Hq + 2, D)
+    y = rnd(51, Tk + 3, 2 * Hkv + 1, D)
+    x[Tq:], y[Tk:] = float("nan"), float("nan")
+    q, k, v = x[:, 1:Hq + 1], y[:, :Hkv], y[:, Hkv + 1:]
+    xd, yd = x.to(DEV), y.to(DEV)
+    big = torch.full((Tq + 3, Hq + 1, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Tq + 3, Hq), 7.0, device=DEV)
+    out = ssm.attn_prefill(xd[:, 1:Hq + 1], yd[:, :Hkv], yd[:, Hkv + 1:], torch.from_numpy(cu_q).to(DEV),
+                           torch.from_numpy(cu_k).to(DEV), causal=causal, out=big[:, 1:], lse=lse)
+    ref = whole_sequences(f64(q)[:Tq], f64(k)[:Tk], f64(v)[:Tk], cu_q, cu_k, causal, D ** -0.5)
+    check_attn(out[:Tq], lse[:Tq], ref, "bf16", D, f"{case} x {B}")
+    assert torch.all(big[Tq:] == 3.0) and torch.all(big[:, 0] == 3.0) and torch.all(lse[Tq:] == 7.0)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([700], 8, 2, 128), ([90, 1500], 4, 4, 64), ([300] * 20, 8, 2, 128), ([7] * 90, 4, 1, 72)])
+def test_attn_prefill_graph_replays(lens, Hq, Hkv, D):
+    """A captured call replayed on new inputs in the same buffers against the eager call; one graph for the
+    kernel of few rows and one for the other."""
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(DEV)
+    x = torch.empty(sum(lens), Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    out = torch.empty(sum(lens), Hq, D, dtype=torch.bfloat16, device=DEV)
+    x.copy_(rnd(60, *x.shape).to(DEV))
+    ssm.attn_prefill(q, k, v, cu, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ssm.attn_prefill(q, k, v, cu, out=out)
+    for i in range(4):
+        x.copy_(rnd(61 + i, *x.shape).to(DEV))
+        out.zero_()
+        g.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(ssm.attn_prefill(q, k, v, cu), got), i
