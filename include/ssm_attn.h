@@ -40,9 +40,10 @@
  * the io dtype itself.
  *
  * head_dim is a multiple of 8 in [8, 256].  io dtypes: SSM_F32, SSM_BF16.  Products of bf16 inputs
- * run on the matrix cores with fp32 sums, and softmax weights are rounded to bf16 (2^-8 relative,
- * the size of the output's own rounding) for the product with v; fp32 inputs are multiplied in fp32
- * throughout.  Softmax maxima, sums and the partial results of a split are fp32.
+ * run on the matrix cores with fp32 sums; for the product with v, prompt attention rounds a softmax weight
+ * to bf16 (2^-8 relative, the size of the output's own rounding), and decode holds it as the sum of two bf16
+ * (2^-17).  fp32 inputs are multiplied in fp32 throughout.  Softmax maxima, sums and the partial results of a
+ * split are fp32.
  *
  * Conventions (ownership, ordering, errors before any HIP call, no allocation, no mutable global
  * state, no host synchronisation, the current device) as in ssm.h.  Index arrays (slots,

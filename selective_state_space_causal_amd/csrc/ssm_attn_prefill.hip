@@ -117,7 +117,7 @@ void attn_prefill(PrefillArgs a) {
   __syncthreads();
 
   const int h = blockIdx.x, places = gridDim.y, place = blockIdx.y;
-  int64_t dealt = 0;  // tiles dealt to all places before this round
+  int64_t dealt = 0;  // tiles dealt to all places so far
   bool forwards = true;
   int top = (int)(((unsigned)a.Tk + KT - 1) / KT);
   // The next tile of rows; false when there are no more.
