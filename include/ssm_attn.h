@@ -42,8 +42,9 @@
  * head_dim is a multiple of 8 in [8, 256].  io dtypes: SSM_F32, SSM_BF16.  Products of bf16 inputs
  * run on the matrix cores with fp32 sums; for the product with v, prompt attention rounds a softmax weight
  * to bf16 (2^-8 relative, the size of the output's own rounding), and decode holds it as the sum of two bf16
- * (2^-17).  fp32 inputs are multiplied in fp32 throughout.  Softmax maxima, sums and the partial results of a
- * split are fp32.
+ * (2^-17).  fp32 inputs keep fp32's accuracy throughout: prompt attention multiplies them as three bf16
+ * parts each (what is left out is below 2^-25 of a product; magnitudes up to 2^127), decode on the fp32
+ * matrix instructions.  Softmax maxima, sums and the partial results of a split are fp32.
  *
  * Conventions (ownership, ordering, errors before any HIP call, no allocation, no mutable global
  * state, no host synchronisation, the current device) as in ssm.h.  Index arrays (slots,

@@ -335,10 +335,19 @@ void attn_prefill(PrefillArgs a) {
   }
 }
 
+// Two buffers of K and V (64 KB up to 128 channels) and two waves a SIMD: two workgroups of four waves on a CU, or one of
+// eight.  Eight share each key tile between twice the rows, which long sequences gain by (2048 keys 2%, 8192 4%); shorter ones
+// lose more to tiles of rows that are partly empty (1024 keys 1%, 512 3%, 32 25%).
 template <int DP>
 void launch_bf16(PrefillArgs& a, hipStream_t s) {
-  constexpr int NW = 4, KT = DP > 128 ? 32 : 64, PER_CU = DP > 192 ? 1 : 2;  // two buffers of K and V: 64 KB, two workgroups on a CU up to 128
-  attn_prefill<DP, NW, KT><<<tiles_grid(a, NW * 32, 256 * PER_CU), dim3(NW * 64), 0, s>>>(a);
+  constexpr int KT = DP > 128 ? 32 : 64, PER_CU = DP > 192 ? 1 : 2;
+  if constexpr (DP <= 128) {
+    if (a.Tk / a.B >= 2048) {
+      attn_prefill<DP, 8, KT><<<tiles_grid(a, 256, 256), dim3(512), 0, s>>>(a);
+      return;
+    }
+  }
+  attn_prefill<DP, 4, KT><<<tiles_grid(a, 128, 256 * PER_CU), dim3(256), 0, s>>>(a);
 }
 
 // Few rows: the keys split over waves, so that more of the chip is at work and a row's way along the keys is shorter

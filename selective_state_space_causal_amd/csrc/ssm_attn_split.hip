@@ -10,7 +10,10 @@
 // channel's keys).  A step's V is loaded while its scores are computed, the next step's K while its output is.
 // Past a sequence's end keys are read as zeros (the buffer's bounds) and masked.
 //
-// fp32 runs on the fp32 matrix instructions, a sixteenth of bf16's rate, which bounds it.
+// fp32 operands are split into three bf16 each, x = h + m + l to 2^-27 of x (each the remainder of the last,
+// rounded), and multiplied as hh + hm + mh + mm + hl + lh: what is left out, ml + lm + ll, is below 2^-25 of a product,
+// half of what one fp32 rounding may be.  Six bf16 products take 3/8 of the time of the fp32 matrix instruction on the
+// same numbers (a sixteenth of bf16's rate).
 #include "ssm_attn_prefill.h"
 
 namespace ssm {
@@ -58,6 +61,38 @@ __device__ __forceinline__ void load_v(u32 (*v)[NB][VW], const char* p, int byte
     }
 }
 
+struct Three {
+  bf16x8 h, m, l;
+};
+__device__ __forceinline__ Three split(const float (&x)[8]) {
+  u32x4 t[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const u32 w = pack_bf16(a, b);
+      t[j][i] = w;
+      a -= __uint_as_float(w << 16), b -= __uint_as_float(w & 0xFFFF0000u);  // exact
+    }
+  }
+  return Three{__builtin_bit_cast(bf16x8, t[0]), __builtin_bit_cast(bf16x8, t[1]), __builtin_bit_cast(bf16x8, t[2])};
+}
+__device__ __forceinline__ Three split(u32x4 a, u32x4 b) {
+  const float x[8] = {__uint_as_float(a[0]), __uint_as_float(a[1]), __uint_as_float(a[2]), __uint_as_float(a[3]),
+                      __uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]), __uint_as_float(b[3])};
+  return split(x);
+}
+// The small terms first.
+__device__ __forceinline__ f32x16 product(const Three& a, const Three& b, f32x16 c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.l, b.h, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.h, b.l, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.m, b.m, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.m, b.h, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.h, b.m, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.h, b.h, c, 0, 0, 0);
+}
+
 template <typename IO, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
   constexpr bool BF = sizeof(IO) == 2;
@@ -68,7 +103,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
   constexpr bool QREG = DP * ES <= 512;  // Q in registers beside a step's K, V and output, else in LDS
   __shared__ float wml[NW][32][2];
   __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
-  __shared__ __attribute__((aligned(16))) u32x4 ql[QREG ? 1 : NQ][64];
+  __shared__ __attribute__((aligned(16))) u32x4 ql[QREG ? 1 : BF ? NQ : NQ / 2 * 3][64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kts = (int)a.k.ts, vts = (int)a.v.ts, row_bytes = a.D * ES;
@@ -95,17 +130,34 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
     u32x4 kx[NQ];
     int j0 = wave * 32;
     if (j0 < last) load_k<NQ, ES>(kx, kp + (int64_t)j0 * a.k.ts, span(j0, kts), col * kts, half, row_bytes);
-    u32x4 qf[QREG ? NQ : 1];
     const char* qp = a.q.p + (int64_t)(q0 + tok) * a.q.ts + (int64_t)(h * a.G + g) * a.q.hs;
+    const auto read_q = [&](int i) {
+      const int e = (2 * i + half) * 16;
+      return e < row_bytes ? *reinterpret_cast<const u32x4*>(qp + e) : u32x4{0, 0, 0, 0};
+    };
+    // Q: pieces as K's; of fp32, two pieces at a time in three parts
+    constexpr int NP = BF ? NQ : NQ / 2, PARTS = BF ? 1 : 3;
+    bf16x8 qf[QREG ? NP : 1][PARTS];
     if constexpr (!QREG) __syncthreads();
 #pragma unroll
-    for (int i = QREG ? 0 : wave; i < NQ; i += QREG ? 1 : NW) {
-      const int e = (2 * i + half) * 16;
-      const u32x4 x = e < row_bytes ? *reinterpret_cast<const u32x4*>(qp + e) : u32x4{0, 0, 0, 0};
-      if constexpr (QREG) qf[i] = x;
-      else ql[i][lane] = x;
+    for (int i = QREG ? 0 : wave; i < NP; i += QREG ? 1 : NW) {
+      bf16x8 x[PARTS];
+      if constexpr (BF) {
+        x[0] = __builtin_bit_cast(bf16x8, read_q(i));
+      } else {
+        const Three t = split(read_q(2 * i), read_q(2 * i + 1));
+        x[0] = t.h, x[1] = t.m, x[2] = t.l;
+      }
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        if constexpr (QREG) qf[i][j] = x[j];
+        else ql[i * PARTS + j][lane] = __builtin_bit_cast(u32x4, x[j]);
+      }
     }
     if constexpr (!QREG) __syncthreads();
+    const auto part = [&](int i, int j) {
+      return QREG ? qf[QREG ? i : 0][j] : __builtin_bit_cast(bf16x8, ql[QREG ? 0 : i * PARTS + j][lane]);
+    };
     f32x16 o[NB * VE] = {};
     float m = -INFINITY, l = 0.0f;
 
@@ -115,16 +167,11 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
       __builtin_amdgcn_sched_barrier(0);
       f32x16 s = {};
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const u32x4 qx = QREG ? qf[QREG ? i : 0] : ql[QREG ? 0 : i][lane];
-        if constexpr (BF) {
-          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kx[i]), __builtin_bit_cast(bf16x8, qx), s,
-                                                      0, 0, 0);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kx[i][j]), __uint_as_float(qx[j]), s, 0, 0, 0);
-        }
+      for (int i = 0; i < NP; ++i) {
+        if constexpr (BF)
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kx[i]), part(i, 0), s, 0, 0, 0);
+        else
+          s = product(split(kx[2 * i], kx[2 * i + 1]), Three{part(i, 0), part(i, 1), part(i, 2)}, s);
       }
       __builtin_amdgcn_sched_barrier(0);
       const int jn = j0 + NW * 32;
@@ -150,9 +197,9 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
       for (int c = 0; c < NB * VE; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
-      if constexpr (BF) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
+      for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
+        if constexpr (BF) {
           u32x4 pf;
 #pragma unroll
           for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
@@ -170,15 +217,20 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
               oc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf), oc,
                                                            0, 0, 0);
             }
-        }
-      } else {
+        } else {
+          float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+          for (int i = 0; i < 8; ++i) x[i] = s[8 * t + i];
+          const Three p = split(x);
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int c = 0; c < VE; ++c)
-              o[n * VE + c] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(vx[i][n][c]), s[i], o[n * VE + c], 0, 0, 0);
+            for (int c = 0; c < VE; ++c) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(vx[8 * t + i][n][c]);
+              o[n * VE + c] = product(split(x), p, o[n * VE + c]);
+            }
+        }
       }
     }
 

@@ -557,3 +557,16 @@ def test_attn_prefill_graph_replays(lens, Hq, Hkv, D):
         got = out.clone()
         torch.cuda.synchronize()
         assert torch.equal(ssm.attn_prefill(q, k, v, cu), got), i
+
+
+@pytest.mark.parametrize("lens,past,Hq,Hkv,D", [([2200, 3000], [0, 40], 12, 1, 64), ([2500], [700], 16, 2, 96), ([2304], [0], 24, 3, 128)])
+def test_attn_prefill_long_sequences(lens, past, Hq, Hkv, D):
+    """Sequences of more than 2048 keys."""
+    q, k, v, cu_q, cu_k = prefill_case(lens, past, Hq, Hkv, D, "bf16")
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    out = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), torch.from_numpy(cu_q).to(DEV), torch.from_numpy(cu_k).to(DEV), lse=lse)
+    ref = whole_sequences(f64(q), f64(k), f64(v), cu_q, cu_k, True, D ** -0.5)
+    o, rlse, mag, smax, qkmax = ref
+    tol, ltol = O.attention_tolerance(HALF["bf16"], HALF["bf16"], o, mag, smax, qkmax, D, 1 << 12)
+    close(out, o, tol, "long sequences")
+    assert np.all(np.abs(f64(lse) - rlse) <= ltol + 2.0 ** -22 * np.abs(rlse))
