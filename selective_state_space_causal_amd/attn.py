@@ -11,6 +11,7 @@ import ctypes
 import functools
 import math
 import struct
+import warnings
 from typing import Optional
 
 import torch
@@ -84,6 +85,16 @@ class _Calls:
 
 
 _calls = None
+_native = None  # the usual case of the calls below, natively (csrc/attn_binding.cpp); NotImplemented for any other
+
+
+class _NoNative:
+    """Every case goes through this file."""
+
+    @staticmethod
+    def _not_usual(*args):
+        return NotImplemented
+    rope = kv_write = kv_read = attn_prefill = attn_decode_step = _not_usual
 
 
 def _entry() -> _Calls:
@@ -91,6 +102,23 @@ def _entry() -> _Calls:
     if _calls is None:
         _calls = _Calls(_lib.load())
     return _calls
+
+
+def _bound():
+    global _native
+    if _native is None:
+        lib = _lib.load()
+        try:
+            from . import _attn_fast
+            _attn_fast.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+                "ssm_rope", "ssm_kv_write", "ssm_kv_read", "ssm_attn_prefill", "ssm_attn_decode_step",
+                "ssm_attn_decode_workspace_bytes")))
+            _native = _attn_fast
+        except ImportError as e:
+            warnings.warn(f"the attention calls' native binding is not built ({e}): small calls are slower; run "
+                          "selective_state_space_causal_amd/build.py")
+            _native = _NoNative
+    return _native
 
 
 _I32, _I64, _F32, _F64 = torch.int32, torch.int64, torch.float32, torch.float64
@@ -199,6 +227,10 @@ def rope(q, k, positions, freq, *, interleaved: bool = False, mscale: float = 1.
          stream=None):
     """ssm_rope: q [T, Hq, D] and k [T, Hkv, D] (or None) rotated by positions [T] int64; freq (and
     mscale) as rope_frequencies gives them.  Returns (q_out, k_out); pass q_out=q, k_out=k for in place."""
+    if stream is None:
+        r = (_native or _bound()).rope(q, k, positions, freq, interleaved, mscale, q_out, k_out)
+        if r is not NotImplemented:
+            return r
     call = _entry().rope
     T, Hq, D = shape = _three(q, "q")
     dev, dtype = q.device, q.dtype
@@ -238,7 +270,7 @@ class KVCache:
     tensors are the caller's; this holds them and their description."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "_desc", "address", "device", "kv_heads", "head_dim", "page_size", "pages",
-                 "io_only")
+                 "io_only", "index", "is_bf16")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4:
@@ -267,6 +299,8 @@ class KVCache:
         pages, heads, page_size, dim = shape
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, dim
         self.io_only = dtype if kind == KV_IO else None  # the io dtype that a cache of that dtype is tied to
+        self.index = dev.index
+        self.is_bf16 = None if kind != KV_IO else dtype == torch.bfloat16
         self._desc = desc = _Buffer()  # a _Cache
         _cache_fields(desc, 0, k.data_ptr(), v.data_ptr(), pks, pvs, pages, page_size, heads, dim, kind)
         self.address = ctypes.addressof(desc)
@@ -300,6 +334,11 @@ def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, 
     """ssm_kv_write: keys and values k, v [T, Hkv, D] into the cache rows slots [T] int64 (page *
     page_size + place; out of range: skipped).  With positions and freq the keys are rotated on the way, and q
     [T, Hq, D] too where given; a k_out tensor receives the rotated keys.  Returns q_out (None without q)."""
+    if stream is None:
+        r = (_native or _bound()).kv_write(k, v, cache.address, cache.index, cache.is_bf16, slots, q, positions, freq,
+                                           interleaved, mscale, q_out, k_out)
+        if r is not NotImplemented:
+            return r
     call = _entry().kv_write
     T = _three(k, "k")[0]
     dev, dtype = cache.device, k.dtype
@@ -345,13 +384,18 @@ def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, 
 def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream=None):
     """ssm_kv_read: the rows at slots [T] int64 as (k, v) [T, Hkv, D] in dtype (the cache's own, or bfloat16
     for the 8-bit types, where not given); slots out of range read as zeros."""
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else cache.io_only or torch.bfloat16
+    if stream is None and dtype in _IO:
+        r = (_native or _bound()).kv_read(cache.address, cache.index, cache.is_bf16, slots, dtype == torch.bfloat16, k_out,
+                                          v_out)
+        if r is not NotImplemented:
+            return r
     call = _entry().kv_read
     dev = cache.device
     if slots.dim() != 1:
         raise ValueError(f"slots must have one axis, got {tuple(slots.shape)}")
     T = slots.shape[0]
-    if dtype is None:
-        dtype = k_out.dtype if k_out is not None else cache.io_only or torch.bfloat16
     cache.check_io(dtype)
     if dtype not in _IO:
         raise TypeError(f"io tensors must be float32 or bfloat16, got {dtype}")
@@ -385,6 +429,10 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, *, causal: bool = True, scale: Option
     defaults to cu_q); causal lets its last query see all its keys, the one before one less, and so on.  scale
     defaults to 1 / sqrt(D).  A query that sees no key gives zeros.  Returns out [Tq, Hq, D]; an lse tensor
     [Tq, Hq] fp32 receives the log of the softmax sums."""
+    if stream is None:
+        r = (_native or _bound()).attn_prefill(q, k, v, cu_q, cu_q if cu_k is None else cu_k, causal, scale, out, lse)
+        if r is not NotImplemented:
+            return r
     call = _entry().attn_prefill
     Tq, Hq, D = shape = _three(q, "q")
     Tk, Hkv, _ = _three(k, "k")
@@ -429,6 +477,10 @@ def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] =
     among them: write it first).  table [B, width] int32: the pages of each sequence; lens [B] int32.  scale defaults
     to 1 / sqrt(D).  workspace: attn_decode_workspace_bytes() bytes, allocated where not given.  Returns out
     [B, Hq, D]; an lse tensor [B, Hq] fp32 receives the log of the softmax sums."""
+    if stream is None and workspace is None:
+        r = (_native or _bound()).attn_decode_step(q, cache.address, cache.index, cache.is_bf16, table, lens, scale, out, lse)
+        if r is not NotImplemented:
+            return r
     call = _entry().attn_decode_step
     B, Hq, D = _three(q, "q")
     dev, dtype = cache.device, q.dtype

@@ -1,4 +1,5 @@
-"""Build libssm.so (the C ABI of include/ssm.h) from csrc/*.hip for gfx950 with hipcc."""
+"""Build libssm.so (the C ABI of include/ssm.h) from csrc/*.hip for gfx950 with hipcc, and _attn_fast.so, the
+native half of attn.py, from csrc/attn_binding.cpp."""
 from __future__ import annotations
 
 import glob
@@ -21,6 +22,31 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 
 # hipBLASLt runs the projection GEMMs (csrc/ssm_proj.hip).
 LINK_LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
+
+
+# The native half of attn.py's binding (host code only; torch's headers).
+FAST = os.path.join(PKG, "_attn_fast.so")
+FAST_SRC = os.path.join(CSRC, "attn_binding.cpp")
+
+
+def build_binding(verbose: bool = False) -> str:
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
+    tmp = FAST + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           *[x for p in (*cpp_extension.include_paths(), "/opt/rocm/include") for x in ("-isystem", p)],
+           "-I", sysconfig.get_paths()["include"], FAST_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{os.path.realpath(lib)}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {FAST_SRC}:\n{r.stderr}")
+    os.replace(tmp, FAST)
+    return FAST
 
 
 def hipcc() -> str:
@@ -67,7 +93,10 @@ def build(verbose: bool = False, jobs: int = 8, sanitize: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+        binding = None if sanitize else ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
+        if binding is not None:
+            binding.result()
     out = SAN_LIB if sanitize else LIB
     tmp = out + ".tmp"
     if sanitize:

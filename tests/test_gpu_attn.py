@@ -570,3 +570,82 @@ def test_attn_prefill_long_sequences(lens, past, Hq, Hkv, D):
     tol, ltol = O.attention_tolerance(HALF["bf16"], HALF["bf16"], o, mag, smax, qkmax, D, 1 << 12)
     close(out, o, tol, "long sequences")
     assert np.all(np.abs(f64(lse) - rlse) <= ltol + 2.0 ** -22 * np.abs(rlse))
+
+
+# ---------------------------------------------------------------- the binding's two halves
+
+def test_native_and_python_bindings_agree(monkeypatch):
+    """Every call through the native half of the binding and through attn.py alone: the same bits, given outputs filled
+    and returned as they are, and the same refusals."""
+    from selective_state_space_causal_amd import attn as A
+    assert A._bound() is not A._NoNative, "the native binding is not built"
+    T, Hq, Hkv, D, page = 70, 6, 2, 64, 16
+    q, k, v = packed(70, T, Hq, Hkv, D, "bf16")
+    freq, m = ssm.rope_frequencies(32, scaling="yarn", factor=4.0, device=DEV)
+    pos, slots = torch.arange(T, device=DEV) * 3, torch.randperm(96, generator=torch.Generator().manual_seed(1))[:T].to(DEV)
+    cu = torch.tensor([0, 30, T], dtype=torch.int32, device=DEV)
+    table = torch.arange(6, dtype=torch.int32, device=DEV)[None].repeat(2, 1)
+    lens = torch.tensor([90, 0], dtype=torch.int32, device=DEV)
+    caches = {kind: new_cache(6, Hkv, page, D, kind, "bf16", fill=0) for kind in ("int8", "e4m3", "io")}
+    big = new_cache(600, Hkv, page, D, "e4m3", "bf16", fill=0)  # a table of several chunks: with a workspace
+    wide = torch.arange(600, dtype=torch.int32, device=DEV)[None]
+
+    def calls():
+        res = []
+        for inter in (False, True):
+            res += ssm.rope(q, k, pos, freq, interleaved=inter, mscale=m)
+        res.append(ssm.rope(q, None, pos, freq)[0])
+        qo, ko = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+        r = ssm.rope(q, k, pos, freq, q_out=qo, k_out=ko)
+        assert r[0] is qo and r[1] is ko
+        res += r
+        for c in caches.values():
+            c.k.view(torch.uint8).zero_()
+            assert ssm.kv_write(k, v, c, slots) is None
+            res.append(c.k.view(torch.uint8).clone())
+            res.append(ssm.kv_write(k, v, c, slots, q=q, positions=pos, freq=freq, mscale=m))
+            ko = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+            assert ssm.kv_write(k, v, c, slots, q=q, positions=pos, freq=freq, mscale=m, q_out=qo, k_out=ko) is qo
+            assert ssm.kv_write(k, v, c, slots, positions=pos, freq=freq, interleaved=True, k_out=ko) is None
+            res += [qo.clone(), ko, c.k.view(torch.uint8).clone(), c.v.view(torch.uint8).clone()]
+            res += ssm.kv_read(c, slots)
+            if c.io_only is None:
+                res += ssm.kv_read(c, slots, dtype=torch.float32)
+            lse = torch.empty(2, Hq, device=DEV)
+            res += [ssm.attn_decode_step(q[:2], c, table, lens, lse=lse), lse]
+            out = torch.empty(2, Hq, D, dtype=torch.bfloat16, device=DEV)
+            assert ssm.attn_decode_step(q[:2], c, table, lens, scale=0.3, out=out) is out
+            res.append(out)
+        res.append(ssm.attn_decode_step(q[:1], big, wide, torch.tensor([9000], dtype=torch.int32, device=DEV)))
+        lse = torch.empty(T, Hq, device=DEV)
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=DEV)
+        assert ssm.attn_prefill(q, k, v, cu, cu, causal=False, scale=0.2, out=out, lse=lse) is out
+        return [t.clone() for t in res] + [out, lse, ssm.attn_prefill(q, k, v, cu)]
+
+    def refusals():
+        c = caches["int8"]
+        bad = [lambda: ssm.rope(q, None, pos[:-1], freq), lambda: ssm.rope(q, None, pos, freq.float()), lambda: ssm.rope(q.half(), None, pos, freq),
+               lambda: ssm.rope(q, None, pos, freq, k_out=k), lambda: ssm.rope(q, None, pos.cpu(), freq), lambda: ssm.rope(q, k, pos, freq, q_out=k),
+               lambda: ssm.rope(q[..., ::2], None, pos, freq), lambda: ssm.rope(q, None, pos, freq, q_out=q[:, 1:]),
+               lambda: ssm.rope(q[..., :12].contiguous(), None, pos, freq[:4]), lambda: ssm.kv_write(k, v[:-1], c, slots),
+               lambda: ssm.kv_write(k, v, c, slots, q=q), lambda: ssm.kv_write(k, v, c, slots, positions=pos),
+               lambda: ssm.kv_write(k.float(), v, c, slots), lambda: ssm.kv_write(k.float(), v.float(), caches["io"], slots),
+               lambda: ssm.kv_write(k, v, c, slots.int()), lambda: ssm.kv_read(c, slots[:, None]), lambda: ssm.kv_read(c, slots, dtype=torch.float16),
+               lambda: ssm.kv_read(caches["io"], slots, dtype=torch.float32), lambda: ssm.kv_read(c, slots, k_out=k, v_out=k),
+               lambda: ssm.attn_prefill(q, k, v, cu.long()), lambda: ssm.attn_prefill(q, k, v[:-1], cu), lambda: ssm.attn_prefill(q, k, v, cu, scale=-1.0),
+               lambda: ssm.attn_prefill(q, k, v, cu, out=q), lambda: ssm.attn_prefill(q[:, :5], k, v, cu), lambda: ssm.attn_prefill(q, k, v, cu[:1]),
+               lambda: ssm.attn_decode_step(q[:2], c, table[:1], lens), lambda: ssm.attn_decode_step(q[:2], c, table, lens.long()),
+               lambda: ssm.attn_decode_step(q[:2], c, table[0], lens), lambda: ssm.attn_decode_step(q[:2].float(), caches["io"], table, lens),
+               lambda: ssm.attn_decode_step(q[:2, :, :32], c, table, lens), lambda: ssm.attn_decode_step(q[:2], c, table, lens, out=q[:2])]
+        res = []
+        for f in bad:
+            with pytest.raises((ValueError, TypeError, ssm.SsmError)) as e:
+                f()
+            res.append((type(e.value), str(e.value)))
+        return res
+
+    native, said = calls(), refusals()
+    monkeypatch.setattr(A, "_native", A._NoNative)
+    for i, (a, b) in enumerate(zip(native, calls())):
+        assert torch.equal(a, b), i
+    assert refusals() == said
