@@ -94,7 +94,7 @@ class _NoNative:
     @staticmethod
     def _not_usual(*args):
         return NotImplemented
-    rope = kv_write = kv_read = attn_prefill = attn_decode_step = _not_usual
+    describe = rope = kv_write = kv_read = attn_prefill = attn_decode_step = _not_usual
 
 
 def _entry() -> _Calls:
@@ -273,37 +273,35 @@ class KVCache:
                  "io_only", "index", "is_bf16")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
+        self._desc = desc = _Buffer()  # a _Cache
+        self.address = at = ctypes.addressof(desc)
+        r = (_native or _bound()).describe(at, k, v, k_scale, v_scale)
+        if r is NotImplemented:
+            r = self._describe(desc, k, v, k_scale, v_scale)
+        self.pages, self.kv_heads, self.page_size, self.head_dim, self.index, self.is_bf16 = r
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.io_only = None if self.is_bf16 is None else k.dtype  # the io dtype that a cache of that dtype is tied to
+
+    def _describe(self, desc, k, v, ks, vs):
+        """The checks, by name; fills desc."""
         if k.dim() != 4:
             raise ValueError(f"k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
         shape, dtype, dev = k.shape, k.dtype, k.device
         kind = _CODES.get(dtype, KV_IO)
-        ks, vs = k_scale, v_scale
         if kind == KV_IO:
             if dtype not in _IO:
                 raise TypeError(f"a cache holds float32, bfloat16, int8 or float8_e4m3fn, got {dtype}")
             if ks is not None or vs is not None:
                 raise ValueError("k_scale and v_scale: only the 8-bit types have scales")
-            pks = pvs = 0
         else:
-            rows = shape[:3]
-            if ks is None or vs is None or ks.shape != rows or vs.shape != rows or ks.dtype != _F32 or vs.dtype != _F32 or \
-                    ks.device != dev or vs.device != dev or not ks.is_contiguous() or not vs.is_contiguous():
-                self._refuse(ks, "k_scale", rows, _F32, dev)
-                self._refuse(vs, "v_scale", rows, _F32, dev)
-            pks, pvs = ks.data_ptr(), vs.data_ptr()
-        if not k.is_cuda or v is None or v.shape != shape or v.dtype != dtype or v.device != dev or \
-                not k.is_contiguous() or not v.is_contiguous():
-            self._refuse(k, "k", shape, dtype, dev)
-            self._refuse(v, "v", shape, dtype, dev)
-        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, ks, vs, dev
+            self._refuse(ks, "k_scale", shape[:3], _F32, dev)
+            self._refuse(vs, "v_scale", shape[:3], _F32, dev)
+        self._refuse(k, "k", shape, dtype, dev)
+        self._refuse(v, "v", shape, dtype, dev)
         pages, heads, page_size, dim = shape
-        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, dim
-        self.io_only = dtype if kind == KV_IO else None  # the io dtype that a cache of that dtype is tied to
-        self.index = dev.index
-        self.is_bf16 = None if kind != KV_IO else dtype == torch.bfloat16
-        self._desc = desc = _Buffer()  # a _Cache
-        _cache_fields(desc, 0, k.data_ptr(), v.data_ptr(), pks, pvs, pages, page_size, heads, dim, kind)
-        self.address = ctypes.addressof(desc)
+        _cache_fields(desc, 0, k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+                      pages, page_size, heads, dim, kind)
+        return pages, heads, page_size, dim, dev.index, None if kind != KV_IO else dtype == torch.bfloat16
 
     def _sizes(self):
         return self.pages, self.page_size, self.kv_heads, self.head_dim

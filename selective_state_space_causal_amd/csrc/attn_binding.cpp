@@ -256,6 +256,39 @@ PyObject* attn_decode_step(PyObject* const* a) {
   return out.defined() ? own(std::move(out)) : same(a[7]);
 }
 
+// describe(address of a cache's description, k, v, k_scale, v_scale): fills it and gives (pages, heads, page_size,
+// head_dim, device index, io_only_bf16)
+PyObject* describe(PyObject* const* a) {
+  Call c;
+  const at::Tensor* k = c.tensor(a[1]);
+  const at::Tensor* v = c.tensor(a[2]);
+  if (!c.ok || k->dim() != 4 || v->sizes() != k->sizes() || v->scalar_type() != k->scalar_type() || !k->is_contiguous() ||
+      !v->is_contiguous())
+    return not_usual();
+  const at::ScalarType t = k->scalar_type();
+  const bool codes = t == at::kChar || t == at::kFloat8_e4m3fn;
+  if (!codes && t != at::kFloat && t != at::kBFloat16) return not_usual();
+  const int64_t n[4] = {k->size(0), k->size(1), k->size(2), k->size(3)};
+  for (int i = 1; i < 4; ++i)
+    if (n[i] > INT32_MAX) return not_usual();
+  const at::Tensor* s[2] = {nullptr, nullptr};
+  for (int i = 0; i < 2; ++i) {
+    if (!codes) {
+      if (a[3 + i] != Py_None) return not_usual();
+      continue;
+    }
+    s[i] = c.tensor(a[3 + i]);
+    if (!c.ok || s[i]->scalar_type() != at::kFloat || s[i]->sizes() != k->sizes().slice(0, 3) || !s[i]->is_contiguous())
+      return not_usual();
+  }
+  *static_cast<ssm_kv_cache*>(PyLong_AsVoidPtr(a[0])) =
+      ssm_kv_cache{k->data_ptr(), v->data_ptr(), s[0] ? s[0]->mutable_data_ptr<float>() : nullptr,
+                   s[1] ? s[1]->mutable_data_ptr<float>() : nullptr, n[0], (int32_t)n[2], (int32_t)n[1], (int32_t)n[3],
+                   !codes ? SSM_KV_IO : t == at::kChar ? SSM_KV_I8 : SSM_KV_E4M3};
+  return Py_BuildValue("LLLLiO", (long long)n[0], (long long)n[1], (long long)n[2], (long long)n[3], c.device,
+                       codes ? Py_None : t == at::kBFloat16 ? Py_True : Py_False);
+}
+
 // bind(rope, kv_write, kv_read, attn_prefill, attn_decode_step, workspace_bytes): addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (nargs != 6) {
@@ -294,6 +327,7 @@ PyMethodDef method(const char* name, PyObject* (*f)(PyObject*, PyObject* const*,
   return PyMethodDef{name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method("bind", bind),
+                         method("describe", guarded<describe, 5>),
                          method("rope", guarded<rope, 8>),
                          method("kv_write", guarded<kv_write, 13>),
                          method("kv_read", guarded<kv_read, 7>),

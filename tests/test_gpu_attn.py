@@ -644,8 +644,24 @@ def test_native_and_python_bindings_agree(monkeypatch):
             res.append((type(e.value), str(e.value)))
         return res
 
-    native, said = calls(), refusals()
+    def described():
+        res = []
+        for c in (*caches.values(), big):
+            n = ssm.KVCache(c.k, c.v, c.k_scale, c.v_scale)
+            res.append([bytes(n._desc[:56]), *(getattr(n, x) for x in n.__slots__ if x not in ("_desc", "address"))])
+        c = caches["int8"]
+        for bad in ((c.k, c.v), (c.k, c.v[:2], c.k_scale, c.v_scale), (c.k, c.v, c.k_scale[:2], c.v_scale), (c.k[:, :, ::2], c.v[:, :, ::2]),
+                    (c.k, c.v, c.k_scale.double(), c.v_scale), (c.k.half(), c.v.half()), (c.k[0], c.v[0]), (c.k, c.v.cpu(), c.k_scale, c.v_scale),
+                    (caches["io"].k, caches["io"].v, c.k_scale, c.v_scale), (c.k, None, c.k_scale, c.v_scale)):
+            with pytest.raises((ValueError, TypeError)) as e:
+                ssm.KVCache(*bad)
+            res.append((type(e.value), str(e.value)))
+        return res
+
+    native, said, caches_native = calls(), refusals(), described()
     monkeypatch.setattr(A, "_native", A._NoNative)
+    for a, b in zip(caches_native, described()):
+        assert all(x is y if isinstance(x, torch.Tensor) else x == y for x, y in zip(a, b))
     for i, (a, b) in enumerate(zip(native, calls())):
         assert torch.equal(a, b), i
     assert refusals() == said
