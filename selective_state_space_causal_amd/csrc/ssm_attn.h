@@ -68,7 +68,7 @@ inline Span span(const void* p, int64_t bytes) {
 inline bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 constexpr int64_t MAX_TOKENS = INT32_MAX;
-// Largest strides in elements: 64 tokens of fp32 stay within 2^31 bytes (a tile's offsets are 32-bit), and
+// Largest strides in elements: 64 tokens of fp32 and 128 of bf16 stay within 2^31 bytes (a tile's offsets are 32-bit), and
 // all byte counts within int64.
 constexpr int64_t MAX_TOKEN_STRIDE = int64_t(1) << 23, MAX_HEAD_STRIDE = int64_t(1) << 48;
 

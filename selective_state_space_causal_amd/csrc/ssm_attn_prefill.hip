@@ -85,22 +85,23 @@ __device__ __forceinline__ void load_tile(const char* p, int ts, const int* off,
   }
 }
 
-// bf16: a workgroup of NW waves has 32 rows a wave; key tiles of KT keys go straight into one of two LDS buffers
-// while the other is worked on.  A workgroup takes tiles of rows in turn until there are none, and the key
+// bf16: a workgroup of NW waves has 32 rows for every KS waves, which share the keys: key tiles of KS times KT keys go
+// straight into one of two LDS buffers while the other is worked on, KT keys of them for each of the KS.  A workgroup takes tiles of rows in turn until there are none, and the key
 // tiles of one follow those of the last without a break: the next one's first keys are loaded under the
 // last key tile of this one, its queries under that tile's softmax, and the output is stored under what comes then.
 // Each head's tiles are dealt out in the order of falling work, forwards and backwards in turn.
-template <int DP, int NW, int KT>
+template <int DP, int NW, int KT, int KS>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(DP <= 192 ? 2 : 1, DP <= 192 ? 2 : 1)))
 void attn_prefill(PrefillArgs a) {
   typedef Tile<DP> L;
-  constexpr int QT = NW * 32, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH, AHEAD = 4;
-  constexpr int BYTES = KT * CH * 16, NL = KT * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
+  constexpr int RW = NW / KS, QT = RW * 32, KB = KT * KS, NS = KT / 32, ND = DP / 32, NQ = DP / 16, CH = L::CH, AHEAD = 4;
+  constexpr int BYTES = KB * CH * 16, NL = KB * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
   // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
   __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
   __shared__ int4 seqs[64];
+  __shared__ float2 stats[KS > 1 ? NW / 2 : 1][64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rw = wave % RW, kw = wave / RW;
   if (threadIdx.x < 64) seqs[threadIdx.x] = bounds(a, threadIdx.x);
 
   // This thread's pieces of a tile: the chunk of memory that belongs at each place (the first one past a row's end:
@@ -119,13 +120,13 @@ void attn_prefill(PrefillArgs a) {
   const int h = blockIdx.x, places = gridDim.y, place = blockIdx.y;
   int64_t dealt = 0;  // tiles dealt to all places so far
   bool forwards = true;
-  int top = (int)(((unsigned)a.Tk + KT - 1) / KT);
+  int top = (int)(((unsigned)a.Tk + KB - 1) / KB);
   // The next tile of rows; false when there are no more.
   const auto next = [&](Work& w) {
     const int64_t idx = dealt + (forwards ? place : places - 1 - place);
     dealt += places;
     forwards = !forwards;
-    if (a.B <= 64) return find_sorted(a, QT, KT, seqs[here(lane)], idx, top, w);
+    if (a.B <= 64) return find_sorted(a, QT, KB, seqs[here(lane)], idx, top, w);
     const bool found = find_tile(a, QT, idx, w);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) of its loads here, not under the products
     if (!found) return false;
@@ -139,17 +140,17 @@ void attn_prefill(PrefillArgs a) {
   const auto keys_of = [&](const Work& w) {  // of a tile's last row
     return seen_by(w, min(w.tile * QT + QT - 1, w.lq * a.G - 1) / a.G);
   };
-  // Keys j0 .. j0 + KT - 1 into a buffer; past the end the last key again (finite, masked below).
+  // Keys j0 .. j0 + KB - 1 into a buffer; past the end the last key again (finite, masked below).
   const auto load = [&](const Work& w, int j0, char* kt, char* vt) {
-    const int last = min(w.lk - 1 - j0, KT - 1);
-    load_tile<NL, NW, CH, KT>(a.k.p + (int64_t)(w.k0 + j0) * a.k.ts + (int64_t)h * a.k.hs, kts, koff, last, wave, kt);
-    load_tile<NL, NW, CH, KT>(a.v.p + (int64_t)(w.k0 + j0) * a.v.ts + (int64_t)h * a.v.hs, vts, voff, last, wave, vt);
+    const int last = min(w.lk - 1 - j0, KB - 1);
+    load_tile<NL, NW, CH, KB>(a.k.p + (int64_t)(w.k0 + j0) * a.k.ts + (int64_t)h * a.k.hs, kts, koff, last, wave, kt);
+    load_tile<NL, NW, CH, KB>(a.v.p + (int64_t)(w.k0 + j0) * a.v.ts + (int64_t)h * a.v.hs, vts, voff, last, wave, vt);
   };
   // Q as the right operand: a lane's row, in the order that the K reads below use.
   u32x4 qf[NQ];
   const auto load_q = [&](const Work& w) {
     const int c = here(lane), half = c >> 5;
-    const int r = min(w.tile * QT + wave * 32 + (c & 31), w.lq * a.G - 1), tok = r / a.G;
+    const int r = min(w.tile * QT + rw * 32 + (c & 31), w.lq * a.G - 1), tok = r / a.G;
     const char* qp = a.q.p + (int64_t)(w.q0 + tok) * a.q.ts + (int64_t)(h * a.G + r - tok * a.G) * a.q.hs;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -166,7 +167,7 @@ void attn_prefill(PrefillArgs a) {
   float m, l;
   const auto begin = [&] {
     const int rows = w.lq * a.G;
-    r0 = w.tile * QT + wave * 32;
+    r0 = w.tile * QT + rw * 32;
     seen = seen_by(w, min(r0 + col, rows - 1) / a.G);
     wave_first = seen_by(w, min(r0, rows - 1) / a.G);
     wave_last = r0 >= rows ? 0 : seen_by(w, min(r0 + 31, rows - 1) / a.G);
@@ -179,6 +180,9 @@ void attn_prefill(PrefillArgs a) {
   };
 
   const auto work = [&](const char* kt, const char* vt, bool last) {
+      const int j1 = j0 + kw * KT;  // this wave's keys of the tile
+      kt += kw * (KT * CH * 16);
+      vt += kw * (KT * CH * 16);
       // Operands are read some products ahead; the barriers hold each read in its place.
       const auto read_k = [&](int i) {
         return *reinterpret_cast<const bf16x8*>(kt + L::k_at(i / NQ * 32 + col, 2 * (i % NQ) + half));
@@ -198,12 +202,12 @@ void attn_prefill(PrefillArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);
       if (last) load_q(nx);
-      if (j0 + KT > wave_first) {  // some row of the wave does not see some key of the tile
+      if (j1 + KT > wave_first) {  // some row of the wave does not see some key of the tile
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int key = j0 + n * 32 + 8 * (i / 4) + 4 * half + i % 4;
+            const int key = j1 + n * 32 + 8 * (i / 4) + 4 * half + i % 4;
             s[n][i] = key < seen ? s[n][i] : -INFINITY;
           }
       }
@@ -277,6 +281,53 @@ void attn_prefill(PrefillArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     };
 
+  // KS waves' shares of the keys joined, in halves: the upper half of the shares goes to the lower through LDS (kc and vc,
+  // which it fills, in turns where it is larger), until the first has all.
+  const auto join = [&](char* kc, char* vc) {
+    constexpr int PIECES = BYTES / (NW / 2 * 1024);  // 16-byte pieces of a lane that a buffer holds, of NW / 2 waves
+#pragma unroll
+    for (int g = KS / 2; g >= 1; g /= 2) {
+      const bool gives = kw >= g && kw < 2 * g, takes = kw < g;
+      const int i = gives ? (kw - g) * RW + rw : wave;
+      if (gives) stats[i][lane] = make_float2(m, l);
+      float mine = 0.0f, theirs = 0.0f;
+#pragma unroll
+      for (int p0 = 0; p0 < ND * 4; p0 += 2 * PIECES) {
+        const auto piece = [&](int p) {
+          return reinterpret_cast<f32x4*>((p < PIECES ? kc + p * (NW / 2 * 1024) : vc + (p - PIECES) * (NW / 2 * 1024)) +
+                                          i * 1024 + lane * 16);
+        };
+        if (gives) {
+#pragma unroll
+          for (int p = p0; p < ND * 4 && p < p0 + 2 * PIECES; ++p) {
+            f32x4 x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = o[p / 4][p % 4 * 4 + j];
+            *piece(p - p0) = x;
+          }
+        }
+        __syncthreads();
+        if (takes) {
+          if (p0 == 0) {
+            const float2 other = stats[i][lane];
+            const float to = fmaxf(m, other.x), base = to == -INFINITY ? 0.0f : to;
+            mine = hw_exp2(m - base);
+            theirs = hw_exp2(other.x - base);
+            m = to;
+            l = l * mine + other.y * theirs;
+          }
+#pragma unroll
+          for (int p = p0; p < ND * 4 && p < p0 + 2 * PIECES; ++p) {
+            const f32x4 x = *piece(p - p0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[p / 4][p % 4 * 4 + j] = o[p / 4][p % 4 * 4 + j] * mine + x[j] * theirs;
+          }
+        }
+        __syncthreads();
+      }
+    }
+  };
+
   // The halves of a row hold 4 channels of 8 in turn: exchanged, each has whole 16-byte pieces.
   const auto store = [&] {
     l = half_sum(l);
@@ -305,20 +356,21 @@ void attn_prefill(PrefillArgs a) {
 
   // One key tile, from (kc, vc), while the next one comes into (kn, vn); false when all is done.
   const auto advance = [&](char* kc, char* vc, char* kn, char* vn) {
-    const bool ends = j0 + KT >= block_last;
-    if (!ends) load(w, j0 + KT, kn, vn);
+    const bool ends = j0 + KB >= block_last;
+    if (!ends) load(w, j0 + KB, kn, vn);
     if (fresh) more = next(nx), fresh = false;
     if (ends && more && keys_of(nx) > 0) load(nx, 0, kn, vn);
-    const bool sees = j0 < wave_last;
+    const bool sees = j0 + kw * KT < wave_last;
     if (sees) work(kc, vc, ends && more);
     if (!sees && ends && more) load_q(nx);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), said here: the compiler then waits for no load under the products
     __syncthreads();  // the reads of (kc, vc) are over, (kn, vn) and a next tile's Q are there
     if (!ends) {
-      j0 += KT;
+      j0 += KB;
       return true;
     }
-    store();
+    if constexpr (KS > 1) join(kc, vc);
+    if (kw == 0) store();
     if (!more) return false;
     w = nx;
     begin();
@@ -335,36 +387,67 @@ void attn_prefill(PrefillArgs a) {
   }
 }
 
-// Two buffers of K and V (64 KB up to 128 channels) and two waves a SIMD: two workgroups of four waves on a CU, or one of
-// eight.  Eight share each key tile between twice the rows, which long sequences gain by (2048 keys 2%, 8192 4%); shorter ones
-// lose more to tiles of rows that are partly empty (1024 keys 1%, 512 3%, 32 25%).
+// How many waves share a tile of rows.  With few tiles a row's way along the keys, or CUs without a second wave a SIMD, set
+// the time, and waves that share the keys of 128 or 64 rows are faster; with many, each key tile in LDS should serve as many
+// rows as possible.  n: tiles of 128 rows, over all key heads; k: keys of a sequence; both on the average, since the
+// lengths are on the device.  head_dim 128, us with (rows, shares) of
+//                                       32, 8   64, 4   128, 2   128, 1   256, 1
+//   n   64, k  1000 (8 and 2 heads)       18.2    17.3     21.1     23.9
+//   n  126, k  2000                       35.3    27.2     34.5     42.4
+//   n  258, k  4096                        111    56.7     66.6     78.1      103
+//   n  288, k   546 (4 to 8 heads)        48.1    31.9     24.5     27.2     32.1
+//   n  514, k  8192                        387     182      147      178      205
+//   n  592, k   562 (32 and 8 heads)      93.5    51.1     38.4     31.5     34.8
+//   n 1016, k  2000                        419     192      154      134      136
+//   n 2056, k  8192                       1534     697      542      514      491
+//   n  168, k   143                       20.6    15.4     11.6     11.0     14.7
+// Without the mask all tiles of rows are as long, and there is nothing to even out where the tiles are more than the CUs.
+enum Shares { Eight32, Four64, Two128, One128, One256 };
+Shares shares_of(const PrefillArgs& a) {
+  const int64_t n = tiles_at_most(a, 128) * a.Hkv, k = a.Tk / a.B;
+  // 32 rows straight from memory (ssm_attn_split.hip): rows of 64 channels, and those too wide for four shares, gain longer.
+  if (n <= (a.D > 192 ? 96 : 64) || (n <= (a.D > 64 && a.D <= 128 ? 96 : 128) && k >= 1024)) return Eight32;
+  if (k < 256) return One128;
+  if (n <= (a.causal ? 260 : 130) && (a.D <= 128 || a.D > 192)) return Four64;
+  if (n <= (!a.causal ? 260 : k >= 1024 ? 576 : 320) && a.D <= 192) return Two128;
+  return k >= 6000 && a.D <= 128 ? One256 : One128;
+}
+
+// Two buffers of K and V are 64 KB up to 128 channels for 64 keys, 128 KB for the 128 of two or four shares.  Two waves a
+// SIMD, one past 192 channels, whose four waves are two shares of 64 rows.
 template <int DP>
-void launch_bf16(PrefillArgs& a, hipStream_t s) {
+void launch_bf16(PrefillArgs& a, Shares how, hipStream_t s) {
   constexpr int KT = DP > 128 ? 32 : 64, PER_CU = DP > 192 ? 1 : 2;
   if constexpr (DP <= 128) {
-    if (a.Tk / a.B >= 2048) {
-      attn_prefill<DP, 8, KT><<<tiles_grid(a, 256, 256), dim3(512), 0, s>>>(a);
+    if (how == Four64) {
+      attn_prefill<DP, 8, 32, 4><<<tiles_grid(a, 64, 256), dim3(512), 0, s>>>(a);
+      return;
+    }
+    if (how == One256) {
+      attn_prefill<DP, 8, KT, 1><<<tiles_grid(a, 256, 256), dim3(512), 0, s>>>(a);
       return;
     }
   }
-  attn_prefill<DP, 4, KT><<<tiles_grid(a, 128, 256 * PER_CU), dim3(256), 0, s>>>(a);
-}
-
-// Few rows: the keys split over waves, so that more of the chip is at work and a row's way along the keys is shorter
-// (8 query and 2 key heads of 128: 1000 tokens 19 us against 25, 2000 38 against 43).  With more tiles of rows the
-// keys, read again for every 32 rows, cost more than that saves (32 and 8 heads: 500 tokens 21 against 16.5).
-bool few_rows(const PrefillArgs& a) {
-  const int64_t work = tiles_at_most(a, 128) * a.Hkv;
-  return work <= 64 || (work <= 128 && a.Tk / a.B >= 1024);
+  if constexpr (DP <= 192) {
+    if (how == Two128) {
+      attn_prefill<DP, 8, KT, 2><<<tiles_grid(a, 128, 256), dim3(512), 0, s>>>(a);
+      return;
+    }
+  } else if (how == Four64) {
+    attn_prefill<DP, 4, KT, 2><<<tiles_grid(a, 64, 256), dim3(256), 0, s>>>(a);
+    return;
+  }
+  attn_prefill<DP, 4, KT, 1><<<tiles_grid(a, 128, 256 * PER_CU), dim3(256), 0, s>>>(a);
 }
 
 hipError_t launch(PrefillArgs& a, bool bf16, hipStream_t s) {
-  if (!bf16 || few_rows(a)) launch_split(a, bf16, s);
-  else if (a.D <= 64) launch_bf16<64>(a, s);
-  else if (a.D <= 96) launch_bf16<96>(a, s);
-  else if (a.D <= 128) launch_bf16<128>(a, s);
-  else if (a.D <= 192) launch_bf16<192>(a, s);
-  else launch_bf16<256>(a, s);
+  const Shares how = bf16 ? shares_of(a) : Eight32;
+  if (how == Eight32) launch_split(a, bf16, s);
+  else if (a.D <= 64) launch_bf16<64>(a, how, s);
+  else if (a.D <= 96) launch_bf16<96>(a, how, s);
+  else if (a.D <= 128) launch_bf16<128>(a, how, s);
+  else if (a.D <= 192) launch_bf16<192>(a, how, s);
+  else launch_bf16<256>(a, how, s);
   return hipGetLastError();
 }
 

@@ -572,6 +572,55 @@ def test_attn_prefill_long_sequences(lens, past, Hq, Hkv, D):
     assert np.all(np.abs(f64(lse) - rlse) <= ltol + 2.0 ** -22 * np.abs(rlse))
 
 
+@pytest.mark.parametrize("Hkv,D,causal", [  # Hkv: 66 tiles of 128 rows to a key head
+    (2, 64, True), (2, 80, True), (2, 96, True), (3, 128, True), (1, 128, False), (2, 256, True), (1, 224, False),  # 64 rows
+    (4, 64, True), (4, 72, True), (4, 128, True), (3, 120, False), (2, 192, True), (3, 136, False)])  # 128 rows
+def test_attn_prefill_shared_keys(Hkv, D, causal):
+    """Tiles of rows whose keys are shared by waves: sequences of all lengths, none and one among them, rows that see
+    no key, shares that see none, as views of a packed projection into a strided output."""
+    lq, past, G = [300, 1, 0, 37, 64, 65, 5], [700, 500, 300, 900, 0, 1, -3], 16
+    lk = [max(a + b, 0) for a, b in zip(lq, past)]
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lq, lk))
+    Tq, Tk, Hq = int(cu_q[-1]), int(cu_k[-1]), Hkv * G
+    x, y = rnd(70, Tq + 3, Hq + 2, D), rnd(71, Tk + 3, 2 * Hkv + 1, D)
+    x[Tq:], y[Tk:] = float("nan"), float("nan")
+    q, k, v = x[:, 1:Hq + 1], y[:, :Hkv], y[:, Hkv + 1:]
+    xd, yd = x.to(DEV), y.to(DEV)
+    big = torch.full((Tq + 3, Hq + 1, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Tq + 3, Hq), 7.0, device=DEV)
+    args = (xd[:Tq, 1:Hq + 1], yd[:Tk, :Hkv], yd[:Tk, Hkv + 1:], torch.from_numpy(cu_q).to(DEV), torch.from_numpy(cu_k).to(DEV))
+    out = ssm.attn_prefill(*args, causal=causal, out=big[:Tq, 1:], lse=lse[:Tq])
+    ref = whole_sequences(f64(q)[:Tq], f64(k)[:Tk], f64(v)[:Tk], cu_q, cu_k, causal, D ** -0.5)
+    check_attn(out, lse[:Tq], ref, "bf16", D, f"{Hkv} {D}")
+    assert torch.all(big[Tq:] == 3.0) and torch.all(big[:, 0] == 3.0) and torch.all(lse[Tq:] == 7.0)
+    again = ssm.attn_prefill(*args, causal=causal)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("Hkv,D", [(2, 128), (2, 256), (2, 192), (4, 64)])
+def test_attn_prefill_shared_keys_graph_replays(Hkv, D):
+    test_attn_prefill_graph_replays([700, 0, 350], Hkv * 8, Hkv, D)
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D,causal", [(2000, 5000, 40, 1, 64, True), (1700, 4500, 48, 1, 128, False),
+                                                      (6200, 0, 26, 2, 96, True)])
+def test_attn_prefill_very_long_sequence(new, past, Hq, Hkv, D, causal):
+    """Thousands of keys and rows: the first, some middle and the last tokens, and the last key head, against the
+    same rows as sequences of their own."""
+    g = torch.Generator().manual_seed(80)
+    q, k, v = (torch.randn(n, h, D, generator=g).bfloat16() for n, h in ((new, Hq), (new + past, Hkv), (new + past, Hkv)))
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (new, new + past))
+    out = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu_q, cu_k, causal=causal)
+    G = Hq // Hkv
+    for first, last in ((0, 20), (new // 2, new // 2 + 20), (new - 20, new)):
+        keys = past + last if causal else past + new
+        kv = [f64(t)[:keys, -1:] for t in (k, v)]
+        o, _, mag, smax, qkmax = whole_sequences(f64(q)[first:last, -G:], *kv, np.array([0, last - first]), np.array([0, keys]),
+                                                 causal, D ** -0.5)
+        tol, _ = O.attention_tolerance(HALF["bf16"], HALF["bf16"], o, mag, smax, qkmax, D, 1 << 13)
+        close(out[first:last, -G:], o, tol, f"tokens from {first}")
+
+
 # ---------------------------------------------------------------- the binding's two halves
 
 def test_native_and_python_bindings_agree(monkeypatch):
