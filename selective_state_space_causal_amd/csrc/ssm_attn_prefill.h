@@ -20,7 +20,20 @@ struct PrefillArgs {
   int B, Tq, Tk, Hq, Hkv, G, D;
   int causal;
   float scale_log2;  // scale * log2(e)
+  unsigned g_times, g_shift;  // division by G
 };
+
+// x / G for 0 <= x < 2^31: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), which is in [2^31, 2^32), x m / 2^(31 + s) is
+// above x / G by less than x / 2^31 / G, too little to reach the next whole number.
+inline void set_group(PrefillArgs& a, int G) {
+  a.G = G;
+  a.g_shift = 0;
+  while ((int64_t(1) << a.g_shift) < G) ++a.g_shift;
+  a.g_times = (unsigned)(((uint64_t(1) << (31 + a.g_shift)) + G - 1) / G);
+}
+__device__ __forceinline__ int by_group(const PrefillArgs& a, int x) {
+  return (int)(__umulhi(2u * (unsigned)x, a.g_times) >> a.g_shift);
+}
 
 // Inclusive prefix sum over the wave's lanes.
 __device__ __forceinline__ int wave_scan(int x) {

@@ -138,7 +138,7 @@ void attn_prefill(PrefillArgs a) {
     return a.causal ? min(max(token + 1 + w.lk - w.lq, 0), w.lk) : w.lk;
   };
   const auto keys_of = [&](const Work& w) {  // of a tile's last row
-    return seen_by(w, min(w.tile * QT + QT - 1, w.lq * a.G - 1) / a.G);
+    return seen_by(w, by_group(a, min(w.tile * QT + QT - 1, w.lq * a.G - 1)));
   };
   // Keys j0 .. j0 + KB - 1 into a buffer; past the end the last key again (finite, masked below).
   const auto load = [&](const Work& w, int j0, char* kt, char* vt) {
@@ -150,7 +150,7 @@ void attn_prefill(PrefillArgs a) {
   u32x4 qf[NQ];
   const auto load_q = [&](const Work& w) {
     const int c = here(lane), half = c >> 5;
-    const int r = min(w.tile * QT + rw * 32 + (c & 31), w.lq * a.G - 1), tok = r / a.G;
+    const int r = min(w.tile * QT + rw * 32 + (c & 31), w.lq * a.G - 1), tok = by_group(a, r);
     const char* qp = a.q.p + (int64_t)(w.q0 + tok) * a.q.ts + (int64_t)(h * a.G + r - tok * a.G) * a.q.hs;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -168,9 +168,9 @@ void attn_prefill(PrefillArgs a) {
   const auto begin = [&] {
     const int rows = w.lq * a.G;
     r0 = w.tile * QT + rw * 32;
-    seen = seen_by(w, min(r0 + col, rows - 1) / a.G);
-    wave_first = seen_by(w, min(r0, rows - 1) / a.G);
-    wave_last = r0 >= rows ? 0 : seen_by(w, min(r0 + 31, rows - 1) / a.G);
+    seen = seen_by(w, by_group(a, min(r0 + col, rows - 1)));
+    wave_first = seen_by(w, by_group(a, min(r0, rows - 1)));
+    wave_last = r0 >= rows ? 0 : seen_by(w, by_group(a, min(r0 + 31, rows - 1)));
     block_last = keys_of(w);
     j0 = 0;
     m = -INFINITY;
@@ -333,7 +333,7 @@ void attn_prefill(PrefillArgs a) {
     l = half_sum(l);
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int lane = here(threadIdx.x & 63), half = lane >> 5;
-    const int rows = w.lq * a.G, r = r0 + (lane & 31), rc = min(r, rows - 1), tok = rc / a.G, head = h * a.G + rc - tok * a.G;
+    const int rows = w.lq * a.G, r = r0 + (lane & 31), rc = min(r, rows - 1), tok = by_group(a, rc), head = h * a.G + rc - tok * a.G;
     char* op = a.out.p + (int64_t)(w.q0 + tok) * a.out.ts + (int64_t)head * a.out.hs + half * 16;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -505,7 +505,7 @@ extern "C" int ssm_attn_prefill(const ssm_attn_dims* d, const ssm_view* q, const
   a.Tk = (int)Tk;
   a.Hq = d->q_heads;
   a.Hkv = d->kv_heads;
-  a.G = d->q_heads / d->kv_heads;
+  set_group(a, d->q_heads / d->kv_heads);
   a.D = d->head_dim;
   a.causal = d->causal;
   a.scale_log2 = d->scale * 1.4426950408889634f;

@@ -118,11 +118,11 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
     const int q0 = w.q0, lq = w.lq, k0 = w.k0, lk = w.lk;
     const int rows = lq * a.G, r0 = tile * QT;
     const int r = r0 + col, rc = min(r, rows - 1);
-    const int tok = rc / a.G, g = rc - tok * a.G;
+    const int tok = by_group(a, rc), g = rc - tok * a.G;
     const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
     const int seen = seen_by(tok);
-    const int first = __builtin_amdgcn_readfirstlane(seen_by(r0 / a.G));
-    const int last = __builtin_amdgcn_readfirstlane(seen_by(min(r0 + 31, rows - 1) / a.G));
+    const int first = __builtin_amdgcn_readfirstlane(seen_by(by_group(a, r0)));
+    const int last = __builtin_amdgcn_readfirstlane(seen_by(by_group(a, min(r0 + 31, rows - 1))));
 
     const char* kp = a.k.p + (int64_t)k0 * a.k.ts + (int64_t)h * a.k.hs;
     const char* vp = a.v.p + (int64_t)k0 * a.v.ts + (int64_t)h * a.v.hs;
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
           hm = fmaxf(hm, wml[x][row][0]);
         }
         y *= sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int t = rr / a.G, head = h * a.G + rr - t * a.G;
+        const int t = by_group(a, rr), head = h * a.G + rr - t * a.G;
         char* op = a.out.p + (int64_t)(q0 + t) * a.out.ts + (int64_t)head * a.out.hs + (n * BC + e) * ES;
         if constexpr (BF) *reinterpret_cast<u32x2*>(op) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
         else *reinterpret_cast<f32x4*>(op) = y;
