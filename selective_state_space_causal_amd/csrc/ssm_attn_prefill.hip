@@ -65,24 +65,11 @@ struct Tile {
   __device__ static int v_at(int row, int ch) { return (row * CH + (ch ^ v_swap(row))) * 16; }
 };
 
-// A thread's NL pieces of a tile, at byte off[] of its rows, straight into LDS: a wave's 64 pieces in a row, NW
-// waves in turn.  Rows past the last one repeat it (CH pieces to a row, ts bytes between rows).  32-bit
-// offsets: a tile's rows are within 2 GiB.
-template <int NL, int NW, int CH, int KT>
-__device__ __forceinline__ void load_tile(const char* p, int ts, const int* off, int last, int wave, char* lds) {
+// A lane's 16 bytes at byte `off` of a tile's rows straight into LDS, a wave's 64 pieces in a row.  32-bit offsets: a tile's
+// rows are within 2 GiB.
+__device__ __forceinline__ void load_piece(const char* p, int off, char* lds) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
-  if (last >= KT - 1) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16, off[i], 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = ((i * NW + wave) * 64 + (int)(threadIdx.x & 63)) / CH;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds + (i * NW + wave) * 1024), 16,
-                                               off[i] - max(row - last, 0) * ts, 0, 0, 0);
-    }
-  }
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, lds), 16, off, 0, 0, 0);
 }
 
 // bf16: a workgroup of NW waves has 32 rows for every KS waves, which share the keys: key tiles of KS times KT keys go
@@ -140,11 +127,37 @@ void attn_prefill(PrefillArgs a) {
   const auto keys_of = [&](const Work& w) {  // of a tile's last row
     return seen_by(w, by_group(a, min(w.tile * QT + QT - 1, w.lq * a.G - 1)));
   };
-  // Keys j0 .. j0 + KB - 1 into a buffer; past the end the last key again (finite, masked below).
-  const auto load = [&](const Work& w, int j0, char* kt, char* vt) {
-    const int last = min(w.lk - 1 - j0, KB - 1);
-    load_tile<NL, NW, CH, KB>(a.k.p + (int64_t)(w.k0 + j0) * a.k.ts + (int64_t)h * a.k.hs, kts, koff, last, wave, kt);
-    load_tile<NL, NW, CH, KB>(a.v.p + (int64_t)(w.k0 + j0) * a.v.ts + (int64_t)h * a.v.hs, vts, voff, last, wave, vt);
+  // A tile of keys on its way.
+  struct Coming {
+    const char *kp, *vp;
+    int keys;  // of them; 0: none comes
+  };
+  // Whole tiles are asked for piece by piece under the first products where a SIMD has one wave (256 channels: 8000 tokens
+  // 413 to 360 us): a wave waits some 800 cycles to issue them.  With two waves a SIMD the other one works meanwhile, and
+  // the pieces between the products cost 1 to 4%.
+  constexpr bool UNDER = DP > 192;
+  const auto coming = [&](const Work& w, int j0) {
+    return Coming{a.k.p + (int64_t)(w.k0 + j0) * a.k.ts + (int64_t)h * a.k.hs,
+                  a.v.p + (int64_t)(w.k0 + j0) * a.v.ts + (int64_t)h * a.v.hs, min(w.lk - j0, KB)};
+  };
+  // Piece i of NL of K, then of NL of V, of a whole tile into (kt, vt).
+  const auto load_whole = [&](const Coming& t, int i, char* kt, char* vt) {
+    if (i < NL) load_piece(t.kp, koff[i], kt + (i * NW + wave) * 1024);
+    else load_piece(t.vp, voff[i - NL], vt + ((i - NL) * NW + wave) * 1024);
+  };
+  // All of a tile; past the last key that one again (finite, masked below).
+  const auto load = [&](const Coming& t, char* kt, char* vt) {
+    if (!UNDER && t.keys == KB) {
+#pragma unroll
+      for (int i = 0; i < 2 * NL; ++i) load_whole(t, i, kt, vt);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int past = max(((i * NW + wave) * 64 + here(lane)) / CH - (t.keys - 1), 0), at = (i * NW + wave) * 1024;
+      load_piece(t.kp, koff[i] - past * kts, kt + at);
+      load_piece(t.vp, voff[i] - past * vts, vt + at);
+    }
   };
   // Q as the right operand: a lane's row, in the order that the K reads below use.
   u32x4 qf[NQ];
@@ -179,7 +192,8 @@ void attn_prefill(PrefillArgs a) {
     for (int d = 0; d < ND; ++d) o[d] = f32x16{};
   };
 
-  const auto work = [&](const char* kt, const char* vt, bool last) {
+  const auto work = [&](const char* kt, const char* vt, bool last, const Coming& t, char* kn, char* vn) {
+      const bool under = UNDER && t.keys == KB;
       const int j1 = j0 + kw * KT;  // this wave's keys of the tile
       kt += kw * (KT * CH * 16);
       vt += kw * (KT * CH * 16);
@@ -199,6 +213,9 @@ void attn_prefill(PrefillArgs a) {
         __builtin_amdgcn_sched_barrier(0);
         sn = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % AHEAD], __builtin_bit_cast(bf16x8, qf[i % NQ]), sn, 0, 0, 0);
         if (i + AHEAD < NS * NQ) kf[i % AHEAD] = read_k(i + AHEAD);
+#pragma unroll
+        for (int p = 0; p < 2 * NL; ++p)
+          if (p * NS * NQ / (2 * NL) == i && under) load_whole(t, p, kn, vn);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (last) load_q(nx);
@@ -357,11 +374,13 @@ void attn_prefill(PrefillArgs a) {
   // One key tile, from (kc, vc), while the next one comes into (kn, vn); false when all is done.
   const auto advance = [&](char* kc, char* vc, char* kn, char* vn) {
     const bool ends = j0 + KB >= block_last;
-    if (!ends) load(w, j0 + KB, kn, vn);
-    if (fresh) more = next(nx), fresh = false;
-    if (ends && more && keys_of(nx) > 0) load(nx, 0, kn, vn);
     const bool sees = j0 + kw * KT < wave_last;
-    if (sees) work(kc, vc, ends && more);
+    if (!UNDER && !ends) load(coming(w, j0 + KB), kn, vn);
+    if (fresh) more = next(nx), fresh = false;
+    Coming t = ends ? coming(nx, 0) : coming(w, j0 + KB);
+    if (ends && (!more || keys_of(nx) <= 0)) t.keys = 0;
+    if (UNDER ? t.keys > 0 && !(sees && t.keys == KB) : ends && t.keys > 0) load(t, kn, vn);
+    if (sees) work(kc, vc, ends && more, t, kn, vn);
     if (!sees && ends && more) load_q(nx);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), said here: the compiler then waits for no load under the products
     __syncthreads();  // the reads of (kc, vc) are over, (kn, vn) and a next tile's Q are there
@@ -379,7 +398,7 @@ void attn_prefill(PrefillArgs a) {
   };
 
   begin();
-  if (block_last > 0) load(w, 0, kt0, vt0);
+  if (block_last > 0) load(coming(w, 0), kt0, vt0);
   load_q(w);
   __builtin_amdgcn_s_waitcnt(0x0F70);
   __syncthreads();
