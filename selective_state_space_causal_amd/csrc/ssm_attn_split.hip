@@ -100,7 +100,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
   // Channels of a lane, blocks of 32 VE, words of a lane's channels of one key
   constexpr int VE = DP % 128 == 0 ? 4 : DP % 64 == 0 ? 2 : 1, NB = DP / (32 * VE), VW = VE * ES / 4;
   static_assert(VW >= 1, "bf16 takes two channels at a time");
-  constexpr bool QREG = DP * ES <= 512;  // Q in registers beside a step's K, V and output, else in LDS
+  constexpr bool QREG = BF || DP <= 64;  // Q in registers beside a step's K, V and output, else in LDS (fp32's is three parts)
   __shared__ float wml[NW][32][2];
   __shared__ __attribute__((aligned(16))) float wo[NW][32][32 * VE + 4];
   __shared__ __attribute__((aligned(16))) u32x4 ql[QREG ? 1 : BF ? NQ : NQ / 2 * 3][64];
@@ -277,11 +277,19 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
   }
 }
 
-// Waves of a workgroup: eight, two a SIMD, where registers allow.
+// Waves of a workgroup: eight, two a SIMD, where registers allow (fp32 rows of 96 and 128 channels with Q in LDS: 1000 tokens of
+// 8 and 2 heads 39.6 to 36.7 us, 4000 of 32 and 8 195 to 178).  fp32 rows of 64 channels fit twice on a CU with four: eight gain
+// 10% while the tiles leave CUs half empty, and lose 25 to 60% after.
 template <typename IO, int DP>
 void launch_dp(const PrefillArgs& a, hipStream_t s) {
-  constexpr int NW = sizeof(IO) == 2 && DP <= 128 ? 8 : 4;
-  attn_split<IO, DP, NW><<<tiles_grid(a, 32, INT32_MAX), dim3(NW * 64), 0, s>>>(a);
+  constexpr bool BF = sizeof(IO) == 2;
+  if constexpr (DP <= 128) {
+    if (BF || DP > 64 || tiles_at_most(a, 32) * a.Hkv <= 512) {
+      attn_split<IO, DP, 8><<<tiles_grid(a, 32, INT32_MAX), dim3(512), 0, s>>>(a);
+      return;
+    }
+  }
+  if constexpr (DP > 128 || (!BF && DP <= 64)) attn_split<IO, DP, 4><<<tiles_grid(a, 32, INT32_MAX), dim3(256), 0, s>>>(a);
 }
 
 }  // namespace
