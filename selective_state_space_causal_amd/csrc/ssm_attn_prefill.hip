@@ -85,7 +85,8 @@ void attn_prefill(PrefillArgs a) {
   constexpr int BYTES = KB * CH * 16, NL = KB * CH / (NW * 64);  // a tile's bytes and 16-byte loads of a thread
   // Four arrays, not two of two: the compiler then knows that the loads in flight do not write what is read.
   __shared__ __attribute__((aligned(16))) char kt0[BYTES], kt1[BYTES], vt0[BYTES], vt1[BYTES];
-  __shared__ int4 seqs[64];
+  __shared__ int4 seqs[64], found_q[2][NW];
+  __shared__ int2 found_k[2][NW];
   __shared__ float2 stats[KS > 1 ? NW / 2 : 1][64];
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rw = wave % RW, kw = wave / RW;
@@ -105,20 +106,46 @@ void attn_prefill(PrefillArgs a) {
   __syncthreads();
 
   const int h = blockIdx.x, places = gridDim.y, place = blockIdx.y;
-  int64_t dealt = 0;  // tiles dealt to all places so far
-  bool forwards = true;
   int top = (int)(((unsigned)a.Tk + KB - 1) / KB);
-  // The next tile of rows; false when there are no more.
+  // The tile that this place takes in a round; tile -1 past the last.
+  const auto find = [&](int round) {
+    const int64_t idx = (int64_t)round * places + (round & 1 ? places - 1 - place : place);
+    Work w = {};
+    bool found;
+    if (a.B <= 64) {
+      found = find_sorted(a, QT, KB, seqs[here(lane)], idx, top, w);
+    } else {
+      found = find_tile(a, QT, idx, w);
+      w.tile = w.tiles - 1 - w.tile;  // causal: a sequence's tiles with the most keys first
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) of its loads here, not under the products
+    }
+    if (!found) w.tile = -1;
+    return w;
+  };
+  // Finding a tile takes a wave some 2000 cycles: from the second on each wave finds another one of the next NW, for all (2 to
+  // 5% of calls with several tiles to a place).
+  const auto find_batch = [&](int batch) {
+    const Work w = find(1 + batch * NW + wave);
+    if (here(lane) == 0) {
+      found_q[batch & 1][wave] = make_int4(w.tile, w.q0, w.lq, 0);
+      found_k[batch & 1][wave] = make_int2(w.k0, w.lk);
+    }
+  };
+  // The next one; false when there are no more.  A barrier lies between two calls: a batch is found two calls after the last one
+  // of its place was taken, and three or more before its first is.
+  int taken = 0;
   const auto next = [&](Work& w) {
-    const int64_t idx = dealt + (forwards ? place : places - 1 - place);
-    dealt += places;
-    forwards = !forwards;
-    if (a.B <= 64) return find_sorted(a, QT, KB, seqs[here(lane)], idx, top, w);
-    const bool found = find_tile(a, QT, idx, w);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) of its loads here, not under the products
-    if (!found) return false;
-    w.tile = w.tiles - 1 - w.tile;  // causal: a sequence's tiles with the most keys first
-    return true;
+    const int batch = taken / NW, i = taken % NW;
+    if (i == 1) find_batch(batch + 1);
+    const int4 q = found_q[batch & 1][i];
+    const int2 k = found_k[batch & 1][i];
+    ++taken;
+    w.tile = __builtin_amdgcn_readfirstlane(q.x);
+    w.q0 = __builtin_amdgcn_readfirstlane(q.y);
+    w.lq = __builtin_amdgcn_readfirstlane(q.z);
+    w.k0 = __builtin_amdgcn_readfirstlane(k.x);
+    w.lk = __builtin_amdgcn_readfirstlane(k.y);
+    return w.tile >= 0;
   };
   // Keys that a token of a sequence sees: [0, seen_by).
   const auto seen_by = [&](const Work& w, int token) {
@@ -172,8 +199,8 @@ void attn_prefill(PrefillArgs a) {
     }
   };
 
-  Work w, nx = {};
-  if (!next(w)) return;
+  Work w = find(0), nx = {};
+  if (w.tile < 0) return;
   bool more = false, fresh = true;  // more: nx is the next tile; fresh: not yet looked for
   int r0, seen, wave_first, wave_last, block_last, j0;
   f32x16 o[ND];
@@ -400,6 +427,7 @@ void attn_prefill(PrefillArgs a) {
   begin();
   if (block_last > 0) load(coming(w, 0), kt0, vt0);
   load_q(w);
+  find_batch(0);
   __builtin_amdgcn_s_waitcnt(0x0F70);
   __syncthreads();
   while (advance(kt0, vt0, kt1, vt1) && advance(kt1, vt1, kt0, vt0)) {
