@@ -19,6 +19,10 @@
 // 4 key heads of 256: 45 us against 76 with one); one for a wide cache of fp32, whose keys take the registers.
 // The page numbers are read a step ahead, by the scalar unit.
 //
+// 8-bit codes are exact in bf16, so fp32 calls multiply them as bf16 too: q and the weights are split into three bf16,
+// x = h + m + l to 2^-27 of x (each the remainder of the last, rounded), and the three products take a fifth of the time of the
+// fp32 matrix instruction.  A cache of fp32 is multiplied in fp32.
+//
 // The long axis is split into chunks, one workgroup each; its waves take 32 keys in turn and join their
 // results in LDS.  With more than one chunk the partial results (maximum, sum, unnormalised output, fp32)
 // are joined by a second kernel.  Both joins add in a fixed order.
@@ -80,6 +84,14 @@ __device__ __forceinline__ unsigned widen_pair(unsigned w, int p) {
                 : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
 }
 
+// Two values rounded to bf16, and what that leaves of them (exact).
+__device__ __forceinline__ unsigned take_bf16(float& x0, float& x1) {
+  const unsigned w = pack_bf16(x0, x1);
+  x0 -= __uint_as_float(w << 16);
+  x1 -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
+}
+
 // Element c of one channel piece as fp32: V words w of VE elements of CS bytes.
 template <int KV, int CS>
 __device__ __forceinline__ float element_f32(const unsigned* w, int c) {
@@ -116,8 +128,9 @@ __device__ __forceinline__ void load_words(unsigned* w, const char* p) {
 // A workgroup is one (chunk, 16 heads of a key head, sequence).
 template <typename IO, int KV, int DP>
 __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP > 128 ? 1 : 2) : DP > 128 ? 2 : 3) void attn_decode(DecodeArgs a) {
-  constexpr bool BF = sizeof(IO) == 2;
-  constexpr int CS = KV == SSM_KV_IO ? sizeof(IO) : 1;
+  constexpr bool BF = sizeof(IO) == 2, CODES = KV != SSM_KV_IO;
+  constexpr int CS = CODES ? 1 : sizeof(IO);
+  constexpr int QPARTS = BF ? 1 : 3, WPARTS = BF ? 2 : 3;  // bf16 that make one value of q and one weight
   // K: pieces of KB bytes; 16, but 8 of 8-bit codes where a row may be that short
   constexpr int KB = CS == 1 && DP == 64 ? 8 : 16, KE = KB / CS, NK = DP / (4 * KE), KW = KB / 4;
   // V: VE channels of a lane, NB blocks of 16 VE channels
@@ -141,7 +154,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
     const char* qp = a.q.p + (int64_t)b * a.q.ts + (int64_t)head * a.q.hs;
     // Q in the order of K's pieces.  Where a row ends, a lane reads an earlier piece of it against zeros.
     int koff[NK];
-    unsigned qf[NK][KE * (BF ? 2 : 4) / 4];
+    unsigned qf[NK][BF || CODES ? KE / 2 * QPARTS : KE];  // bf16 by eights of channels, the parts of an eight one after another
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const int e = (4 * i + w4) * KE;
@@ -153,7 +166,18 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
         u32x4 x = {0, 0, 0, 0};
         if (at >= e && at < D) x = *reinterpret_cast<const u32x4*>(qp + at * (int)sizeof(IO));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qf[i][4 * h + j] = x[j];
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (BF || !CODES) qf[i][4 * h + j] = x[j];
+        }
+        if constexpr (!BF && CODES) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float f0 = __uint_as_float(x[2 * j]), f1 = __uint_as_float(x[2 * j + 1]);
+#pragma unroll
+            for (int part = 0; part < QPARTS; ++part)
+              qf[i][(h / 2 * QPARTS + part) * 4 + h % 2 * 2 + j] = take_bf16(f0, f1);
+          }
+        }
       }
     }
     int voff[NB];  // channels past the row's end are made of its first ones and not stored
@@ -206,7 +230,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          if constexpr (BF) {
+          if constexpr (BF || CODES) {
 #pragma unroll
             for (int h = 0; h < KE / 8; ++h) {
               u32x4 kf;
@@ -215,9 +239,13 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
                            widen_pair<KV>(x.k[t][i][2 * h + 1], 0), widen_pair<KV>(x.k[t][i][2 * h + 1], 1)};
               else
                 kf = u32x4{x.k[t][i][0], x.k[t][i][1], x.k[t][i][2], x.k[t][i][3]};
-              const u32x4 q = {qf[i][4 * h], qf[i][4 * h + 1], qf[i][4 * h + 2], qf[i][4 * h + 3]};
-              s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf),
-                                                             __builtin_bit_cast(bf16x8, q), s[t], 0, 0, 0);
+#pragma unroll
+              for (int part = QPARTS - 1; part >= 0; --part) {  // the small ones first
+                const unsigned* qh = qf[i] + (h * QPARTS + part) * 4;
+                const u32x4 q = {qh[0], qh[1], qh[2], qh[3]};
+                s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf),
+                                                               __builtin_bit_cast(bf16x8, q), s[t], 0, 0, 0);
+              }
             }
           } else {
 #pragma unroll
@@ -268,14 +296,14 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
           l += p;  // this quarter's keys only; joined at the end
           s[t][i] = KV != SSM_KV_IO ? p * x.sv[t][i] : p;
         }
-      if constexpr (BF) {
-        // A weight as the sum of two bf16 (2^-17): one alone would be as inexact as the output's own rounding.
-        u32x4 pf, pr;
+      if constexpr (BF || CODES) {
+        // bf16: a weight as the sum of two (2^-17), as one alone would be as inexact as the output's own rounding.
+        u32x4 pw[WPARTS];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x0 = s[j / 2][j % 2 * 2], x1 = s[j / 2][j % 2 * 2 + 1];
-          pf[j] = pack_bf16(x0, x1);
-          pr[j] = pack_bf16(x0 - __uint_as_float(pf[j] << 16), x1 - __uint_as_float(pf[j] & 0xFFFF0000u));
+          float x0 = s[j / 2][j % 2 * 2], x1 = s[j / 2][j % 2 * 2 + 1];
+#pragma unroll
+          for (int part = 0; part < WPARTS; ++part) pw[part][j] = take_bf16(x0, x1);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -299,7 +327,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP >
             f32x4& o0 = o[n * VE + c];
             f32x4& o1 = o[n * VE + c + 1];
 #pragma unroll
-            for (const u32x4& p : {pf, pr}) {
+            for (const u32x4& p : pw) {
               const bf16x8 w = __builtin_bit_cast(bf16x8, p);
               o0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v0), w, o0, 0, 0, 0);
               o1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v1), w, o1, 0, 0, 0);
