@@ -16,7 +16,7 @@
 // All of a step's loads are issued before its first product, and are hidden by the other waves of a SIMD: three of
 // them up to head_dim 128, with registers for one set of keys each, measured better than two that load 32 keys ahead
 // (64 sequences of up to 8192 int8 tokens, 8 key heads of 128: 122 us, 4.6 TB/s, against 132); two above (32 sequences,
-// 4 key heads of 256: 45 us against 76 with one); one for a wide cache of fp32, whose keys take the registers.
+// 4 key heads of 256: 45 us against 76 with one); fewer in fp32, whose keys or parts of q take the registers.
 // The page numbers are read a step ahead, by the scalar unit.
 //
 // 8-bit codes are exact in bf16, so fp32 calls multiply them as bf16 too: q and the weights are split into three bf16,
@@ -125,9 +125,16 @@ __device__ __forceinline__ void load_words(unsigned* w, const char* p) {
   }
 }
 
+// Waves of a SIMD.
+constexpr int waves_of(bool bf16, bool codes, int DP) {
+  if (bf16) return DP > 128 ? 2 : 3;
+  if (codes) return DP > 192 ? 1 : DP > 64 ? 2 : 3;  // 59 sequences of 818 keys of 256: 37 us, 46 with two
+  return DP > 128 ? 1 : 2;
+}
+
 // A workgroup is one (chunk, 16 heads of a key head, sequence).
 template <typename IO, int KV, int DP>
-__global__ __launch_bounds__(NW * 64, sizeof(IO) == 4 && KV == SSM_KV_IO ? (DP > 128 ? 1 : 2) : DP > 128 ? 2 : 3) void attn_decode(DecodeArgs a) {
+__global__ __launch_bounds__(NW * 64, waves_of(sizeof(IO) == 2, KV != SSM_KV_IO, DP)) void attn_decode(DecodeArgs a) {
   constexpr bool BF = sizeof(IO) == 2, CODES = KV != SSM_KV_IO;
   constexpr int CS = CODES ? 1 : sizeof(IO);
   constexpr int QPARTS = BF ? 1 : 3, WPARTS = BF ? 2 : 3;  // bf16 that make one value of q and one weight
