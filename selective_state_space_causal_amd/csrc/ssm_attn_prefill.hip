@@ -448,12 +448,13 @@ void attn_prefill(PrefillArgs a) {
 //   n 1016, k  2000                        419     192      154      134      136
 //   n 2056, k  8192                       1534     697      542      514      491
 //   n  168, k   143                       20.6    15.4     11.6     11.0     14.7
-// Without the mask all tiles of rows are as long, and there is nothing to even out where the tiles are more than the CUs.
+// Without the mask all tiles of rows are as long, and there is nothing to even out where the tiles are more than the CUs
+// (2500 tokens of 4 heads over one key head, n 79: Eight32 64 us, Four64 32; 2000, n 63: 28 and 27, and of 64 channels 15 and 20).
 enum Shares { Eight32, Four64, Two128, One128, One256 };
 Shares shares_of(const PrefillArgs& a) {
   const int64_t n = tiles_at_most(a, 128) * a.Hkv, k = a.Tk / a.B;
   // 32 rows straight from memory (ssm_attn_split.hip): rows of 64 channels, and those too wide for four shares, gain longer.
-  if (n <= (a.D > 192 ? 96 : 64) || (n <= (a.D > 64 && a.D <= 128 ? 96 : 128) && k >= 1024)) return Eight32;
+  if (n <= 64 || (a.causal && ((n <= 96 && a.D > 192) || (n <= (a.D > 64 && a.D <= 128 ? 96 : 128) && k >= 1024)))) return Eight32;
   if (k < 256) return One128;
   if (n <= (a.causal ? 260 : 130) && (a.D <= 128 || a.D > 192)) return Four64;
   if (n <= (!a.causal ? 260 : k >= 1024 ? 576 : 320) && a.D <= 192) return Two128;
