@@ -125,8 +125,8 @@ int ssm_kv_read(int64_t tokens, int32_t io_dtype, const ssm_kv_cache* cache, con
 
 typedef struct {
   int64_t batch;     /* sequences, 1 .. SSM_ATTN_MAX_BATCH */
-  int64_t q_tokens;  /* tokens of q and out (all sequences) */
-  int64_t k_tokens;  /* tokens of k and v */
+  int64_t q_tokens;  /* tokens of q and out (all sequences); q_tokens * (q_heads / kv_heads) <= 2^30 - 32 */
+  int64_t k_tokens;  /* tokens of k and v, below 2^31 - 2^20 */
   int32_t q_heads;
   int32_t kv_heads;
   int32_t head_dim;

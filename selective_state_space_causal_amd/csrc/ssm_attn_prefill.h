@@ -9,6 +9,10 @@
 namespace ssm {
 namespace attn {
 
+// Limits of a call, so that the kernels' ints hold: they step up to 256 keys past a sequence's end, and add the counts of
+// tiles (of 32 rows or more) of 64 sequences, each of which may claim every row where the offsets are not in order.
+constexpr int64_t MAX_KEYS = (int64_t)INT32_MAX - (1 << 20), MAX_ROWS = (int64_t(1) << 30) - 32;
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
 
@@ -33,6 +37,11 @@ inline void set_group(PrefillArgs& a, int G) {
 }
 __device__ __forceinline__ int by_group(const PrefillArgs& a, int x) {
   return (int)(__umulhi(2u * (unsigned)x, a.g_times) >> a.g_shift);
+}
+
+// Keys that a token (below lq) of a sequence sees: the first ones.  In an order whose sums stay within 32 bits.
+__device__ __forceinline__ int seen_of(const PrefillArgs& a, int lq, int lk, int token) {
+  return a.causal ? max(lk - (lq - 1 - token), 0) : lk;
 }
 
 // Inclusive prefix sum over the wave's lanes.

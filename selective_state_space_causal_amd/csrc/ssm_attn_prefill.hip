@@ -148,9 +148,7 @@ void attn_prefill(PrefillArgs a) {
     return w.tile >= 0;
   };
   // Keys that a token of a sequence sees: [0, seen_by).
-  const auto seen_by = [&](const Work& w, int token) {
-    return a.causal ? min(max(token + 1 + w.lk - w.lq, 0), w.lk) : w.lk;
-  };
+  const auto seen_by = [&](const Work& w, int token) { return seen_of(a, w.lq, w.lk, token); };
   const auto keys_of = [&](const Work& w) {  // of a tile's last row
     return seen_by(w, by_group(a, min(w.tile * QT + QT - 1, w.lq * a.G - 1)));
   };
@@ -514,8 +512,8 @@ extern "C" int ssm_attn_prefill(const ssm_attn_dims* d, const ssm_view* q, const
   if (const int st = check_heads(d->kv_heads, d->head_dim)) return st;
   if (d->q_heads % d->kv_heads) return SSM_ERR_SHAPE;
   if (d->batch < 1 || d->batch > SSM_ATTN_MAX_BATCH) return SSM_ERR_SHAPE;
-  if (d->q_tokens < 0 || d->k_tokens < 0 || d->k_tokens > MAX_TOKENS) return SSM_ERR_SHAPE;
-  if (d->q_tokens > MAX_TOKENS / (d->q_heads / d->kv_heads)) return SSM_ERR_SHAPE;
+  if (d->q_tokens < 0 || d->k_tokens < 0 || d->k_tokens > MAX_KEYS) return SSM_ERR_SHAPE;
+  if (d->q_tokens > MAX_ROWS / (d->q_heads / d->kv_heads)) return SSM_ERR_SHAPE;
   if (!isfinite(d->scale) || !(d->scale > 0.0f) || (d->causal != 0 && d->causal != 1)) return SSM_ERR_SHAPE;
   if (d->q_tokens == 0) return SSM_OK;
   if (!cu_q || !cu_k) return SSM_ERR_NULL;

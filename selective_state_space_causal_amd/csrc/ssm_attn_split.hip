@@ -119,7 +119,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
     const int rows = lq * a.G, r0 = tile * QT;
     const int r = r0 + col, rc = min(r, rows - 1);
     const int tok = by_group(a, rc), g = rc - tok * a.G;
-    const auto seen_by = [&](int token) { return a.causal ? min(max(token + 1 + lk - lq, 0), lk) : lk; };
+    const auto seen_by = [&](int token) { return seen_of(a, lq, lk, token); };
     const int seen = seen_by(tok);
     const int first = __builtin_amdgcn_readfirstlane(seen_by(by_group(a, r0)));
     const int last = __builtin_amdgcn_readfirstlane(seen_by(by_group(a, min(r0 + 31, rows - 1))));
