@@ -46,14 +46,14 @@ def attn_block_prefill(hidden, weights: dict, q_heads: int, cache: "attn.KVCache
     """hidden [T, d_model]: the new tokens of all sequences, packed (cu_q, int32 [batch + 1]), at cache rows `slots`
     and `positions` [T] int64; freq and mscale as rope_frequencies gives them.  weights: "qkv" [(Hq + 2 Hkv) D,
     d_model] and "out" [d_model, Hq D].  Sequences that already have cached tokens: context_slots are the
-    slots of all of each sequence's tokens, the new ones last, packed by cu_k.  Returns [T, d_model]."""
+    slots of all of each sequence's tokens, the new ones last, packed by cu_k (both or neither).  Returns [T, d_model]."""
+    if (context_slots is None) != (cu_k is None):
+        raise ValueError("context_slots and cu_k go together")
     q, k, v = _heads(hidden, weights, q_heads, cache)
     attn.kv_write(k, v, cache, slots, q=q, positions=positions, freq=freq, interleaved=interleaved, mscale=mscale, q_out=q,
                   k_out=k)
     if context_slots is not None:
         k, v = attn.kv_read(cache, context_slots, dtype=hidden.dtype)
-    elif cu_k is not None:
-        raise ValueError("cu_k without context_slots")
     o = attn.attn_prefill(q, k, v, cu_q, cu_k)
     return linear(o.view(hidden.shape[0], -1), weights["out"])
 
