@@ -55,7 +55,7 @@ def attn_block_prefill(hidden, weights: dict, q_heads: int, cache: "attn.KVCache
     if context_slots is not None:
         k, v = attn.kv_read(cache, context_slots, dtype=hidden.dtype)
     o = attn.attn_prefill(q, k, v, cu_q, cu_k)
-    return linear(o.view(hidden.shape[0], -1), weights["out"])
+    return linear(o.flatten(1), weights["out"])
 
 
 def attn_block_decode(hidden_t, weights: dict, q_heads: int, cache: "attn.KVCache", table, lens, freq, *,
@@ -68,4 +68,4 @@ def attn_block_decode(hidden_t, weights: dict, q_heads: int, cache: "attn.KVCach
     slots = cache_slots(table, torch.arange(table.shape[0], device=table.device), positions, cache.page_size)
     attn.kv_write(k, v, cache, slots, q=q, positions=positions, freq=freq, interleaved=interleaved, mscale=mscale, q_out=q)
     o = attn.attn_decode_step(q, cache, table, lens, workspace=workspace)
-    return linear(o.view(hidden_t.shape[0], -1), weights["out"])
+    return linear(o.flatten(1), weights["out"])

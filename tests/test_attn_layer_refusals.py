@@ -41,3 +41,10 @@ def test_context_slots_and_cu_k_go_together(calls, given):
         attn_layer.attn_block_prefill(torch.zeros(2, 4), weights(), 1, Cache(), torch.arange(2), cu, torch.arange(2),
                                       torch.ones(4), **given)
     assert calls == []
+
+
+def test_no_tokens(calls):
+    """A prompt of no tokens gives [0, d_model], as the operators do."""
+    out = attn_layer.attn_block_prefill(torch.zeros(0, 4), weights(), 1, Cache(), torch.arange(0),
+                                        torch.tensor([0, 0], dtype=torch.int32), torch.arange(0), torch.ones(4))
+    assert out.shape == (0, 4) and calls == ["kv_write", "attn_prefill"]
