@@ -26,6 +26,8 @@ def cache_slots(table, seq, positions, page_size: int):
     """Slots of tokens: token i is at `positions[i]` of sequence `seq[i]`, whose pages are table[seq[i]] (int32
     [batch, width]).  -1 where there is no page (kv_write skips it).  int64, on table's device."""
     width = table.shape[1]
+    if width == 0:  # nothing to look up
+        return torch.full_like(positions, -1)
     at = positions.div(page_size, rounding_mode="floor")
     page = table[seq, at.clamp(0, width - 1)].long()
     held = (at >= 0) & (at < width) & (page >= 0)

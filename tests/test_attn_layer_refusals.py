@@ -48,3 +48,15 @@ def test_no_tokens(calls):
     out = attn_layer.attn_block_prefill(torch.zeros(0, 4), weights(), 1, Cache(), torch.arange(0),
                                         torch.tensor([0, 0], dtype=torch.int32), torch.arange(0), torch.ones(4))
     assert out.shape == (0, 4) and calls == ["kv_write", "attn_prefill"]
+
+
+def test_slots_of_a_table_without_pages():
+    """No pages: no slots, and no index into the table, which would lie outside it."""
+    table = torch.empty(2, 0, dtype=torch.int32)
+    assert attn_layer.cache_slots(table, torch.tensor([0, 1, 1]), torch.tensor([0, 5, -1]), 16).tolist() == [-1, -1, -1]
+
+
+def test_slots():
+    table = torch.tensor([[3, 0, -1], [1, 2, 4]], dtype=torch.int32)
+    seq, pos = torch.tensor([0, 0, 1, 0, 0, 1]), torch.tensor([5, 16, 47, 33, -1, 48])
+    assert attn_layer.cache_slots(table, seq, pos, 16).tolist() == [53, 0, 79, -1, -1, -1]
