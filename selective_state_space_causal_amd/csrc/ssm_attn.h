@@ -175,5 +175,12 @@ inline Cache cache_of(const ssm_kv_cache* c) {
   return r;
 }
 
+// The stream of a call whose checks are done.  An error that an earlier, unrelated call left behind is dropped, so that
+// what hipGetLastError says after the launch is the launch's own.
+inline hipStream_t ready(void* stream) {
+  (void)hipGetLastError();
+  return static_cast<hipStream_t>(stream);
+}
+
 }  // namespace attn
 }  // namespace ssm

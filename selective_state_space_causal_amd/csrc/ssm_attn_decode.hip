@@ -622,7 +622,7 @@ int ssm_attn_decode_step(int64_t batch, int32_t q_heads, int32_t io_dtype, float
   if (!isfinite(a.scale_log2) || !(a.scale_log2 > 0.0f)) return SSM_ERR_SHAPE;
   a.po = static_cast<float*>(workspace);
   a.ml = a.po + (int64_t)batch * q_heads * a.chunks * cache->head_dim;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = ready(stream);
   const hipError_t e = io_dtype == SSM_BF16 ? launch_decode_attn<ssm::bf16_t>(a, cache->kv_dtype, s)
                                             : launch_decode_attn<float>(a, cache->kv_dtype, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;

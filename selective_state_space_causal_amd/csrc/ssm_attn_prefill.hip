@@ -556,7 +556,7 @@ extern "C" int ssm_attn_prefill(const ssm_attn_dims* d, const ssm_view* q, const
   a.causal = d->causal;
   a.scale_log2 = d->scale * 1.4426950408889634f;
   if (!isfinite(a.scale_log2) || !(a.scale_log2 > 0.0f)) return SSM_ERR_SHAPE;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = ready(stream);
   const hipError_t e = launch(a, d->io_dtype == SSM_BF16, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }

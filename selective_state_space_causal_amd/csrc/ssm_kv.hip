@@ -456,7 +456,7 @@ int ssm_rope(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
   a.Hk = k_heads;
   a.D = head_dim;
   set_rope(a, rope);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = ready(stream);
   const hipError_t e = io_dtype == SSM_BF16 ? launch_rows<ssm::bf16_t, SSM_KV_IO, true, false>(a, s)
                                             : launch_rows<float, SSM_KV_IO, true, false>(a, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
@@ -530,7 +530,7 @@ int ssm_kv_write(int64_t tokens, int32_t io_dtype, const ssm_kv_cache* cache, co
   if (rope) set_rope(a, rope);
   a.c = cache_of(cache);
   a.slots = slots;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = ready(stream);
   const hipError_t e = io_dtype == SSM_BF16 ? launch_write<ssm::bf16_t>(a, cache->kv_dtype, rope != nullptr, s)
                                             : launch_write<float>(a, cache->kv_dtype, rope != nullptr, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
@@ -563,7 +563,7 @@ int ssm_kv_read(int64_t tokens, int32_t io_dtype, const ssm_kv_cache* cache, con
   a.c = cache_of(cache);
   a.slots = slots;
   a.T = T;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = ready(stream);
   hipError_t e;
   if (io_dtype == SSM_BF16)
     e = cache->kv_dtype == SSM_KV_IO   ? launch_read<ssm::bf16_t, SSM_KV_IO>(a, s)
