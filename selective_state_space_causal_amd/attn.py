@@ -112,7 +112,7 @@ def _bound():
             from . import _attn_fast
             _attn_fast.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
                 "ssm_rope", "ssm_kv_write", "ssm_kv_read", "ssm_attn_prefill", "ssm_attn_decode_step",
-                "ssm_attn_decode_workspace_bytes")))
+                "ssm_attn_decode_workspace_bytes")), _fail)
             _native = _attn_fast
         except ImportError as e:
             warnings.warn(f"the attention calls' native binding is not built ({e}): small calls are slower; run "

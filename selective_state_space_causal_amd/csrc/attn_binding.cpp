@@ -3,8 +3,9 @@
 // A small call (a few tokens) spends longer in the interpreter than on the GPU: reading each tensor's shape, type,
 // device and strides, and making the outputs.  Each function here takes the arguments of the function of its name in
 // attn.py, on the current stream, and answers NotImplemented, having done nothing, whenever anything about them is not the usual
-// (another type, shape or device, a missing tensor, a status other than success to report): attn.py then goes
-// through its own checks, which name what is wrong.  So it holds no message and no behaviour of its own.  The entry
+// (another type, shape or device, a missing tensor, a refusal to report): attn.py then goes
+// through its own checks, which name what is wrong.  So it holds no message and no behaviour of its own.  A launch that
+// fails may have done something (a call in place must not be made twice): it is raised from here.  The entry
 // points of libssm.so are handed over by address (bind): this module does not load the library.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -26,7 +27,26 @@ decltype(&ssm_attn_prefill) f_prefill;
 decltype(&ssm_attn_decode_step) f_decode;
 decltype(&ssm_attn_decode_workspace_bytes) f_workspace;
 
+PyObject* raise_status;  // attn.py's function of a name and a status that raises
+
 PyObject* not_usual() { Py_RETURN_NOTIMPLEMENTED; }
+
+// A Python object of a call's own, given back unless the call succeeds.  Outputs are made before the launch, so that
+// nothing can go wrong after it.
+struct Ref {
+  PyObject* p;
+  explicit Ref(PyObject* object) : p(object) {}
+  Ref(const Ref&) = delete;
+  ~Ref() { Py_XDECREF(p); }
+  // What to answer for the status that entry point `name` returned; every refusal comes before any launch.
+  PyObject* after(int status, const char* name) {
+    if (status == SSM_ERR_LAUNCH) return PyObject_CallFunction(raise_status, "si", name, status);
+    if (status != SSM_OK) return not_usual();
+    PyObject* r = p;
+    p = nullptr;
+    return r;
+  }
+};
 
 // A call is usual until something is not; the device of the first tensor is that of all.
 struct Call {
@@ -94,6 +114,10 @@ PyObject* same(PyObject* o) {
   Py_INCREF(o);
   return o;
 }
+bool put(Ref& tuple, int i, PyObject* o) {
+  if (o) PyTuple_SET_ITEM(tuple.p, i, o);
+  return o != nullptr;
+}
 
 const ssm_kv_cache* cache_at(PyObject* address) {
   return static_cast<const ssm_kv_cache*>(PyLong_AsVoidPtr(address));
@@ -120,16 +144,13 @@ PyObject* rope(PyObject* const* a) {
   if (!c.ok) return not_usual();
   const int64_t Hk = k ? k->size(1) : 0;
   if (Hq > SSM_ATTN_MAX_HEADS || Hk > SSM_ATTN_MAX_HEADS || D > SSM_ATTN_MAX_HEAD_DIM) return not_usual();
-  at::Tensor qo, ko;
-  if (a[6] == Py_None) qo = c.fresh_io(vqo, T, Hq, D);
-  if (k && a[7] == Py_None) ko = c.fresh_io(vko, T, Hk, D);
-  if (f_rope(T, (int32_t)Hq, (int32_t)Hk, (int32_t)D, c.io_code(), &r, &vq, &vqo, k ? &vk : nullptr, k ? &vko : nullptr,
-             c.stream()) != SSM_OK)
-    return not_usual();
-  PyObject* out = PyTuple_New(2);
-  PyTuple_SET_ITEM(out, 0, a[6] == Py_None ? own(std::move(qo)) : same(a[6]));
-  PyTuple_SET_ITEM(out, 1, ko.defined() ? own(std::move(ko)) : same(a[7]));
-  return out;
+  Ref out(PyTuple_New(2));
+  if (!out.p || !put(out, 0, a[6] == Py_None ? own(c.fresh_io(vqo, T, Hq, D)) : same(a[6])) ||
+      !put(out, 1, k && a[7] == Py_None ? own(c.fresh_io(vko, T, Hk, D)) : same(a[7])))
+    return nullptr;
+  return out.after(f_rope(T, (int32_t)Hq, (int32_t)Hk, (int32_t)D, c.io_code(), &r, &vq, &vqo, k ? &vk : nullptr,
+                          k ? &vko : nullptr, c.stream()),
+                   "ssm_rope");
 }
 
 // kv_write(k, v, cache, device, io_only_bf16, slots, q, positions, freq, interleaved, mscale, q_out, k_out)
@@ -155,12 +176,12 @@ PyObject* kv_write(PyObject* const* a) {
   if (!c.ok || !cache_takes(a[4], c.dtype)) return not_usual();
   const int64_t Hq = q ? q->size(1) : 0;
   if (Hq > SSM_ATTN_MAX_HEADS) return not_usual();
-  at::Tensor qo;
-  if (q && a[11] == Py_None) qo = c.fresh_io(vqo, T, Hq, D);
-  if (f_kv_write(T, c.io_code(), cache, slots->const_data_ptr<int64_t>(), &vk, &vv, rotated ? &r : nullptr, (int32_t)Hq,
-                 q ? &vq : nullptr, q ? &vqo : nullptr, a[12] != Py_None ? &vko : nullptr, c.stream()) != SSM_OK)
-    return not_usual();
-  return qo.defined() ? own(std::move(qo)) : same(a[11]);
+  Ref out(q && a[11] == Py_None ? own(c.fresh_io(vqo, T, Hq, D)) : same(a[11]));
+  if (!out.p) return nullptr;
+  return out.after(f_kv_write(T, c.io_code(), cache, slots->const_data_ptr<int64_t>(), &vk, &vv, rotated ? &r : nullptr,
+                              (int32_t)Hq, q ? &vq : nullptr, q ? &vqo : nullptr, a[12] != Py_None ? &vko : nullptr,
+                              c.stream()),
+                   "ssm_kv_write");
 }
 
 // kv_read(cache, device, io_only_bf16, slots, bf16, k_out, v_out)
@@ -176,14 +197,11 @@ PyObject* kv_read(PyObject* const* a) {
   for (int i = 0; i < 2; ++i)
     if (a[5 + i] != Py_None) c.io(a[5 + i], v[i], T, H, D);
   if (!c.ok) return not_usual();
-  at::Tensor out[2];
+  Ref out(PyTuple_New(2));
+  if (!out.p) return nullptr;
   for (int i = 0; i < 2; ++i)
-    if (a[5 + i] == Py_None) out[i] = c.fresh_io(v[i], T, H, D);
-  if (f_kv_read(T, c.io_code(), cache, slots->const_data_ptr<int64_t>(), &v[0], &v[1], c.stream()) != SSM_OK)
-    return not_usual();
-  PyObject* r = PyTuple_New(2);
-  for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(r, i, out[i].defined() ? own(std::move(out[i])) : same(a[5 + i]));
-  return r;
+    if (!put(out, i, a[5 + i] == Py_None ? own(c.fresh_io(v[i], T, H, D)) : same(a[5 + i]))) return nullptr;
+  return out.after(f_kv_read(T, c.io_code(), cache, slots->const_data_ptr<int64_t>(), &v[0], &v[1], c.stream()), "ssm_kv_read");
 }
 
 // scale: a float, or None for 1 / sqrt(D)
@@ -211,8 +229,8 @@ PyObject* attn_prefill(PyObject* const* a) {
   if (!c.ok || cq->size(0) < 2 || !PyBool_Check(a[5]) || D < 1 || D > SSM_ATTN_MAX_HEAD_DIM || Hq > SSM_ATTN_MAX_HEADS ||
       k->size(1) > SSM_ATTN_MAX_HEADS || !scale_of(a[6], D, d.scale))
     return not_usual();
-  at::Tensor out;
-  if (a[7] == Py_None) out = c.fresh_io(vo, T, Hq, D);
+  Ref out(a[7] == Py_None ? own(c.fresh_io(vo, T, Hq, D)) : same(a[7]));
+  if (!out.p) return nullptr;
   d.batch = cq->size(0) - 1;
   d.q_tokens = T;
   d.k_tokens = k->size(0);
@@ -221,10 +239,9 @@ PyObject* attn_prefill(PyObject* const* a) {
   d.head_dim = (int32_t)D;
   d.io_dtype = c.io_code();
   d.causal = a[5] == Py_True;
-  if (f_prefill(&d, &vq, &vk, &vv, cq->const_data_ptr<int32_t>(), ck->const_data_ptr<int32_t>(), &vo,
-                lse ? lse->mutable_data_ptr<float>() : nullptr, c.stream()) != SSM_OK)
-    return not_usual();
-  return out.defined() ? own(std::move(out)) : same(a[7]);
+  return out.after(f_prefill(&d, &vq, &vk, &vv, cq->const_data_ptr<int32_t>(), ck->const_data_ptr<int32_t>(), &vo,
+                             lse ? lse->mutable_data_ptr<float>() : nullptr, c.stream()),
+                   "ssm_attn_prefill");
 }
 
 // attn_decode_step(q, cache, device, io_only_bf16, table, lens, scale, out, lse)
@@ -245,15 +262,15 @@ PyObject* attn_decode_step(PyObject* const* a) {
   if (!c.ok || !cache_takes(a[3], c.dtype) || Hq > SSM_ATTN_MAX_HEADS || !scale_of(a[6], D, scale))
     return not_usual();
   const int64_t W = table->size(1);
-  at::Tensor out, ws;
-  if (a[7] == Py_None) out = c.fresh_io(vo, B, Hq, D);
+  Ref out(a[7] == Py_None ? own(c.fresh_io(vo, B, Hq, D)) : same(a[7]));
+  if (!out.p) return nullptr;
+  at::Tensor ws;
   const size_t need = f_workspace(B, (int32_t)Hq, cache, W);
   if (need) ws = c.fresh({(int64_t)need}, at::kByte);
-  if (f_decode(B, (int32_t)Hq, c.io_code(), scale, cache, &vq, table->const_data_ptr<int32_t>(), W,
-               lens->const_data_ptr<int32_t>(), &vo, lse ? lse->mutable_data_ptr<float>() : nullptr,
-               need ? ws.mutable_data_ptr() : nullptr, need, c.stream()) != SSM_OK)
-    return not_usual();
-  return out.defined() ? own(std::move(out)) : same(a[7]);
+  return out.after(f_decode(B, (int32_t)Hq, c.io_code(), scale, cache, &vq, table->const_data_ptr<int32_t>(), W,
+                            lens->const_data_ptr<int32_t>(), &vo, lse ? lse->mutable_data_ptr<float>() : nullptr,
+                            need ? ws.mutable_data_ptr() : nullptr, need, c.stream()),
+                   "ssm_attn_decode_step");
 }
 
 // describe(address of a cache's description, k, v, k_scale, v_scale): fills it and gives (pages, heads, page_size,
@@ -289,10 +306,10 @@ PyObject* describe(PyObject* const* a) {
                        codes ? Py_None : t == at::kBFloat16 ? Py_True : Py_False);
 }
 
-// bind(rope, kv_write, kv_read, attn_prefill, attn_decode_step, workspace_bytes): addresses
+// bind(rope, kv_write, kv_read, attn_prefill, attn_decode_step, workspace_bytes, raise_status): addresses, and a function
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+  if (nargs != 7) {
+    PyErr_SetString(PyExc_TypeError, "bind takes six addresses and a function");
     return nullptr;
   }
   void* p[6];
@@ -309,6 +326,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   f_prefill = reinterpret_cast<decltype(f_prefill)>(p[3]);
   f_decode = reinterpret_cast<decltype(f_decode)>(p[4]);
   f_workspace = reinterpret_cast<decltype(f_workspace)>(p[5]);
+  Py_INCREF(a[6]);
+  Py_XDECREF(raise_status);
+  raise_status = a[6];
   Py_RETURN_NONE;
 }
 

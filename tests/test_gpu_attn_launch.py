@@ -58,3 +58,47 @@ def test_an_error_left_behind_is_not_the_call_s(native, monkeypatch):
         for a, b in zip(wrote, want):
             same = torch.equal(a, b)
             assert same, f"{name}: not the result of one call"
+
+
+def test_a_launch_error_is_reported_and_not_tried_again(monkeypatch):
+    """The entry points replaced by ones that do nothing but report a failed launch: the native binding calls them once and
+    raises; nothing has been written and the library is not asked again."""
+    assert A._bound() is not A._NoNative, "the native binding is not built"
+    calls, names = [], ["ssm_rope", "ssm_kv_write", "ssm_kv_read", "ssm_attn_prefill", "ssm_attn_decode_step"]
+    i32, i64, f32, vp, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+    arguments = [(i64, i32, i32, i32, i32) + (vp,) * 6, (i64, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp),
+                 (i64, i32) + (vp,) * 5, (vp,) * 9, (i64, i32, i32, f32, vp, vp, vp, i64, vp, vp, vp, vp, size, vp)]
+
+    def failing(name, types):
+        def entry(*args):
+            calls.append(name)
+            return 7  # SSM_ERR_LAUNCH
+        return ctypes.CFUNCTYPE(ctypes.c_int, *types)(entry)
+    stubs = [failing(n, t) for n, t in zip(names, arguments)]
+    ops = operators()
+    before = [[t.clone() for t in wrote] for _, _, wrote in ops]
+    lib, said = A._lib.load(), {}
+
+    class Failing:
+        def __getattr__(self, name):
+            return stubs[names.index(name)] if name in names else getattr(lib, name)
+    A._entry()  # attn.py's own half keeps the library
+    with monkeypatch.context() as m:
+        m.setattr(A._lib, "load", Failing)
+        A._native = None
+        A._bound()
+    try:
+        for name, call, _ in ops:
+            with pytest.raises(ssm.SsmError) as e:
+                call()
+            said[name] = (e.value.status, str(e.value))
+    finally:
+        A._native = None
+        A._bound()  # the library's entry points again
+    assert calls == names
+    for name, (status, text) in said.items():
+        assert status == 7 and name in text and "SSM_ERR_LAUNCH" in text
+    for (name, _, wrote), old in zip(ops, before):
+        assert all(torch.equal(a, b) for a, b in zip(wrote, old)), name
+    ops[0][1]()
+    assert not torch.equal(ops[0][2][0], before[0][0])  # and it rotates again
