@@ -154,11 +154,22 @@ def _view(t: torch.Tensor, name: str, shape, dtype, device):
     return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
 
+def _made(make, stream, device, returned=True):
+    """make()'s tensor, from the memory pool of the stream that writes it: a block of the current stream's pool may still
+    be in use by work queued there, which nothing orders before `stream`'s.  A returned one is used on the
+    current stream, so its memory is not handed out again before that is done with it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _new(like: torch.Tensor, shape, stream):
     """A contiguous output [T, H, D] and its view."""
-    t = like.new_empty(shape)
-    if stream is not None:  # allocated for the current stream, used on another: not to be handed out before that is done
-        t.record_stream(stream)
+    t = _made(lambda: like.new_empty(shape), stream, like.device)
     return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
@@ -402,9 +413,7 @@ def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream
     views, outs = [], []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-            if stream is not None:
-                t.record_stream(stream)
+            t = _made(lambda: torch.empty(shape, dtype=dtype, device=dev), stream, dev)
             views.append((t.data_ptr(), shape[1] * shape[2], shape[2]))
         else:
             views.append(_view(t, name, shape, dtype, dev))
@@ -499,9 +508,7 @@ def attn_decode_step(q, cache: KVCache, table, lens, *, scale: Optional[float] =
     if workspace is None:
         size = _decode_workspace(B, Hq, *cache._sizes(), W)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _made(lambda: torch.empty(size, dtype=torch.uint8, device=dev), stream, dev, returned=False)
             pw = workspace.data_ptr()
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")

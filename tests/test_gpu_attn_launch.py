@@ -102,3 +102,21 @@ def test_a_launch_error_is_reported_and_not_tried_again(monkeypatch):
         assert all(torch.equal(a, b) for a, b in zip(wrote, old)), name
     ops[0][1]()
     assert not torch.equal(ops[0][2][0], before[0][0])  # and it rotates again
+
+
+def test_a_given_stream_s_outputs_are_not_the_current_stream_s_memory():
+    """A block just freed on the current stream, which work queued there may still use, is not what a call on another stream
+    writes to."""
+    q = torch.randn(64, HQ, D, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    cu = torch.tensor([0, 64], dtype=torch.int32, device=DEV)
+    want = ssm.attn_prefill(q, q, q, cu)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    freed = want.clone()
+    at = freed.data_ptr()
+    del freed
+    got = ssm.attn_prefill(q, q, q, cu, stream=s)
+    assert got.data_ptr() != at
+    assert torch.empty_like(got).data_ptr() == at  # it stays the current stream's
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want)
