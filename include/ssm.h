@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 2
+#define SSM_ABI_VERSION 3
 #define SSM_MAX_STATE 16 /* largest supported d_state */
 #define SSM_CONV_WIDTH 4 /* the only supported d_conv */
 #define SSM_MAX_D_INNER (1 << 24) /* largest d_inner of one call */

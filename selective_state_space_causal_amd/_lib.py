@@ -14,7 +14,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssm_san.so" if os.environ.get("SSM_SANITIZE") == "1" else "libssm.so")
 
 SSM_F32, SSM_BF16 = 0, 1
-ABI_VERSION = 2
+ABI_VERSION = 3
 MAX_STATE = 16
 CONV_W = 4
 
@@ -54,6 +54,8 @@ def load(path: str = LIB_PATH):
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     lib.ssm_abi_version.restype = ctypes.c_int
     lib.ssm_abi_version.argtypes = []
+    if lib.ssm_abi_version() != ABI_VERSION:  # before entry points that another version may not have
+        raise ImportError(f"libssm ABI {lib.ssm_abi_version()} != binding ABI {ABI_VERSION}")
     lib.ssm_status_str.restype = ctypes.c_char_p
     lib.ssm_status_str.argtypes = [ctypes.c_int]
     lib.ssm_prefill_workspace_bytes.restype = sz
@@ -108,8 +110,6 @@ def load(path: str = LIB_PATH):
     lib.ssm_calib_read_sink_floats.argtypes = []
     from . import attn
     attn.declare(lib)
-    if lib.ssm_abi_version() != ABI_VERSION:
-        raise ImportError(f"libssm ABI {lib.ssm_abi_version()} != binding ABI {ABI_VERSION}")
     _lib = lib
     return lib
 

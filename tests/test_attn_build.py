@@ -1,8 +1,6 @@
 """The build and the binding's parts, without a GPU: the library does not depend on the binding's native half, and parts of
 another version are refused by name."""
 import ctypes
-import importlib.machinery
-import importlib.util
 import os
 import subprocess
 
@@ -35,3 +33,20 @@ def test_the_library_is_built_where_the_native_half_is_not(monkeypatch, tmp_path
         assert B.build() == str(tmp_path / "LIB.so")
     assert done == [False, True] and (tmp_path / "LIB.so").read_text() == "made"
     assert not os.path.exists(tmp_path / "FAST.so")
+
+
+def test_a_library_of_another_version_is_refused_by_version(monkeypatch, tmp_path):
+    """Before any entry point is looked up that it may not have."""
+    src, so = tmp_path / "old.c", tmp_path / "old.so"
+    src.write_text(f"int ssm_abi_version(void) {{ return {L.ABI_VERSION - 1}; }}\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    monkeypatch.setattr(L, "_lib", None)
+    with pytest.raises(ImportError, match=f"ABI {L.ABI_VERSION - 1}"):
+        L.load(str(so))
+
+
+def test_the_attention_entry_points_have_a_version_of_their_own():
+    """Version 2 is the library without them."""
+    assert L.ABI_VERSION == 3
+    with open(os.path.join(B.ROOT, "include", "ssm.h")) as f:
+        assert "#define SSM_ABI_VERSION 3\n" in f.read()
