@@ -110,12 +110,12 @@ def _bound():
         lib = _lib.load()
         try:
             from . import _attn_fast
-            _attn_fast.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            _attn_fast.bind(lib.ssm_abi_version(), *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
                 "ssm_rope", "ssm_kv_write", "ssm_kv_read", "ssm_attn_prefill", "ssm_attn_decode_step",
                 "ssm_attn_decode_workspace_bytes")), _fail)
             _native = _attn_fast
-        except ImportError as e:
-            warnings.warn(f"the attention calls' native binding is not built ({e}): small calls are slower; run "
+        except (ImportError, TypeError) as e:  # TypeError: built before versions were compared
+            warnings.warn(f"the attention calls' native binding is not built for this library ({e}): small calls are slower; run "
                           "selective_state_space_causal_amd/build.py")
             _native = _NoNative
     return _native

@@ -306,10 +306,16 @@ PyObject* describe(PyObject* const* a) {
                        codes ? Py_None : t == at::kBFloat16 ? Py_True : Py_False);
 }
 
-// bind(rope, kv_write, kv_read, attn_prefill, attn_decode_step, workspace_bytes, raise_status): addresses, and a function
+// bind(version, rope, kv_write, kv_read, attn_prefill, attn_decode_step, workspace_bytes, raise_status): the library's ABI
+// version, which has to be the one that this module fills structures for, addresses, and a function
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes six addresses and a function");
+  if (nargs != 8) {
+    PyErr_SetString(PyExc_TypeError, "bind takes a version, six addresses and a function");
+    return nullptr;
+  }
+  const long version = PyLong_AsLong(*a++);
+  if (version != SSM_ABI_VERSION) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ImportError, "built for libssm ABI %d, not %ld", SSM_ABI_VERSION, version);
     return nullptr;
   }
   void* p[6];

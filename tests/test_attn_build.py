@@ -50,3 +50,22 @@ def test_the_attention_entry_points_have_a_version_of_their_own():
     assert L.ABI_VERSION == 3
     with open(os.path.join(B.ROOT, "include", "ssm.h")) as f:
         assert "#define SSM_ABI_VERSION 3\n" in f.read()
+
+
+def test_a_native_half_of_another_version_is_refused(monkeypatch):
+    """It fills the library's structures by the layout it was compiled with."""
+    from selective_state_space_causal_amd import _attn_fast
+    lib = L.load()
+    entries = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "ssm_rope", "ssm_kv_write", "ssm_kv_read", "ssm_attn_prefill", "ssm_attn_decode_step", "ssm_attn_decode_workspace_bytes")]
+    with pytest.raises(ImportError, match="ABI"):
+        _attn_fast.bind(L.ABI_VERSION + 1, *entries, A._fail)
+    _attn_fast.bind(L.ABI_VERSION, *entries, A._fail)
+
+    for error in (ImportError, TypeError):  # TypeError: of before versions were compared
+        def refuses(*args):
+            raise error("another ABI")
+        monkeypatch.setattr(_attn_fast, "bind", refuses)
+        monkeypatch.setattr(A, "_native", None)
+        with pytest.warns(UserWarning, match="another ABI"):
+            assert A._bound() is A._NoNative
