@@ -202,7 +202,7 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[s
                 fastest kept
       "yarn"    pairs that turn more than beta_fast times over original_max tokens are kept, those that
                 turn less than beta_slow times are slowed by factor, a linear ramp between, and
-                mscale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023)."""
+                mscale = 0.1 ln(factor) + 1 for factors above 1 (Peng et al., "YaRN", 2023)."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
     if not (base > 1.0 and math.isfinite(base)) or not (factor > 0.0 and math.isfinite(factor)):
@@ -222,7 +222,7 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[s
         lo, hi = max(0, math.floor(pair_of(beta_fast))), min(rot_dim - 1, math.ceil(pair_of(beta_slow)))
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         freq = freq / factor * ramp + freq * (1 - ramp)
-        mscale = 0.1 * math.log(factor) + 1.0
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
     elif scaling not in (None, "ntk"):
         raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
     return freq.to(device), mscale
