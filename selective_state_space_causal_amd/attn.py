@@ -207,6 +207,8 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: Optional[s
         raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
     if not (base > 1.0 and math.isfinite(base)) or not (factor > 0.0 and math.isfinite(factor)):
         raise ValueError("base must be above 1 and factor above 0")
+    if scaling is None and factor != 1.0:
+        raise ValueError(f"a factor of {factor} needs a scaling: 'linear', 'ntk' or 'yarn'")
     i = torch.arange(rot_dim // 2, dtype=torch.float64)
     mscale = 1.0
     if scaling == "ntk":
