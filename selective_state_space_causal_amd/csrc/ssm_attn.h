@@ -97,20 +97,27 @@ inline Span view_span(const ssm_view* v, int64_t tokens, int64_t heads, int64_t 
   return span(v->data, ((tokens - 1) * v->token_stride + (heads - 1) * v->head_stride + D) * es);
 }
 
-// Whether two views over the same token and head counts touch a common byte.  Views into one packed
-// projection interleave (q, k and v heads of a token side by side) without sharing a byte: with equal
-// token strides, rows are compared modulo the stride.
+// Whether [pa, pa + wa) and [pb, pb + wb), each repeated at every multiple of `period` bytes, share no byte.
+inline bool apart(const void* pa, int64_t wa, const void* pb, int64_t wb, int64_t period) {
+  if (wa > period || wb > period) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+  const int64_t off = b >= a ? (int64_t)((b - a) % (uintptr_t)period)
+                             : (int64_t)((period - (int64_t)((a - b) % (uintptr_t)period)) % period);
+  return off >= wa && off + wb <= period;  // b's starts past a's, and ends before a's next
+}
+
+// Whether two views may touch a common byte.  Views into one packed projection interleave without sharing one: whole
+// rows of heads, token by token (q, k and v heads of a token in blocks: equal token strides), or single heads (each head's
+// q, k and v next to one another: equal head strides, of which the token strides are multiples).
 inline bool views_overlap(const ssm_view* a, int64_t ta, int64_t ha, const ssm_view* b, int64_t tb, int64_t hb,
                           int64_t D, int64_t es) {
   if (!overlaps(view_span(a, ta, ha, D, es), view_span(b, tb, hb, D, es))) return false;
-  if (a->token_stride != b->token_stride || a->token_stride == 0) return true;
-  const int64_t ts = a->token_stride * es;
-  const int64_t wa = ((ha - 1) * a->head_stride + D) * es, wb = ((hb - 1) * b->head_stride + D) * es;
-  if (wa > ts || wb > ts) return true;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data), pb = reinterpret_cast<uintptr_t>(b->data);
-  const int64_t off = pb >= pa ? (int64_t)((pb - pa) % (uintptr_t)ts)
-                               : (int64_t)((ts - (int64_t)((pa - pb) % (uintptr_t)ts)) % ts);
-  return off < wa || off + wb > ts;  // b's row starts inside a's row, or runs into a's next row
+  const int64_t ts = a->token_stride, hs = a->head_stride;
+  if (ts == b->token_stride && ts > 0 &&
+      apart(a->data, ((ha - 1) * hs + D) * es, b->data, ((hb - 1) * b->head_stride + D) * es, ts * es))
+    return false;
+  return !(hs == b->head_stride && hs > 0 && ts % hs == 0 && b->token_stride % hs == 0 &&
+           apart(a->data, D * es, b->data, D * es, hs * es));
 }
 
 // Whether the rows that a view writes are disjoint (a stride of 0 or too small makes them overlap).
