@@ -393,10 +393,11 @@ def kv_write(k, v, cache: KVCache, slots, *, q=None, positions=None, freq=None, 
 
 
 def kv_read(cache: KVCache, slots, *, dtype=None, k_out=None, v_out=None, stream=None):
-    """ssm_kv_read: the rows at slots [T] int64 as (k, v) [T, Hkv, D] in dtype (the cache's own, or bfloat16
-    for the 8-bit types, where not given); slots out of range read as zeros."""
+    """ssm_kv_read: the rows at slots [T] int64 as (k, v) [T, Hkv, D] in dtype (where not given that of
+    k_out or v_out, else the cache's own, bfloat16 for the 8-bit types); slots out of range read as zeros."""
     if dtype is None:
-        dtype = k_out.dtype if k_out is not None else cache.io_only or torch.bfloat16
+        given = k_out if k_out is not None else v_out
+        dtype = given.dtype if given is not None else cache.io_only or torch.bfloat16
     if stream is None and dtype in _IO:
         r = (_native or _bound()).kv_read(cache.address, cache.index, cache.is_bf16, slots, dtype == torch.bfloat16, k_out,
                                           v_out)

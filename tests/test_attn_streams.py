@@ -105,3 +105,15 @@ def test_workspace_comes_from_the_given_stream_s_pool(streams, calls):
     assert out.shape == (1, 1, 8)
     (ws,) = streams.made
     assert ws.pool == "given"  # used on that stream alone: nothing to wait for
+
+
+def test_rows_are_read_back_in_the_given_output_s_type(streams, calls):
+    """Of either output: v_out alone as well as k_out alone."""
+    f32 = torch.zeros(3, 1, 8)
+    for given in (dict(k_out=f32), dict(v_out=f32)):
+        types = []
+        with pytest.MonkeyPatch.context() as m:
+            m.setattr(A, "_view", lambda t, name, shape, dtype, device: (types.append(dtype), (0, 0, 0))[1])
+            m.setattr(torch, "empty", lambda shape, dtype, device: (types.append(dtype), streams.allocate())[1])
+            A.kv_read(calls, torch.zeros(3, dtype=torch.int64), stream="given", **given)
+        assert types == [torch.float32] * 2, given
