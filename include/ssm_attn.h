@@ -43,8 +43,11 @@
  * run on the matrix cores with fp32 sums; for the product with v, prompt attention rounds a softmax weight
  * to bf16 (2^-8 relative, the size of the output's own rounding), and decode holds it as the sum of two bf16
  * (2^-17).  fp32 inputs keep fp32's accuracy throughout: prompt attention multiplies them as three bf16
- * parts each (what is left out is below 2^-25 of a product; magnitudes up to 2^127), decode on the fp32
- * matrix instructions.  Softmax maxima, sums and the partial results of a split are fp32.
+ * parts each (what is left out is below 2^-25 of a product); decode against an 8-bit cache multiplies q and the
+ * weights as three bf16 parts each (to 2^-27 of them) with the codes, which are exact, and against an fp32 cache on the fp32
+ * matrix instructions.  What is split into parts (q, and k and v of a prompt) has magnitudes up to 2^127, and sums of
+ * products stay below 2^128 before the scale of a cached row and `scale` are applied.  Softmax maxima, sums and the
+ * partial results of a split are fp32.
  *
  * Conventions (ownership, ordering, errors before any HIP call, no allocation, no mutable global
  * state, no host synchronisation, the current device) as in ssm.h.  Index arrays (slots,

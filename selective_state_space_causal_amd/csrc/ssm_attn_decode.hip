@@ -20,8 +20,8 @@
 // The page numbers are read a step ahead, by the scalar unit.
 //
 // 8-bit codes are exact in bf16, so fp32 calls multiply them as bf16 too: q and the weights are split into three bf16,
-// x = h + m + l to 2^-27 of x (each the remainder of the last, rounded), and the three products take a fifth of the time of the
-// fp32 matrix instruction.  A cache of fp32 is multiplied in fp32.
+// x = h + m + l to 2^-27 of x (each the remainder of the last, rounded; |x| up to 2^127), and the three products take a fifth of the
+// time of the fp32 matrix instruction.  A cache of fp32 is multiplied in fp32.
 //
 // The long axis is split into chunks, one workgroup each; its waves take 32 keys in turn and join their
 // results in LDS.  With more than one chunk the partial results (maximum, sum, unnormalised output, fp32)

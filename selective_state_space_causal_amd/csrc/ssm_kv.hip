@@ -31,7 +31,8 @@ struct RowArgs {
 
 // cos and sin of position * freq.  The angle in turns is position * freq / (2 pi), kept as a sum of two
 // fp64 (the products' rounding errors by fused multiply-adds, 1 / (2 pi) as two fp64), so reducing it
-// to [-1/2, 1/2] loses nothing at any position below 2^53; then fp32.
+// to [-1/2, 1/2] loses nothing at any position below 2^53.  Then fp32, as the values that are turned are at most that: 2^-25 of
+// half a turn is 9e-8 radians, and the result's error relative to fp64 grows from 4.2e-8 (cos and sin in fp64, rounded) to 5.3e-8.
 __device__ __forceinline__ void angle(int64_t pos, double freq, float mscale, float& c, float& s) {
 #pragma clang fp contract(off)  // each product below is rounded by itself: its error is taken from it
   constexpr double INV_HI = 0x1.45f306dc9c883p-3, INV_LO = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
