@@ -125,7 +125,9 @@ __device__ __forceinline__ void load_words(unsigned* w, const char* p) {
   }
 }
 
-// Waves of a SIMD.
+// Waves of a SIMD.  Measured on both sides: bf16 (three and two, above), and codes in fp32 past 192 channels.  The others follow
+// from the registers of a step and have no figures of one wave more or less; 129 to 192 channels of codes in fp32 spill 14
+// registers with two waves, past 192 channels an unquantised cache spills 12 (bf16) and 28 (fp32).
 constexpr int waves_of(bool bf16, bool codes, int DP) {
   if (bf16) return DP > 128 ? 2 : 3;
   if (codes) return DP > 192 ? 1 : DP > 64 ? 2 : 3;  // 59 sequences of 818 keys of 256: 37 us, 46 with two

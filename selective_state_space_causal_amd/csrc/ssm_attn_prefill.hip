@@ -446,6 +446,9 @@ void attn_prefill(PrefillArgs a) {
 //   n 1016, k  2000                        419     192      154      134      136
 //   n 2056, k  8192                       1534     697      542      514      491
 //   n  168, k   143                       20.6    15.4     11.6     11.0     14.7
+// 32 rows from memory are taken up to n = 64 (with the mask and 1000 keys or more up to 96 or 128): past 64 of them their workgroups,
+// one to a CU, are more than one round.  The table does not settle that border: at its two ends, n = 64 and 126, four shares of
+// 64 rows are 5 and 23% faster, and nothing between has been measured, nor other channels.
 // Without the mask all tiles of rows are as long, and there is nothing to even out where the tiles are more than the CUs
 // (2500 tokens of 4 heads over one key head, n 79: Eight32 64 us, Four64 32; 2000, n 63: 28 and 27, and of 64 channels 15 and 20).
 enum Shares { Eight32, Four64, Two128, One128, One256 };
