@@ -9,7 +9,8 @@ prompts and for one decoded token per sequence, composed from the operators of a
 
 As with the mixer (layer.py), more than one rank adds its partial outputs outside this library.  The two
 projections are plain library GEMMs (torch.nn.functional.linear): both sides are token-major, a layout that
-the mixer's projections do not have.
+the mixer's projections do not have over a prompt.  (For one token per sequence the layouts coincide, and a caller that
+keeps a Projector can run its two projections around attn.py's calls instead.)
 
 A mixer layer's hidden is [B, L, d_model]; hidden.view(-1, d_model) with row ends at multiples of L is the packed
 form of the same tokens.

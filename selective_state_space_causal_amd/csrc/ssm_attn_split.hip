@@ -277,8 +277,8 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
   }
 }
 
-// Waves of a workgroup: eight, two a SIMD, where registers allow (fp32 rows of 96 and 128 channels with Q in LDS: 1000 tokens of
-// 8 and 2 heads 39.6 to 36.7 us, 4000 of 32 and 8 195 to 178).  fp32 rows of 64 channels fit twice on a CU with four: eight gain
+// Waves of a workgroup: eight, two a SIMD, where registers allow (fp32 rows of 96 and 128 channels with Q in LDS: four waves
+// to eight, 1000 tokens of 8 and 2 heads 39.6 to 36.7 us, four prompts of up to 1000 of 32 and 8 195 to 178).  fp32 rows of 64 channels fit twice on a CU with four: eight gain
 // 10% while the tiles leave CUs half empty, and lose 25 to 60% after.
 template <typename IO, int DP>
 void launch_dp(const PrefillArgs& a, hipStream_t s) {
