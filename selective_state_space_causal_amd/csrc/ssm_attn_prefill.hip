@@ -281,6 +281,8 @@ void attn_prefill(PrefillArgs a) {
         s[i / 16][i % 16] = x;
         l += x;  // this half's keys only; joined at the end
       };
+      // A weight is rounded to bf16 once, 2^-8 of it at most, as much as the output's own rounding (with fp32 weights a ragged batch is
+      // off by 1.6e-3 instead of 2.0e-3); a second bf16 of each, as decode has, would be half as many products again, which bound this.
       const auto packed = [&](int g) {
         u32x4 p;
 #pragma unroll

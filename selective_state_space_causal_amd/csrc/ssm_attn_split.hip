@@ -200,7 +200,7 @@ __global__ __launch_bounds__(NW * 64, NW / 4) void attn_split(PrefillArgs a) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {  // 16 keys: this half holds keys 4 half + {0..3, 8..11} of them
         if constexpr (BF) {
-          u32x4 pf;
+          u32x4 pf;  // weights rounded to bf16 once, as in attn_prefill: a call's form does not change its precision
 #pragma unroll
           for (int i = 0; i < 4; ++i) pf[i] = pack_bf16(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
 #pragma unroll

@@ -39,3 +39,15 @@ def test_groups_in_turn_written_and_rotated_in_place(T):
         assert torch.equal(x[:, :, i], before[:, :, i])
     ck, cv = ssm.kv_read(c, torch.arange(T, device=DEV))
     assert torch.equal(ck, want) and torch.equal(cv, before[:, :, G + 1])
+
+
+def test_a_block_of_no_tokens():
+    """attn_block_prefill of an empty batch of prompts."""
+    from selective_state_space_causal_amd import attn_layer
+    H, D, d_model = 2, 64, 128
+    w = {"qkv": torch.zeros(3 * H * D, d_model, dtype=torch.bfloat16, device=DEV), "out": torch.zeros(d_model, H * D, dtype=torch.bfloat16, device=DEV)}
+    c = ssm.KVCache.allocate(2, 16, H, D, torch.int8, DEV)
+    none = torch.empty(0, dtype=torch.int64, device=DEV)
+    out = attn_layer.attn_block_prefill(torch.empty(0, d_model, dtype=torch.bfloat16, device=DEV), w, H, c, none,
+                                        torch.tensor([0, 0], dtype=torch.int32, device=DEV), none, ssm.rope_frequencies(D, device=DEV)[0])
+    assert out.shape == (0, d_model)
