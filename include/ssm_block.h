@@ -1,0 +1,124 @@
+/*
+ * ssm_block.h -- C ABI of the operators between a stack's residual stream and its mixers' projections,
+ * on AMD Instinct MI355X (gfx950).  Part of libssm.so.
+ *
+ * A block of a stack (a selective-SSM mixer, ssm_layer.h, or an attention block, ssm_attn.h) starts with
+ * the sum of the residual stream and a norm, and its input and output projections are most of the bytes
+ * that a decoded token reads.  One rank runs there:
+ *   ssm_rms_norm           the residual's addition and the root-mean-square norm, in the io dtype or in
+ *                          8 bits with a scale per token
+ *   ssm_q4_quantize        a projection's weight in 4 bits with a power of two for each 32 values
+ *   ssm_q4_dequantize      such a weight back in the io dtype
+ *   ssm_q4_linear          products of tokens with such a weight
+ *
+ * Formulas.
+ *   norm       h = x + residual, summed in fp32 and rounded once to the residual's dtype (h = x where
+ *              there is no residual); r = 1 / sqrt(mean(h^2) + eps); y = (h * weight) * r, fp32, rounded
+ *              once to the output's dtype.  (h^2 is fp32: magnitudes stay below 2^63.)
+ *   8-bit rows one fp32 scale per row: amax = max |y|, s = amax * (1 / 448), m = (1 / amax) * 448 (each
+ *              operation rounded to fp32); code = e4m3 of clamp(y * m, -448, 448), nearest even; value =
+ *              code * s.  Rows with amax < 2^-100 get s = 0 and codes 0.  (The rows of the key/value
+ *              cache in ssm_attn.h are made alike.)
+ *   4-bit      w[m, k] = c * 2^(e - 127): c one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (e2m1:
+ *              sign, two bits of exponent, one of mantissa, in code order), e a byte for each 32 values of
+ *              a row (k / 32).  Quantising: amax = max |w| of the group, rounded to three significant bits
+ *              (half away from zero, bit pattern + 2^21), falls in 2^n .. 2^(n+1); e = n - 2 + 127, at most
+ *              252; code = w * 2^(127 - e) to nearest, ties to the even code, at most 6 in magnitude.
+ *              Groups with amax < 2^-100 get codes 0 and e = 127; what rounds to zero keeps its sign.  Every value is exact in bf16 for e in
+ *              [2, 252]; other bytes are outside the contract.
+ *   linear     out[t, m] = x_scale[t] * sum_k x[t, k] w[m, k] (no x_scale for bf16 and fp32 tokens), sums
+ *              in fp32.  Products are exact: bf16 tokens (and e4m3 tokens widened to it) multiply the
+ *              exact 4-bit values on the matrix cores, fp32 tokens as three bf16 parts (to 2^-27 of them;
+ *              magnitudes up to 2^127).  e4m3 tokens with an output in bf16 go through the instruction
+ *              that takes 8- and 4-bit values as they are: it aligns the products of eight columns to the
+ *              largest and drops what is below 2^-13 of it.
+ *              No sum is split differently from one call to the next: a call's bits depend on its sizes
+ *              and values alone.
+ *
+ * 4-bit layout, for W [M, K] row-major in the formulas (M = out_features, K = in_features):
+ *   codes  [ceil(M / 16), ceil(K / 128), 64, 16] bytes: tile (m / 16, k / 128), in it lane
+ *          (k % 128) / 32 * 16 + m % 16, in it byte (k % 32) / 2, low nibble for even k
+ *   scales [ceil(M / 16), ceil(K / 512), 64, 4] bytes: tile (m / 16, k / 512), the same lane, byte
+ *          (k / 128) % 4
+ * Places past M hold anything; places past K hold codes 0 and scales 127 (ssm_q4_quantize writes both so).
+ * A tile is what one wave loads at once, and a lane's 16 bytes one group: the operand
+ * layout of the matrix instruction that takes 4-bit values and a scale for each lane.
+ *
+ * Rows.  A [T, D] tensor is a base pointer and a row stride in elements (ssm_rows), the D values of a row
+ * contiguous.  Row strides lie in [0, 2^22] (written rows may not overlap: at least D where T > 1).
+ * Alignment: bases and row strides multiples of 16 bytes (8 bytes for e4m3 rows that ssm_rms_norm writes;
+ * out of ssm_q4_linear: its dtype's own size).
+ *
+ * Conventions (ownership, ordering, errors before any HIP call, no allocation, no mutable global state,
+ * no host synchronisation, the current device) as in ssm.h.  Outputs may not overlap inputs or each
+ * other, except where said.  0 tokens: a call that does nothing.  Non-finite inputs are outside the
+ * contract; a row's values stay in that row.
+ */
+#ifndef SSM_BLOCK_H
+#define SSM_BLOCK_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ssm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SSM_E4M3 2                /* beside ssm_dtype's SSM_F32 and SSM_BF16: rows in 8 bits */
+#define SSM_NORM_MAX_WIDTH 32768
+#define SSM_Q4_GROUP 32
+#define SSM_Q4_MAX_FEATURES (1 << 20) /* largest in_features and out_features; their product at most 2^38 */
+
+/* A [T, D] tensor on the device; the stride in elements. */
+typedef struct {
+  void* data;
+  int64_t stride;
+} ssm_rows;
+
+/* A 4-bit weight on the device (layout above). */
+typedef struct {
+  void* codes;  /* ssm_q4_codes_bytes() */
+  void* scales; /* ssm_q4_scales_bytes() */
+  int64_t out_features; /* M in [1, SSM_Q4_MAX_FEATURES] */
+  int64_t in_features;  /* K, a multiple of 16 in [16, SSM_Q4_MAX_FEATURES] */
+} ssm_q4_weight;
+
+/*
+ * x [tokens, width] (io_dtype SSM_F32 or SSM_BF16), weight fp32 [width], width a multiple of 8 up to
+ * SSM_NORM_MAX_WIDTH; eps finite and > 0.
+ * residual, residual_out [tokens, width] in residual_dtype (io_dtype, or SSM_F32): both or neither (NULL).
+ * residual_out may be residual itself (in place: same data and stride).
+ * out [tokens, width] in out_dtype: io_dtype, or SSM_E4M3 with scale fp32 [tokens] (NULL otherwise).
+ * out may be x itself where out_dtype is io_dtype.
+ */
+int ssm_rms_norm(int64_t tokens, int64_t width, int32_t io_dtype, int32_t residual_dtype, int32_t out_dtype, float eps,
+                 const ssm_rows* x, const float* weight, const ssm_rows* residual, const ssm_rows* residual_out,
+                 const ssm_rows* out, float* scale, void* stream);
+
+/* Bytes of a weight's codes and scales (0 for invalid sizes). */
+size_t ssm_q4_codes_bytes(int64_t out_features, int64_t in_features);
+size_t ssm_q4_scales_bytes(int64_t out_features, int64_t in_features);
+
+/* w [M, K] in io_dtype into q (every byte of codes and scales is written). */
+int ssm_q4_quantize(int32_t io_dtype, const ssm_rows* w, const ssm_q4_weight* q, void* stream);
+
+/* q back into w [M, K] in io_dtype. */
+int ssm_q4_dequantize(int32_t io_dtype, const ssm_q4_weight* q, const ssm_rows* w, void* stream);
+
+/* Device workspace in bytes that ssm_q4_linear needs (0 = none, or invalid sizes). */
+size_t ssm_q4_linear_workspace_bytes(int64_t tokens, int32_t x_dtype, int64_t out_features, int64_t in_features);
+
+/*
+ * out [tokens, M] (out_dtype SSM_F32 or SSM_BF16) from x [tokens, K] (x_dtype SSM_F32, SSM_BF16, or SSM_E4M3 with
+ * x_scale fp32 [tokens]; NULL otherwise).  tokens below 2^24, tokens * M at most 2^36.  The workspace (16-byte aligned) needs no
+ * initialisation; calls that may run at the same time need one each.
+ */
+int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype, const ssm_rows* x, const float* x_scale,
+                  const ssm_q4_weight* q, const ssm_rows* out, void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* SSM_BLOCK_H */

@@ -108,8 +108,9 @@ def load(path: str = LIB_PATH):
     lib.ssm_calib_read.argtypes = [vp, sz, vp, vp]
     lib.ssm_calib_read_sink_floats.restype = sz
     lib.ssm_calib_read_sink_floats.argtypes = []
-    from . import attn
+    from . import attn, block
     attn.declare(lib)
+    block.declare(lib)
     _lib = lib
     return lib
 

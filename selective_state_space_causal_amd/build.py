@@ -1,5 +1,5 @@
-"""Build libssm.so (the C ABI of include/ssm.h) from csrc/*.hip for gfx950 with hipcc, and _attn_fast.so, the
-native half of attn.py, from csrc/attn_binding.cpp."""
+"""Build libssm.so (the C ABI of include/ssm.h) from csrc/*.hip for gfx950 with hipcc, and _attn_fast.so and
+_block_fast.so, the native halves of attn.py and block.py, from csrc/attn_binding.cpp and csrc/block_binding.cpp."""
 from __future__ import annotations
 
 import glob
@@ -25,29 +25,34 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 LINK_LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
 
 
-# The native half of attn.py's binding (host code only; torch's headers).
+# The native halves of attn.py's and block.py's bindings (host code only; torch's headers).
 FAST = os.path.join(PKG, "_attn_fast.so")
-FAST_SRC = os.path.join(CSRC, "attn_binding.cpp")
 
 
-def build_binding(verbose: bool = False) -> str:
+def bindings():
+    """(source, extension) of each; all beside the first."""
+    return ((os.path.join(CSRC, "attn_binding.cpp"), FAST),
+            (os.path.join(CSRC, "block_binding.cpp"), os.path.join(os.path.dirname(FAST), "_block_fast.so")))
+
+
+def build_binding(src: str, out: str, verbose: bool = False) -> str:
     import sysconfig
 
     from torch.utils import cpp_extension
 
     lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
-    tmp = FAST + ".tmp"
+    tmp = out + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            *[x for p in (*cpp_extension.include_paths(), "/opt/rocm/include") for x in ("-isystem", p)],
-           "-I", sysconfig.get_paths()["include"], FAST_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu",
            "-ltorch_python", f"-Wl,-rpath,{os.path.realpath(lib)}"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {FAST_SRC}:\n{r.stderr}")
-    os.replace(tmp, FAST)
-    return FAST
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
 
 
 def hipcc() -> str:
@@ -94,7 +99,7 @@ def build(verbose: bool = False, jobs: int = 8, sanitize: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        binding = None if sanitize else ex.submit(build_binding, verbose)
+        halves = [] if sanitize else [(out, ex.submit(build_binding, src, out, verbose)) for src, out in bindings()]
         objs = list(ex.map(compile_one, sources()))
     out = SAN_LIB if sanitize else LIB
     tmp = out + ".tmp"
@@ -108,10 +113,12 @@ def build(verbose: bool = False, jobs: int = 8, sanitize: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True, capture_output=not verbose)
     os.replace(tmp, out)
-    if binding is not None and binding.exception() is not None:  # attn.py does without it
-        if os.path.exists(FAST):
-            os.remove(FAST)  # of an earlier build
-        warnings.warn(f"the attention calls' native binding is not built, small calls are slower: {binding.exception()}")
+    for half, made in halves:
+        if made.exception() is not None:  # its Python half does without it
+            if os.path.exists(half):
+                os.remove(half)  # of an earlier build
+            warnings.warn(f"{os.path.basename(half)}, a native half of the binding, is not built, small calls are slower: "
+                          f"{made.exception()}")
     return out
 
 

@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/ssm_attn.h"
+#include "binding.h"
 
 namespace {
 
@@ -26,27 +27,6 @@ decltype(&ssm_kv_read) f_kv_read;
 decltype(&ssm_attn_prefill) f_prefill;
 decltype(&ssm_attn_decode_step) f_decode;
 decltype(&ssm_attn_decode_workspace_bytes) f_workspace;
-
-PyObject* raise_status;  // attn.py's function of a name and a status that raises
-
-PyObject* not_usual() { Py_RETURN_NOTIMPLEMENTED; }
-
-// A Python object of a call's own, given back unless the call succeeds.  Outputs are made before the launch, so that
-// nothing can go wrong after it.
-struct Ref {
-  PyObject* p;
-  explicit Ref(PyObject* object) : p(object) {}
-  Ref(const Ref&) = delete;
-  ~Ref() { Py_XDECREF(p); }
-  // What to answer for the status that entry point `name` returned; every refusal comes before any launch.
-  PyObject* after(int status, const char* name) {
-    if (status == SSM_ERR_LAUNCH) return PyObject_CallFunction(raise_status, "si", name, status);
-    if (status != SSM_OK) return not_usual();
-    PyObject* r = p;
-    p = nullptr;
-    return r;
-  }
-};
 
 // A call is usual until something is not; the device of the first tensor is that of all.
 struct Call {
@@ -108,16 +88,6 @@ struct Call {
                       (float)PyFloat_AS_DOUBLE(mscale)};
   }
 };
-
-PyObject* own(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
-PyObject* same(PyObject* o) {
-  Py_INCREF(o);
-  return o;
-}
-bool put(Ref& tuple, int i, PyObject* o) {
-  if (o) PyTuple_SET_ITEM(tuple.p, i, o);
-  return o != nullptr;
-}
 
 const ssm_kv_cache* cache_at(PyObject* address) {
   return static_cast<const ssm_kv_cache*>(PyLong_AsVoidPtr(address));
@@ -338,20 +308,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   Py_RETURN_NONE;
 }
 
-// No C++ exception passes into the interpreter: what went wrong (memory that ran out) goes wrong again in attn.py.
-template <PyObject* (*F)(PyObject* const*), int N>
-PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != N) return not_usual();
-  try {
-    return F(a);
-  } catch (...) {
-    return not_usual();
-  }
-}
-
-PyMethodDef method(const char* name, PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
-  return PyMethodDef{name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr};
-}
 PyMethodDef methods[] = {method("bind", bind),
                          method("describe", guarded<describe, 5>),
                          method("rope", guarded<rope, 8>),

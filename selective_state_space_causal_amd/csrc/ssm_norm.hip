@@ -1,0 +1,256 @@
+// ssm_norm.hip -- ssm_rms_norm of include/ssm_block.h: h = x + residual, y = (h * weight) / rms(h), in the io dtype or in
+// 8 bits with a scale per row.
+//
+// One pass over the data: a row stays in the registers of the threads that share it (P pieces of 8 values each) from its
+// loads to its stores, so that every value is read and written once.  The call is bound by memory for many rows and by
+// its latency (a load, one reduction, a store) for few.  The sum of h^2 and the largest |h * weight| go through one
+// reduction: r > 0, and rounding keeps order, so max |(h * weight) * r| is exactly (max |h * weight|) * r.
+//
+// Threads to a row: a wave for up to 1024 values (no barrier), else 256 to 1024 threads; a call of few rows takes the form
+// with one piece to a thread, whose chain from the first load to the last store is shortest.  A workgroup takes rows in
+// turn and loads the next one before it reduces this one.
+#include "ssm_block.h"
+
+namespace ssm {
+namespace block {
+namespace {
+
+struct NormArgs {
+  Rows x, res, res_out, out;
+  const float* w;
+  float* scale;
+  int64_t T;
+  int W;
+  float eps;
+};
+
+enum { NO_RES = 0, IO_RES = 1, F32_RES = 2 };
+
+// Eight values as they lie in memory.
+template <typename IO>
+struct Piece {
+  u32x4 v[sizeof(IO) / 2];
+  __device__ __forceinline__ void load(const char* p) {
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(IO) / 2; ++i) v[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(IO) == 4)
+      return __uint_as_float(v[i / 4][i % 4]);
+    else
+      return __uint_as_float(i % 2 ? v[0][i / 2] & 0xFFFF0000u : v[0][i / 2] << 16);
+  }
+};
+
+template <typename IO>
+__device__ __forceinline__ void store8(char* p, const float (&y)[8]) {
+  if constexpr (sizeof(IO) == 4) {
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{y[0], y[1], y[2], y[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{y[4], y[5], y[6], y[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(p) =
+        u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+  }
+}
+
+__device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
+  const auto in = [](float x) { return fminf(fmaxf(x, -448.0f), 448.0f); };
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(in(a), in(b), 0, false);
+  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(in(c), in(d), w, true);
+}
+
+// TPR threads to a row, P pieces of 8 values to a thread; workgroups of max(256, TPR) threads.
+template <typename IO, int RES, bool Q8, int TPR, int P>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs a) {
+  using R = typename std::conditional<RES == F32_RES, float, IO>::type;
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1, NW = TPR / 64;
+  constexpr bool AHEAD = P <= 2;  // more pieces leave no registers for the next row
+  __shared__ float red[2][2][NW];
+  const int tid = threadIdx.x % TPR;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+
+  bool in[P];
+  float w[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    in[p] = (p * TPR + tid) * 8 < a.W;
+    if (AHEAD && in[p]) {
+      const float* wp = a.w + (p * TPR + tid) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[p][i] = wp[i];
+    }
+  }
+  Piece<IO> x[P];
+  Piece<R> s[P];
+  const auto load = [&](int64_t r) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (in[p]) {
+        const int64_t e = (p * TPR + tid) * 8;
+        x[p].load(a.x.p + r * a.x.stride + e * sizeof(IO));
+        if constexpr (RES != NO_RES) s[p].load(a.res.p + r * a.res.stride + e * sizeof(R));
+      }
+  };
+  if (row < a.T) load(row);
+  for (int par = 0; row < a.T; row += step, par ^= 1) {
+    float h[P][8], ss = 0.0f, mx = 0.0f;
+    if (!AHEAD && row >= step) load(row);  // the first was loaded above
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (!in[p]) continue;
+      const int64_t e = (p * TPR + tid) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[p][i] = x[p][i];
+        if constexpr (RES != NO_RES) h[p][i] += s[p][i];
+      }
+      if constexpr (RES != NO_RES) {
+        if constexpr (sizeof(R) == 2) {  // the norm is of the stream as it is stored
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const unsigned b = pack_bf16(h[p][i], h[p][i + 1]);
+            h[p][i] = __uint_as_float(b << 16), h[p][i + 1] = __uint_as_float(b & 0xFFFF0000u);
+          }
+        }
+        store8<R>(a.res_out.p + row * a.res_out.stride + e * sizeof(R), h[p]);
+      }
+      if constexpr (!AHEAD) {
+        const float* wp = a.w + e;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[p][i] = wp[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(h[p][i], h[p][i], ss);
+        h[p][i] *= w[p][i];
+        if constexpr (Q8) mx = fmaxf(mx, fabsf(h[p][i]));
+      }
+    }
+    if (AHEAD && row + step < a.T) load(row + step);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      ss += __shfl_xor(ss, off, 64);
+      if constexpr (Q8) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+    }
+    if constexpr (NW > 1) {  // rows alternate between two buffers: one barrier a row
+      if (tid % 64 == 0) {
+        red[par][0][tid / 64] = ss;
+        if constexpr (Q8) red[par][1][tid / 64] = mx;
+      }
+      __syncthreads();
+      ss = red[par][0][0];
+      if constexpr (Q8) mx = red[par][1][0];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) {
+        ss += red[par][0][i];
+        if constexpr (Q8) mx = fmaxf(mx, red[par][1][i]);
+      }
+    }
+    const float r = __builtin_amdgcn_rsqf(ss / (float)a.W + a.eps);
+    float m = 0.0f;
+    if constexpr (Q8) {
+      const float amax = mx * r;
+      const bool live = amax >= 0x1p-100f;
+      m = live ? (1.0f / amax) * 448.0f : 0.0f;
+      if (tid == 0) a.scale[row] = live ? amax * (1.0f / 448.0f) : 0.0f;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (!in[p]) continue;
+      const int64_t e = (p * TPR + tid) * 8;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = h[p][i] * r;
+      if constexpr (Q8)
+        *reinterpret_cast<u32x2*>(a.out.p + row * a.out.stride + e) =
+            u32x2{codes4(y[0] * m, y[1] * m, y[2] * m, y[3] * m), codes4(y[4] * m, y[5] * m, y[6] * m, y[7] * m)};
+      else
+        store8<IO>(a.out.p + row * a.out.stride + e * sizeof(IO), y);
+    }
+  }
+}
+
+template <typename IO, int RES, bool Q8, int TPR, int P>
+hipError_t launch(const NormArgs& a, hipStream_t s) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1, TPB = TPR < 256 ? 256 : TPR;
+  const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * (2048 / TPB);  // 2048 threads to a CU
+  rms_rows<IO, RES, Q8, TPR, P><<<dim3((unsigned)(want < most ? want : most)), dim3(TPB), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename IO, int RES, bool Q8>
+hipError_t launch_width(const NormArgs& a, hipStream_t s) {
+  const bool few = a.T <= 512;
+  if (a.W <= 512) return launch<IO, RES, Q8, 64, 1>(a, s);
+  if (a.W <= 1024 && !few) return launch<IO, RES, Q8, 64, 2>(a, s);
+  if (a.W <= 2048) return launch<IO, RES, Q8, 256, 1>(a, s);
+  if (a.W <= 4096) return few ? launch<IO, RES, Q8, 512, 1>(a, s) : launch<IO, RES, Q8, 256, 2>(a, s);
+  if (a.W <= 8192) return few ? launch<IO, RES, Q8, 1024, 1>(a, s) : launch<IO, RES, Q8, 512, 2>(a, s);
+  if (a.W <= 16384) return launch<IO, RES, Q8, 1024, 2>(a, s);
+  return launch<IO, RES, Q8, 1024, 4>(a, s);
+}
+
+template <typename IO>
+hipError_t launch_norm(const NormArgs& a, int res, bool q8, hipStream_t s) {
+  if (res == NO_RES) return q8 ? launch_width<IO, NO_RES, true>(a, s) : launch_width<IO, NO_RES, false>(a, s);
+  if (res == IO_RES) return q8 ? launch_width<IO, IO_RES, true>(a, s) : launch_width<IO, IO_RES, false>(a, s);
+  if constexpr (sizeof(IO) == 2)
+    return q8 ? launch_width<IO, F32_RES, true>(a, s) : launch_width<IO, F32_RES, false>(a, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace block
+}  // namespace ssm
+
+extern "C" int ssm_rms_norm(int64_t tokens, int64_t width, int32_t io_dtype, int32_t residual_dtype, int32_t out_dtype,
+                            float eps, const ssm_rows* x, const float* weight, const ssm_rows* residual,
+                            const ssm_rows* residual_out, const ssm_rows* out, float* scale, void* stream) {
+  using namespace ssm::block;
+  if (tokens < 0 || tokens > INT32_MAX || width < 8 || width > SSM_NORM_MAX_WIDTH || width % 8) return SSM_ERR_SHAPE;
+  if (!(eps > 0.0f) || !isfinite(eps)) return SSM_ERR_SHAPE;
+  if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  if (out_dtype != io_dtype && out_dtype != SSM_E4M3) return SSM_ERR_DTYPE;
+  if (residual && residual_dtype != io_dtype && residual_dtype != SSM_F32) return SSM_ERR_DTYPE;
+  const bool q8 = out_dtype == SSM_E4M3;
+  if (tokens == 0) return SSM_OK;  // its tensors have no addresses
+  if ((residual == nullptr) != (residual_out == nullptr) || q8 != (scale != nullptr)) return SSM_ERR_NULL;
+  const int64_t T = tokens, W = width, es = size_of(io_dtype), rs = size_of(residual_dtype), os = size_of(out_dtype);
+  if (!weight) return SSM_ERR_NULL;
+  if (const int st = check_rows(x, es, 16)) return st;
+  if (const int st = check_rows(out, os, q8 ? 8 : 16)) return st;
+  if (residual) {
+    if (const int st = check_rows(residual, rs, 16)) return st;
+    if (const int st = check_rows(residual_out, rs, 16)) return st;
+  }
+  if (!aligned(weight, 16) || (q8 && !aligned(scale, 4))) return SSM_ERR_ALIGN;
+  const Span sw = span(weight, W * 4), ss = span(scale, q8 ? T * 4 : 0);
+  const auto clear = [&](const ssm_rows* o, int64_t e) {  // of the weight and the scales
+    const Span so = rows_span(o, T, W, e);
+    return writable(o, T, W) && !overlaps(so, sw) && !overlaps(so, ss);
+  };
+  if (!clear(out, os) || overlaps(ss, sw) || overlaps(ss, rows_span(x, T, W, es))) return SSM_ERR_ALIAS;
+  if (!(same_rows(out, x) && !q8) && rows_overlap(out, W, os, x, W, es, T)) return SSM_ERR_ALIAS;
+  if (residual) {
+    if (!clear(residual_out, rs) || overlaps(ss, rows_span(residual, T, W, rs))) return SSM_ERR_ALIAS;
+    if (rows_overlap(residual_out, W, rs, x, W, es, T) || rows_overlap(residual_out, W, rs, out, W, os, T) ||
+        rows_overlap(residual, W, rs, out, W, os, T))
+      return SSM_ERR_ALIAS;
+    if (!same_rows(residual_out, residual) && rows_overlap(residual_out, W, rs, residual, W, rs, T)) return SSM_ERR_ALIAS;
+  }
+  NormArgs a = {};
+  a.x = rows_of(x, es);
+  a.res = rows_of(residual, rs);
+  a.res_out = rows_of(residual_out, rs);
+  a.out = rows_of(out, os);
+  a.w = weight;
+  a.scale = scale;
+  a.T = T;
+  a.W = (int)W;
+  a.eps = eps;
+  const int res = !residual ? NO_RES : residual_dtype == io_dtype ? IO_RES : F32_RES;
+  const hipStream_t s = ready(stream);
+  const hipError_t e = io_dtype == SSM_BF16 ? launch_norm<ssm::bf16_t>(a, res, q8, s) : launch_norm<float>(a, res, q8, s);
+  return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
+}
