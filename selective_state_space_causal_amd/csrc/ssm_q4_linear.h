@@ -12,7 +12,9 @@ struct LinearArgs {
   const char* codes;
   const char* scales;
   const float* x_scale;  // e4m3 tokens
-  float* partial;        // [splits, T, M] sums of parts of K
+  float* partial;        // [splits, T, Mp] sums of parts of K
+  int64_t Mp;            // M, a multiple of 4
+  bool wide;             // output rows are aligned to 16 bytes
   int64_t T, M, K, kt, k4;  // tiles along K: of 128 and of 512 columns
   int64_t mt;               // tiles of 16 rows
 };
@@ -74,7 +76,7 @@ __device__ __forceinline__ void three_parts(const float (&x)[8], bf16x8 (&p)[3])
 // Few tokens: ssm_q4_rows.hip.  Any number: ssm_q4_tiles.hip.
 constexpr int64_t ROWS_MAX_TOKENS = 16;
 hipError_t launch_q4_rows(const LinearArgs& a, int x_dtype, int out_dtype, hipStream_t s);
-hipError_t launch_q4_tiles(const LinearArgs& a, int x_dtype, int out_dtype, int splits, hipStream_t s);
+hipError_t launch_q4_tiles(const LinearArgs& a, int x_dtype, int out_dtype, hipStream_t s);
 int q4_tiles_splits(int64_t T, int x_dtype, int64_t M, int64_t K);
 
 }  // namespace block
