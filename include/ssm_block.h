@@ -107,16 +107,12 @@ int ssm_q4_quantize(int32_t io_dtype, const ssm_rows* w, const ssm_q4_weight* q,
 /* q back into w [M, K] in io_dtype. */
 int ssm_q4_dequantize(int32_t io_dtype, const ssm_q4_weight* q, const ssm_rows* w, void* stream);
 
-/* Device workspace in bytes that ssm_q4_linear needs (0 = none, or invalid sizes). */
-size_t ssm_q4_linear_workspace_bytes(int64_t tokens, int32_t x_dtype, int64_t out_features, int64_t in_features);
-
 /*
  * out [tokens, M] (out_dtype SSM_F32 or SSM_BF16) from x [tokens, K] (x_dtype SSM_F32, SSM_BF16, or SSM_E4M3 with
- * x_scale fp32 [tokens]; NULL otherwise).  tokens below 2^24, tokens * M at most 2^36.  The workspace (16-byte aligned) needs no
- * initialisation; calls that may run at the same time need one each.
+ * x_scale fp32 [tokens]; NULL otherwise).  tokens below 2^24, tokens * M at most 2^36.
  */
 int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype, const ssm_rows* x, const float* x_scale,
-                  const ssm_q4_weight* q, const ssm_rows* out, void* workspace, size_t workspace_bytes, void* stream);
+                  const ssm_q4_weight* q, const ssm_rows* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,4 +16,4 @@ from ._lib import (PROJ_DT, PROJ_IN, PROJ_OUT, PROJ_X, Projector, SsmError, conv
                    prefill_pool, q8_dequant_sum, q8_num_blocks, q8_quantize, workspace_bytes)
 from .attn import (KVCache, attn_decode_step, attn_decode_workspace_bytes, attn_prefill, kv_read, kv_write,  # noqa: F401
                    rope, rope_frequencies)
-from .block import (Q4Weight, q4_dequantize, q4_linear, q4_linear_workspace_bytes, q4_quantize, rms_norm)  # noqa: F401
+from .block import Q4Weight, q4_dequantize, q4_linear, q4_quantize, rms_norm  # noqa: F401

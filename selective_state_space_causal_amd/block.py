@@ -7,7 +7,6 @@ fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import warnings
 from typing import NamedTuple, Optional
 
@@ -53,10 +52,8 @@ def declare(lib):
     lib.ssm_q4_quantize.argtypes = [i32, pr, pq, vp]
     lib.ssm_q4_dequantize.restype = ctypes.c_int
     lib.ssm_q4_dequantize.argtypes = [i32, pq, pr, vp]
-    lib.ssm_q4_linear_workspace_bytes.restype = sz
-    lib.ssm_q4_linear_workspace_bytes.argtypes = [i64, i32, i64, i64]
     lib.ssm_q4_linear.restype = ctypes.c_int
-    lib.ssm_q4_linear.argtypes = [i64, i32, i32, pr, vp, pq, pr, vp, sz, vp]
+    lib.ssm_q4_linear.argtypes = [i64, i32, i32, pr, vp, pq, pr, vp]
 
 
 def _fail(name, st):
@@ -82,7 +79,7 @@ def _bound():
         try:
             from . import _block_fast
             _block_fast.bind(lib.ssm_abi_version(), *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-                "ssm_rms_norm", "ssm_q4_linear", "ssm_q4_linear_workspace_bytes")), _fail)
+                "ssm_rms_norm", "ssm_q4_linear")), _fail)
             _native = _block_fast
         except ImportError as e:
             warnings.warn(f"the block calls' native binding is not built for this library ({e}): small calls are slower; run "
@@ -126,8 +123,8 @@ def _vector(t: torch.Tensor, name: str, n: int, device):
                      f"{tuple(t.shape)} on {t.device}")
 
 
-def _empty(shape, dtype, device, stream, returned=True):
-    return _made(lambda: torch.empty(shape, dtype=dtype, device=device), stream, device, returned)
+def _empty(shape, dtype, device, stream):
+    return _made(lambda: torch.empty(shape, dtype=dtype, device=device), stream, device)
 
 
 # ---------------------------------------------------------------- the residual norm
@@ -277,20 +274,11 @@ def q4_dequantize(w: Q4Weight, *, dtype=None, out=None, stream=None):
     return out
 
 
-@functools.lru_cache(maxsize=256)
-def _linear_workspace(tokens, x_code, out_features, in_features):
-    return int(_lib.load().ssm_q4_linear_workspace_bytes(tokens, x_code, out_features, in_features))
-
-
-def q4_linear_workspace_bytes(tokens: int, x_dtype, w: Q4Weight) -> int:
-    return _linear_workspace(tokens, _TOKENS[x_dtype], w.out_features, w.in_features)
-
-
-def q4_linear(x, w: Q4Weight, *, x_scale=None, out_dtype=None, out=None, workspace=None, stream=None):
+def q4_linear(x, w: Q4Weight, *, x_scale=None, out_dtype=None, out=None, stream=None):
     """ssm_q4_linear: x [T, in_features] times the weight's transpose, [T, out_features].  x is float32, bfloat16, or
     float8_e4m3fn with x_scale [T] fp32 (rms_norm gives both).  out_dtype: that of out where given, else x's, bfloat16
-    for 8-bit tokens.  workspace: q4_linear_workspace_bytes() bytes, allocated where not given."""
-    if stream is None and workspace is None:
+    for 8-bit tokens."""
+    if stream is None:
         r = (_native or _bound()).q4_linear(x, w, x_scale, out_dtype, out)
         if r is not NotImplemented:
             return r
@@ -312,18 +300,7 @@ def q4_linear(x, w: Q4Weight, *, x_scale=None, out_dtype=None, out=None, workspa
     if out is None:
         out = _empty(shape, out_dtype, dev, stream)
     vo = _rows(out, "out", shape, out_dtype, dev)
-    code = _TOKENS[x.dtype]
-    pw, size = None, 0
-    if workspace is None:
-        size = _linear_workspace(T, code, w.out_features, w.in_features)
-        if size:
-            workspace = _empty((size,), torch.uint8, dev, stream, returned=False)
-            pw = workspace.data_ptr()
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    else:
-        pw, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = lib.ssm_q4_linear(T, code, _IO[out_dtype], vx, ps, q, vo, pw, size, stream_handle(stream, dev))
+    st = lib.ssm_q4_linear(T, _TOKENS[x.dtype], _IO[out_dtype], vx, ps, q, vo, stream_handle(stream, dev))
     if st != 0:
         _fail("ssm_q4_linear", st)
     return out

@@ -21,7 +21,6 @@ namespace {
 
 decltype(&ssm_rms_norm) f_norm;
 decltype(&ssm_q4_linear) f_linear;
-decltype(&ssm_q4_linear_workspace_bytes) f_workspace;
 
 // A call is usual until something is not; the device of the first tensor is that of all.
 struct Call {
@@ -156,26 +155,24 @@ PyObject* q4_linear(PyObject* const* a) {
   if (!c.ok || xc < 0 || (xc == SSM_E4M3) != (xs != nullptr)) return not_usual();
   if (!dtype_of(a[3], to ? to->scalar_type() : xc == SSM_E4M3 ? at::kBFloat16 : type, out_type)) return not_usual();
   if ((to && to->scalar_type() != out_type) || (out_type != at::kFloat && out_type != at::kBFloat16)) return not_usual();
-  at::Tensor made, ws;
+  at::Tensor made;
   if (!to) {
     made = c.fresh({T, M}, out_type);
     o = ssm_rows{made.data_ptr(), M};
   }
   const ssm_q4_weight q = {codes->data_ptr(), scales->data_ptr(), M, K};
-  const size_t need = f_workspace(T, xc, M, K);
-  if (need) ws = c.fresh({(int64_t)need}, at::kByte);
   Ref out(to ? same(a[4]) : own(std::move(made)));
   if (!out.p) return nullptr;
   return out.after(f_linear(T, xc, code_of(out_type), &x, xs ? xs->const_data_ptr<float>() : nullptr, &q, &o,
-                            need ? ws.mutable_data_ptr() : nullptr, need, c.stream()),
+                            c.stream()),
                    "ssm_q4_linear");
 }
 
-// bind(version, rms_norm, q4_linear, q4_linear_workspace_bytes, raise_status): the library's ABI version, which has to be the
+// bind(version, rms_norm, q4_linear, raise_status): the library's ABI version, which has to be the
 // one that this module fills structures for, addresses, and a function
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes a version, three addresses and a function");
+  if (nargs != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind takes a version, two addresses and a function");
     return nullptr;
   }
   const long version = PyLong_AsLong(*a++);
@@ -183,8 +180,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!PyErr_Occurred()) PyErr_Format(PyExc_ImportError, "built for libssm ABI %d, not %ld", SSM_ABI_VERSION, version);
     return nullptr;
   }
-  void* p[3];
-  for (int i = 0; i < 3; ++i) {
+  void* p[2];
+  for (int i = 0; i < 2; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -193,10 +190,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   }
   f_norm = reinterpret_cast<decltype(f_norm)>(p[0]);
   f_linear = reinterpret_cast<decltype(f_linear)>(p[1]);
-  f_workspace = reinterpret_cast<decltype(f_workspace)>(p[2]);
-  Py_INCREF(a[3]);
+  Py_INCREF(a[2]);
   Py_XDECREF(raise_status);
-  raise_status = a[3];
+  raise_status = a[2];
   Py_RETURN_NONE;
 }
 

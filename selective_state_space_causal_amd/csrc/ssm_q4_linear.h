@@ -1,6 +1,10 @@
-// ssm_q4_linear.h -- what ssm_q4_linear's kernels (ssm_q4_rows.hip, ssm_q4_tiles.hip) share.
+// ssm_q4_linear.h -- what ssm_q4_linear's kernels (ssm_q4_rows.hip, ssm_q4_few.hip, ssm_q4_tiles.hip) share.
 #pragma once
+#include <type_traits>
+
 #include "ssm_block.h"
+
+#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
 
 namespace ssm {
 namespace block {
@@ -11,12 +15,11 @@ struct LinearArgs {
   Rows x, out;
   const char* codes;
   const char* scales;
-  const float* x_scale;  // e4m3 tokens
-  float* partial;        // [splits, T, Mp] sums of parts of K
-  int64_t Mp;            // M, a multiple of 4
-  bool wide;             // output rows are aligned to 16 bytes
+  const float* x_scale;     // e4m3 tokens
   int64_t T, M, K, kt, k4;  // tiles along K: of 128 and of 512 columns
   int64_t mt;               // tiles of 16 rows
+  bool out_bf16;
+  bool wide;                // output rows are aligned to 16 bytes
 };
 
 // How tokens are multiplied.  e4m3 tokens go into the instruction that takes codes as they are (X_E4M3); for an output in fp32
@@ -26,32 +29,35 @@ struct LinearArgs {
 enum { X_F32 = SSM_F32, X_BF16 = SSM_BF16, X_E4M3 = SSM_E4M3, X_WIDE = 3 };
 
 template <int X>
-constexpr int x_size() {  // bytes of a token's value in memory
+constexpr int x_size() {  // bytes of a token's value
   return X == X_F32 ? 4 : X == X_BF16 ? 2 : 1;
 }
 template <int X>
 constexpr bool x_scaled() {
   return X == X_E4M3 || X == X_WIDE;
 }
+template <int X>
+constexpr int planes() {  // bf16 parts of a value
+  return X == X_F32 ? 3 : 1;
+}
 
 __device__ __forceinline__ float pow2(unsigned e) { return __uint_as_float(e << 23); }
 
+template <typename V>
+__device__ __forceinline__ unsigned two(V v) {
+  return __builtin_bit_cast(unsigned, v);
+}
+
 // Eight codes times s in bf16, exactly.
 __device__ __forceinline__ bf16x8 weights8(unsigned c, float s) {
-  const auto two = [](auto v) { return __builtin_bit_cast(unsigned, v); };
-  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))});
+  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))});
 }
 
 // Eight e4m3 values in bf16, exactly.
 __device__ __forceinline__ bf16x8 widen8(unsigned lo, unsigned hi) {
-  const auto two = [](auto v) { return __builtin_bit_cast(unsigned, v); };
-  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))});
+  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))});
 }
 
 // x = p[0] + p[1] + p[2], bf16 each, to 2^-27 of x: a part is rounded to nearest, so what it leaves is at most 2^-9 of it, and
@@ -73,11 +79,66 @@ __device__ __forceinline__ void three_parts(const float (&x)[8], bf16x8 (&p)[3])
   }
 }
 
-// Few tokens: ssm_q4_rows.hip.  Any number: ssm_q4_tiles.hip.
-constexpr int64_t ROWS_MAX_TOKENS = 16;
-hipError_t launch_q4_rows(const LinearArgs& a, int x_dtype, int out_dtype, hipStream_t s);
-hipError_t launch_q4_tiles(const LinearArgs& a, int x_dtype, int out_dtype, hipStream_t s);
-int q4_tiles_splits(int64_t T, int x_dtype, int64_t M, int64_t K);
+// 2 GiB from p on, for loads straight into LDS; every offset is in bounds by construction.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
+}
+
+// Tokens in LDS: rows of 128 columns.  Piece c (16 bytes) of token t lies at place c ^ swap_of(t) of its row, so that 16
+// neighbouring rows' pieces c cover all 64 banks.
+template <int X>
+__device__ __forceinline__ int swap_of(int t) {
+  return x_size<X>() == 1 ? (t >> 1) & 7 : t & 15;
+}
+
+// Eight of a token's values in LDS, as bf16 (fp32 ones in three parts); `eighth`: which eight of the row's 128.
+template <int X>
+struct Eight;
+template <>
+struct Eight<X_BF16> {
+  bf16x8 v;
+  __device__ __forceinline__ void read(const char* row, int eighth, int swap) { v = *reinterpret_cast<const bf16x8*>(row + (eighth ^ swap) * 16); }
+  __device__ __forceinline__ void parts(bf16x8 (&p)[1]) const { p[0] = v; }
+};
+template <>
+struct Eight<X_WIDE> {
+  u32x2 v;
+  __device__ __forceinline__ void read(const char* row, int eighth, int swap) {
+    v = *reinterpret_cast<const u32x2*>(row + (eighth / 2 ^ swap) * 16 + eighth % 2 * 8);
+  }
+  __device__ __forceinline__ void parts(bf16x8 (&p)[1]) const { p[0] = widen8(v[0], v[1]); }
+};
+template <>
+struct Eight<X_F32> {
+  u32x4 v[2];
+  __device__ __forceinline__ void read(const char* row, int eighth, int swap) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<const u32x4*>(row + ((2 * eighth + i) ^ swap) * 16);
+  }
+  __device__ __forceinline__ void parts(bf16x8 (&p)[3]) const {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i / 4][i % 4]);
+    three_parts(f, p);
+  }
+};
+
+// One output: column m of token t.
+template <int X>
+__device__ __forceinline__ void store_one(const LinearArgs& a, int64_t t, int64_t m, float sum) {
+  if constexpr (x_scaled<X>()) sum *= a.x_scale[t];
+  char* const p = a.out.p + t * a.out.stride;
+  if (a.out_bf16)
+    reinterpret_cast<bf16_t*>(p)[m] = from_f32<bf16_t>(sum);
+  else
+    reinterpret_cast<float*>(p)[m] = sum;
+}
+
+hipError_t launch_q4_rows(const LinearArgs& a, int x, hipStream_t s);   // up to rows_tokens(x)
+hipError_t launch_q4_few(const LinearArgs& a, int x, hipStream_t s);    // up to few_tokens(x)
+hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s);  // any number
+constexpr int64_t rows_tokens(int x) { return x == X_F32 ? 1 : 4; }
+constexpr int64_t few_tokens(int x) { return x == X_F32 ? 16 : 32; }
 
 }  // namespace block
 }  // namespace ssm

@@ -305,17 +305,21 @@ def test_linear_by_the_identity_gives_the_tokens(T, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
 @pytest.mark.parametrize("T", [3, 40, 130])
-def test_linear_takes_every_group_s_scale(T, kind):
+@pytest.mark.parametrize("lo,hi", [(117, 137), (123, 133)])
+def test_linear_takes_every_group_s_scale(T, kind, lo, hi):
     """All ones times codes of one: a row's sum is the sum of its groups' scales."""
     M, K = 100, 1104
     rng = np.random.default_rng(3)
-    s = rng.integers(117, 137, (M, -(-K // 32))).astype(np.uint8)
+    s = rng.integers(lo, hi, (M, -(-K // 32))).astype(np.uint8)
     w = ssm.Q4Weight.pack(torch.full((M, K), 2, dtype=torch.uint8), torch.from_numpy(s))
     w = ssm.Q4Weight(w.codes.to(DEV), w.scales.to(DEV), M, K)
     xs = torch.ones(T, device=DEV) if kind == "e4m3" else None
-    got = ssm.q4_linear(torch.ones(T, K, device=DEV).to(DT[kind]), w, x_scale=xs, out_dtype=torch.float32)
-    want = O.dequantize(np.full((M, K), 2), s).sum(1)  # exact in fp32: at most 1104 of 2^9 in steps of 2^-10
-    assert np.array_equal(f64(got), np.broadcast_to(want, (T, M)))
+    got = f64(ssm.q4_linear(torch.ones(T, K, device=DEV).to(DT[kind]), w, x_scale=xs, out_dtype=torch.float32))
+    want = O.dequantize(np.full((M, K), 2), s).sum(1)
+    # Scales of 2^-4 .. 2^5: sums are below 2^5 1104 < 2^16 in steps of 2^-4, exact in fp32's 24 bits.  Of 2^-10 .. 2^9 they
+    # take up to 30: each of at most 1104 additions of positive terms rounds by 2^-23 of the sum at most.
+    tol = 0.0 if lo == 123 else 1104 * 2.0 ** -23
+    assert got.shape == (T, M) and np.all(np.abs(got - want) <= tol * want)
 
 
 @pytest.mark.parametrize("T", [3, 40, 130])
@@ -354,18 +358,6 @@ def test_linear_of_no_tokens():
     assert ssm.q4_linear(torch.zeros(0, 64, device=DEV), w).shape == (0, 40)
     got = ssm.q4_linear(torch.zeros(0, 64, device=DEV).to(E4M3), w, x_scale=torch.zeros(0, device=DEV))
     assert got.shape == (0, 40) and got.dtype == torch.bfloat16
-
-
-def test_linear_s_workspace_is_the_caller_s():
-    w, _ = weight(256, 4096)
-    x = rnd(1, 60, 4096).bfloat16().to(DEV)
-    need = ssm.q4_linear_workspace_bytes(60, torch.bfloat16, w)
-    assert need > 0
-    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
-    got = ssm.q4_linear(x, w, workspace=ws)
-    assert (ws[need:] == 255).all() and torch.equal(got, ssm.q4_linear(x, w))
-    with pytest.raises(ssm.SsmError):
-        ssm.q4_linear(x, w, workspace=ws[:need - 16])
 
 
 def test_linear_past_32_bits():
