@@ -60,7 +60,7 @@ def _fail(name, st):
     raise SsmError(name, st, _lib.load().ssm_status_str(st).decode())
 
 
-_native = None  # the usual case of rms_norm and q4_linear, natively (csrc/block_binding.cpp); NotImplemented for any other
+_native = None  # the usual case of the calls below, natively (csrc/block_binding.cpp); NotImplemented for any other
 
 
 class _NoNative:
@@ -69,7 +69,7 @@ class _NoNative:
     @staticmethod
     def _not_usual(*args):
         return NotImplemented
-    rms_norm = q4_linear = _not_usual
+    rms_norm = q4_linear = q4_quantize = q4_dequantize = _not_usual
 
 
 def _bound():
@@ -79,7 +79,7 @@ def _bound():
         try:
             from . import _block_fast
             _block_fast.bind(lib.ssm_abi_version(), *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-                "ssm_rms_norm", "ssm_q4_linear")), _fail)
+                "ssm_rms_norm", "ssm_q4_linear", "ssm_q4_quantize", "ssm_q4_dequantize")), _fail)
             _native = _block_fast
         except ImportError as e:
             warnings.warn(f"the block calls' native binding is not built for this library ({e}): small calls are slower; run "
@@ -241,6 +241,10 @@ def _q4(w: Q4Weight, device):
 
 def q4_quantize(w, *, out: Optional[Q4Weight] = None, stream=None) -> Q4Weight:
     """ssm_q4_quantize: w [out_features, in_features] (float32 or bfloat16) in 4 bits."""
+    if stream is None and out is None:
+        r = (_native or _bound()).q4_quantize(w)
+        if r is not NotImplemented:
+            return Q4Weight(*r, *w.shape)
     lib = _lib.load()
     M, K = _two(w, "w")
     io, dev = _io(w, "w"), w.device
@@ -259,6 +263,10 @@ def q4_quantize(w, *, out: Optional[Q4Weight] = None, stream=None) -> Q4Weight:
 
 def q4_dequantize(w: Q4Weight, *, dtype=None, out=None, stream=None):
     """ssm_q4_dequantize: the weight [out_features, in_features] in dtype (out's where given, else bfloat16; exact in both)."""
+    if stream is None:
+        r = (_native or _bound()).q4_dequantize(w, dtype, out)
+        if r is not NotImplemented:
+            return r
     lib = _lib.load()
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype

@@ -37,7 +37,7 @@ PyObject* same(PyObject* o) {
   Py_INCREF(o);
   return o;
 }
-[[maybe_unused]] bool put(Ref& tuple, int i, PyObject* o) {
+bool put(Ref& tuple, int i, PyObject* o) {
   if (o) PyTuple_SET_ITEM(tuple.p, i, o);
   return o != nullptr;
 }

@@ -1,4 +1,4 @@
-// block_binding.cpp -- the usual case of rms_norm and q4_linear of block.py, natively (Python extension _block_fast).
+// block_binding.cpp -- the usual case of block.py's calls, natively (Python extension _block_fast).
 //
 // As attn_binding.cpp for attn.py: each function takes the arguments of the function of its name, on the current stream, and
 // answers NotImplemented, having done nothing, whenever anything about them is not the usual; block.py then goes through its
@@ -21,6 +21,8 @@ namespace {
 
 decltype(&ssm_rms_norm) f_norm;
 decltype(&ssm_q4_linear) f_linear;
+decltype(&ssm_q4_quantize) f_quantize;
+decltype(&ssm_q4_dequantize) f_dequantize;
 
 // A call is usual until something is not; the device of the first tensor is that of all.
 struct Call {
@@ -60,6 +62,21 @@ struct Call {
         t->size(3) != n3 || !t->is_contiguous())
       return fail();
     return t;
+  }
+  // A 4-bit weight (codes, scales, out_features, in_features).
+  bool weight(PyObject* o, ssm_q4_weight& q) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) return fail() != nullptr;
+    PyObject* const m = PyTuple_GET_ITEM(o, 2);
+    PyObject* const k = PyTuple_GET_ITEM(o, 3);
+    if (!PyLong_Check(m) || !PyLong_Check(k)) return fail() != nullptr;
+    int over = 0, more = 0;
+    const int64_t M = PyLong_AsLongLongAndOverflow(m, &over), K = PyLong_AsLongLongAndOverflow(k, &more);
+    if (over || more || M < 1 || M > SSM_Q4_MAX_FEATURES || K < 1 || K > SSM_Q4_MAX_FEATURES) return fail() != nullptr;
+    const at::Tensor* codes = bytes(PyTuple_GET_ITEM(o, 0), (M + 15) / 16, (K + 127) / 128, 16);
+    const at::Tensor* scales = bytes(PyTuple_GET_ITEM(o, 1), (M + 15) / 16, (K + 511) / 512, 4);
+    if (!ok) return false;
+    q = ssm_q4_weight{codes->data_ptr(), scales->data_ptr(), M, K};
+    return true;
   }
   at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type) const {
     return at::empty(sizes, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, device)));
@@ -135,20 +152,14 @@ PyObject* rms_norm(PyObject* const* a) {
 PyObject* q4_linear(PyObject* const* a) {
   Call c;
   ssm_rows x, o;
-  if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 4) return not_usual();
-  PyObject* const m = PyTuple_GET_ITEM(a[1], 2);
-  PyObject* const k = PyTuple_GET_ITEM(a[1], 3);
-  if (!PyLong_Check(m) || !PyLong_Check(k)) return not_usual();
-  int over = 0, more = 0;
-  const int64_t M = PyLong_AsLongLongAndOverflow(m, &over), K = PyLong_AsLongLongAndOverflow(k, &more);
-  if (over || more || M < 1 || M > SSM_Q4_MAX_FEATURES || K < 1 || K > SSM_Q4_MAX_FEATURES) return not_usual();
+  ssm_q4_weight q;
+  if (!c.weight(a[1], q)) return not_usual();
+  const int64_t M = q.out_features, K = q.in_features;
   const at::Tensor* tx = c.rows(a[0], x, -1, K);
   if (!tx) return not_usual();
   const int64_t T = tx->size(0);
   const at::ScalarType type = tx->scalar_type();
   const int32_t xc = code_of(type);
-  const at::Tensor* codes = c.bytes(PyTuple_GET_ITEM(a[1], 0), (M + 15) / 16, (K + 127) / 128, 16);
-  const at::Tensor* scales = c.bytes(PyTuple_GET_ITEM(a[1], 1), (M + 15) / 16, (K + 511) / 512, 4);
   const at::Tensor* xs = a[2] == Py_None ? nullptr : c.vector(a[2], T);
   const at::Tensor* to = a[4] == Py_None ? nullptr : c.rows(a[4], o, T, M);
   at::ScalarType out_type;
@@ -160,7 +171,6 @@ PyObject* q4_linear(PyObject* const* a) {
     made = c.fresh({T, M}, out_type);
     o = ssm_rows{made.data_ptr(), M};
   }
-  const ssm_q4_weight q = {codes->data_ptr(), scales->data_ptr(), M, K};
   Ref out(to ? same(a[4]) : own(std::move(made)));
   if (!out.p) return nullptr;
   return out.after(f_linear(T, xc, code_of(out_type), &x, xs ? xs->const_data_ptr<float>() : nullptr, &q, &o,
@@ -168,11 +178,48 @@ PyObject* q4_linear(PyObject* const* a) {
                    "ssm_q4_linear");
 }
 
-// bind(version, rms_norm, q4_linear, raise_status): the library's ABI version, which has to be the
+// q4_quantize(w), without a given output: (codes, scales)
+PyObject* q4_quantize(PyObject* const* a) {
+  Call c;
+  ssm_rows w;
+  const at::Tensor* t = c.rows(a[0], w, -1, -1);
+  if (!t) return not_usual();
+  const int64_t M = t->size(0), K = t->size(1);
+  const int32_t io = code_of(t->scalar_type());
+  if ((io != SSM_F32 && io != SSM_BF16) || M < 1 || M > SSM_Q4_MAX_FEATURES || K < 16 || K > SSM_Q4_MAX_FEATURES || K % 16) return not_usual();
+  at::Tensor codes = c.fresh({(M + 15) / 16, (K + 127) / 128, 64, 16}, at::kByte);
+  at::Tensor scales = c.fresh({(M + 15) / 16, (K + 511) / 512, 64, 4}, at::kByte);
+  const ssm_q4_weight q = {codes.data_ptr(), scales.data_ptr(), M, K};
+  Ref out(PyTuple_New(2));
+  if (!out.p || !put(out, 0, own(std::move(codes))) || !put(out, 1, own(std::move(scales)))) return nullptr;
+  return out.after(f_quantize(io, &w, &q, c.stream()), "ssm_q4_quantize");
+}
+
+// q4_dequantize((codes, scales, out_features, in_features), dtype, out)
+PyObject* q4_dequantize(PyObject* const* a) {
+  Call c;
+  ssm_q4_weight q;
+  ssm_rows w;
+  if (!c.weight(a[0], q)) return not_usual();
+  const at::Tensor* to = a[2] == Py_None ? nullptr : c.rows(a[2], w, q.out_features, q.in_features);
+  at::ScalarType type;
+  if (!c.ok || !dtype_of(a[1], to ? to->scalar_type() : at::kBFloat16, type) || (to && to->scalar_type() != type)) return not_usual();
+  if (type != at::kFloat && type != at::kBFloat16) return not_usual();
+  at::Tensor made;
+  if (!to) {
+    made = c.fresh({q.out_features, q.in_features}, type);
+    w = ssm_rows{made.data_ptr(), q.in_features};
+  }
+  Ref out(to ? same(a[2]) : own(std::move(made)));
+  if (!out.p) return nullptr;
+  return out.after(f_dequantize(code_of(type), &q, &w, c.stream()), "ssm_q4_dequantize");
+}
+
+// bind(version, rms_norm, q4_linear, q4_quantize, q4_dequantize, raise_status): the library's ABI version, which has to be the
 // one that this module fills structures for, addresses, and a function
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes a version, two addresses and a function");
+  if (nargs != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind takes a version, four addresses and a function");
     return nullptr;
   }
   const long version = PyLong_AsLong(*a++);
@@ -180,8 +227,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!PyErr_Occurred()) PyErr_Format(PyExc_ImportError, "built for libssm ABI %d, not %ld", SSM_ABI_VERSION, version);
     return nullptr;
   }
-  void* p[2];
-  for (int i = 0; i < 2; ++i) {
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -190,13 +237,16 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   }
   f_norm = reinterpret_cast<decltype(f_norm)>(p[0]);
   f_linear = reinterpret_cast<decltype(f_linear)>(p[1]);
-  Py_INCREF(a[2]);
+  f_quantize = reinterpret_cast<decltype(f_quantize)>(p[2]);
+  f_dequantize = reinterpret_cast<decltype(f_dequantize)>(p[3]);
+  Py_INCREF(a[4]);
   Py_XDECREF(raise_status);
-  raise_status = a[2];
+  raise_status = a[4];
   Py_RETURN_NONE;
 }
 
 PyMethodDef methods[] = {method("bind", bind), method("rms_norm", guarded<rms_norm, 8>), method("q4_linear", guarded<q4_linear, 5>),
+                         method("q4_quantize", guarded<q4_quantize, 1>), method("q4_dequantize", guarded<q4_dequantize, 3>),
                          PyMethodDef{nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

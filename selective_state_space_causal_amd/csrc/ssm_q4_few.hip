@@ -118,6 +118,7 @@ __global__ __launch_bounds__(64 * WAVES) void q4_few(const LinearArgs a, int spl
         __builtin_amdgcn_s_waitcnt(0x0F70 | ((ST - 1) * LOADS & 15) | ((ST - 1) * LOADS >> 4 << 14));
       else
         __builtin_amdgcn_s_waitcnt(0x0F70);
+      asm volatile("" ::: "memory");  // no read of the ring moves up
       __builtin_amdgcn_sched_barrier(0);
       multiply(p);
       __builtin_amdgcn_sched_barrier(0);

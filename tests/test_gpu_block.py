@@ -429,16 +429,12 @@ def test_the_native_half_takes_the_usual_calls_and_gives_the_same(monkeypatch):
     seen = []
 
     class Spy:
-        @staticmethod
-        def rms_norm(*a):
-            seen.append(fast.rms_norm(*a))
-            return seen[-1]
-
-        @staticmethod
-        def q4_linear(*a):
-            seen.append(fast.q4_linear(*a))
-            return seen[-1]
-    monkeypatch.setattr(B, "_native", Spy)
+        def __getattr__(self, name):
+            def call(*a):
+                seen.append(getattr(fast, name)(*a))
+                return seen[-1]
+            return call
+    monkeypatch.setattr(B, "_native", Spy())
 
     def calls():
         x, g, w = p["x"], p["g"], p["w"]
@@ -450,9 +446,13 @@ def test_the_native_half_takes_the_usual_calls_and_gives_the_same(monkeypatch):
         out += [*ssm.rms_norm(x, g, out=c, scale=s)]
         out += [ssm.q4_linear(x, w), ssm.q4_linear(x, w, out_dtype=torch.float32), ssm.q4_linear(x.float(), w),
                 ssm.q4_linear(c, w, x_scale=s), ssm.q4_linear(x[:3], w, out=torch.zeros(3, 600, device=DEV))]
+        q, r = ssm.q4_quantize(x), ssm.q4_quantize(x.float())
+        assert isinstance(q, ssm.Q4Weight) and q.shape == x.shape
+        out += [q.codes, q.scales, r.codes, r.scales, ssm.q4_dequantize(q), ssm.q4_dequantize(q, dtype=torch.float32),
+                ssm.q4_dequantize(r, out=torch.zeros_like(x))]
         return out
     a = calls()
-    assert len(seen) == 11 and all(r is not NotImplemented for r in seen)
+    assert len(seen) == 16 and all(r is not NotImplemented for r in seen)
     monkeypatch.setattr(B, "_native", B._NoNative)
     for u, v in zip(a, calls()):
         assert u.dtype == v.dtype and torch.equal(u.reshape(-1).view(torch.uint8), v.reshape(-1).view(torch.uint8))
@@ -470,6 +470,10 @@ def test_refusals_on_the_gpu_are_worded():
             ("x_scale", lambda: ssm.q4_linear(x.to(E4M3), w, x_scale=torch.ones(23, device=DEV))),
             ("codes", lambda: ssm.q4_linear(x, w._replace(codes=w.codes[1:]))),
             ("scales", lambda: ssm.q4_linear(x, w._replace(scales=w.scales.int()))),
+            ("codes", lambda: ssm.q4_dequantize(w._replace(codes=w.codes[1:]))),
+            ("out: shape", lambda: ssm.q4_dequantize(w, out=torch.zeros(3, 1040, device=DEV))),
+            ("multiple of 16", lambda: ssm.q4_quantize(torch.zeros(4, 24, device=DEV))),
+            ("contiguous", lambda: ssm.q4_quantize(torch.zeros(4, 64, device=DEV)[:, ::2])),
             ("4-bit weight", lambda: ssm.q4_linear(x, w._replace(in_features=1041)))):
         with pytest.raises(ValueError, match=what):
             call()
