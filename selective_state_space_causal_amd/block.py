@@ -214,6 +214,13 @@ class Q4Weight(NamedTuple):
         return cls(c.view(mt, 16, kt, 4, 16).permute(0, 2, 3, 1, 4).reshape(mt, kt, 64, 16).contiguous(),
                    s.view(mt, 16, k4, 4, 4).permute(0, 2, 4, 1, 3).reshape(mt, k4, 64, 4).contiguous(), M, K)
 
+    def rows(self, start: int, stop: int) -> "Q4Weight":
+        """Rows start .. stop - 1, sharing the memory; both multiples of 16 (or stop the end)."""
+        if not 0 <= start < stop <= self.out_features or start % 16 or (stop % 16 and stop != self.out_features):
+            raise ValueError(f"rows {start} .. {stop} of {self.out_features}: a part starts and ends at multiples of 16")
+        tiles = slice(start // 16, -(-stop // 16))
+        return Q4Weight(self.codes[tiles], self.scales[tiles], stop - start, self.in_features)
+
     @property
     def shape(self):
         """The weight's own shape, as a tensor's."""
@@ -312,3 +319,28 @@ def q4_linear(x, w: Q4Weight, *, x_scale=None, out_dtype=None, out=None, stream=
     if st != 0:
         _fail("ssm_q4_linear", st)
     return out
+
+
+# ---------------------------------------------------------------- a block's way in and out
+
+def block_input(hidden, norm=None, residual=None, *, eps: float = 1e-5, tokens_8bit: bool = False, out=None, scale=None,
+                stream=None):
+    """What a block's first projection reads, as (tokens, scale or None): hidden [T, d_model] itself, or with norm (fp32
+    [d_model]) its norm, after hidden has been added to the residual stream where one is given; tokens_8bit: in
+    float8_e4m3fn with their scales, for a weight in 4 bits."""
+    if norm is None:
+        if residual is not None or tokens_8bit:
+            raise ValueError("residual and tokens_8bit go with norm")
+        return hidden, None
+    y = rms_norm(hidden, norm, residual=residual, eps=eps, out_dtype=E4M3 if tokens_8bit else None, out=out, scale=scale,
+                 stream=stream)
+    return y if tokens_8bit else (y, None)
+
+
+def project(x, w, x_scale=None):
+    """x [T, K] times the transpose of w [M, K]: a Q4Weight (q4_linear), or a tensor of x's dtype (a plain library GEMM)."""
+    if isinstance(w, Q4Weight):
+        return q4_linear(x, w, x_scale=x_scale)
+    if x_scale is not None:
+        raise ValueError("8-bit tokens need a weight in 4 bits")
+    return torch.nn.functional.linear(x, w)

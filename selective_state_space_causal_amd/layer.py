@@ -28,12 +28,20 @@ C); for bf16 with D and L multiples of 8, the conv front and x_proj run as one f
 (ssm_conv_xproj) and u is never stored; otherwise u is materialised and x_proj runs as three
 GEMMs.  out is written in the io dtype by default (the partial that the 8-bit all-reduce codec
 then quantizes); out_dtype=torch.float32 keeps it in fp32.
+
+Weights in 4 bits: in_proj's and out_proj's weights ("in_xz", "in_x", "in_z", "out") may be Q4Weights (block.py).  A decoded
+token is multiplied with them as they are (q4_linear); a prompt reads them back into the io dtype (q4_dequantize), since its
+projections are in the mixer's own channel-major layouts.
+
+With a norm the layer takes the stack's residual stream: hidden (the last block's output) is added to it, and in_proj
+reads its norm, in 8 bits for a decoded token where asked (rms_norm).
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib
+from .block import E4M3, Q4Weight, block_input, q4_dequantize, q4_linear
 
 CONV_W = 4
 
@@ -54,7 +62,12 @@ def _fused_conv_xproj(hidden, weights) -> bool:
     return "x_all" in weights and hidden.dtype == torch.bfloat16 and D % 8 == 0 and L % 8 == 0
 
 
-def alloc_buffers(hidden, weights: dict, d_state: int, out_dtype=None) -> dict:
+def _used(weights: dict, stacked: bool) -> tuple:
+    """The projection weights that a call reads."""
+    return ("in_xz", "out") if stacked else ("in_x", "in_z", "out")
+
+
+def alloc_buffers(hidden, weights: dict, d_state: int, out_dtype=None, normed: bool = False) -> dict:
     """Every tensor the layer writes, on hidden's device."""
     B, L, DM = hidden.shape
     D = weights["in_x"].shape[0]
@@ -75,18 +88,35 @@ def alloc_buffers(hidden, weights: dict, d_state: int, out_dtype=None) -> dict:
     bufs["h"] = torch.empty(B, D, d_state, dtype=torch.float32, device=dev)
     bufs["c"] = torch.empty(B, D, CONV_W - 1, dtype=torch.float32, device=dev)
     bufs["out"] = torch.empty(B, L, DM, dtype=out_dtype or dt, device=dev)
+    if normed:
+        bufs["normed"] = torch.empty(B, L, DM, dtype=dt, device=dev)
+    for k in _used(weights, "xz" in bufs):
+        if isinstance(weights[k], Q4Weight):
+            bufs["w_" + k] = torch.empty(weights[k].shape, dtype=dt, device=dev)
     return bufs
 
 
-def stages(hidden, weights: dict, params: dict, proj: "_lib.Projector", bufs: dict, stream=None):
+def stages(hidden, weights: dict, params: dict, proj: "_lib.Projector", bufs: dict, stream=None, norm=None, residual=None,
+           eps: float = 1e-5):
     """The layer as a list of (stage name, call), in order; each call enqueues its kernels on
     `stream` and writes into `bufs`."""
     P, b = proj, bufs
+    pre = []
+    for k in _used(weights, "xz" in b):
+        if isinstance(weights[k], Q4Weight):
+            pre.append((k + "_weight", lambda w=weights[k], o=b["w_" + k]: q4_dequantize(w, out=o, stream=stream)))
+            weights = {**weights, k: b["w_" + k]}
+    if norm is not None:
+        x, hidden = hidden, b["normed"]
+        pre.append(("norm", lambda: block_input(x.flatten(0, 1), norm, None if residual is None else residual.view(-1, x.shape[2]),
+                                                eps=eps, out=b["normed"].view(-1, x.shape[2]), stream=stream)))
+    elif residual is not None:
+        raise ValueError("residual goes with norm")
     if "xz" in b:
-        st = [("in_proj_xz", lambda: P(_lib.PROJ_IN, hidden, weights["in_xz"], out=b["xz"], stream=stream))]
+        st = pre + [("in_proj_xz", lambda: P(_lib.PROJ_IN, hidden, weights["in_xz"], out=b["xz"], stream=stream))]
     else:
-        st = [("in_proj_x", lambda: P(_lib.PROJ_IN, hidden, weights["in_x"], out=b["x"], stream=stream)),
-              ("in_proj_z", lambda: P(_lib.PROJ_IN, hidden, weights["in_z"], out=b["z"], stream=stream))]
+        st = pre + [("in_proj_x", lambda: P(_lib.PROJ_IN, hidden, weights["in_x"], out=b["x"], stream=stream)),
+                    ("in_proj_z", lambda: P(_lib.PROJ_IN, hidden, weights["in_z"], out=b["z"], stream=stream))]
     if "u" not in b:
         R = weights["x_dt"].shape[0]
         st.append(("conv_xproj", lambda: _lib.conv_xproj(b["x"], params, weights["x_all"], R, lowrank=b["lowrank"],
@@ -104,23 +134,30 @@ def stages(hidden, weights: dict, params: dict, proj: "_lib.Projector", bufs: di
     ]
 
 
-def mixer_prefill(hidden, weights: dict, params: dict, proj: "_lib.Projector", *, out_dtype=None, stream=None):
+def mixer_prefill(hidden, weights: dict, params: dict, proj: "_lib.Projector", *, out_dtype=None, stream=None, norm=None,
+                  residual=None, eps: float = 1e-5):
     """Returns (out [B, L, d_model] partial in out_dtype (default: hidden's dtype), h [B, D, N],
-    conv [B, D, 3])."""
-    bufs = alloc_buffers(hidden, weights, params["A"].shape[1], out_dtype)
-    for _, call in stages(hidden, weights, params, proj, bufs, stream):
+    conv [B, D, 3]).  norm (fp32 [d_model]): in_proj reads the norm of hidden, or with residual [B, L, d_model] (hidden's
+    dtype or fp32, contiguous, updated in place) of its sum with hidden."""
+    bufs = alloc_buffers(hidden, weights, params["A"].shape[1], out_dtype, norm is not None)
+    for _, call in stages(hidden, weights, params, proj, bufs, stream, norm, residual, eps):
         call()
     return bufs["out"], bufs["h"], bufs["c"]
 
 
 # ---- decode: one token per batch row through the layer, from the cache ----
 
-def alloc_decode_buffers(hidden_t, weights: dict, d_state: int, fused: bool, out_dtype=None) -> dict:
-    """Every tensor a decode step writes besides the cache, on hidden_t's device."""
+def alloc_decode_buffers(hidden_t, weights: dict, d_state: int, fused: bool, out_dtype=None, normed: bool = False,
+                         tokens_8bit: bool = False) -> dict:
+    """Every tensor a decode step writes besides the cache and the residual stream, on hidden_t's device."""
     B, DM = hidden_t.shape
     D, R = weights["in_x"].shape[0], weights["x_dt"].shape[0]
     dev, dt = hidden_t.device, hidden_t.dtype
     b = {}
+    if normed:
+        b["normed"] = torch.empty(B, DM, dtype=E4M3 if tokens_8bit else dt, device=dev)
+        if tokens_8bit:
+            b["scale"] = torch.empty(B, dtype=torch.float32, device=dev)
     if B == 1 and "in_xz" in weights:
         b["xz"] = torch.empty(1, 2 * D, 1, dtype=dt, device=dev)
         b["x"], b["z"] = b["xz"][:, :D], b["xz"][:, D:]
@@ -147,20 +184,35 @@ def alloc_decode_buffers(hidden_t, weights: dict, d_state: int, fused: bool, out
 
 
 def decode_stages(hidden_t, weights: dict, params: dict, proj: "_lib.Projector", h, conv, bufs: dict,
-                  fused: bool, stream=None):
+                  fused: bool, stream=None, norm=None, residual=None, eps: float = 1e-5):
     """One decode step of the layer as a list of (stage name, call); h [B, D, N] and conv
     [B, D, 3] are updated in place.  Unfused: in_proj, conv_silu (from the conv cache), x_proj
     (one GEMM for one batch row with the stacked weight, else three), dt_proj, ssm_decode_step,
     out_proj.  Fused: in_proj, ssm_decode_fused, out_proj."""
-    P, b = proj, bufs
+    b = bufs
     B, DM = hidden_t.shape
-    hs = hidden_t.view(B, 1, DM)
+    tokens, scale = (hidden_t, None) if norm is None else (b["normed"], b.get("scale"))
+    hs = tokens.view(B, 1, DM)
+    if scale is not None and not all(isinstance(weights[k], Q4Weight) for k in _used(weights, "xz" in b) if k != "out"):
+        raise ValueError("8-bit tokens need in_proj's weight in 4 bits")
+
+    def P(kind, x, w, *, out, stream):  # one token per row: the layouts of both sides are [B, features]
+        if not isinstance(w, Q4Weight):
+            return proj(kind, x, w, out=out, stream=stream)
+        return q4_linear(x.view(B, -1), w, x_scale=scale if kind == _lib.PROJ_IN else None, out=out.view(B, -1), stream=stream)
+
     R = weights["x_dt"].shape[0]
+    st = []
+    if norm is not None:
+        st.append(("norm", lambda: block_input(hidden_t, norm, residual, eps=eps, tokens_8bit=scale is not None, out=b["normed"],
+                                               scale=scale, stream=stream)))
+    elif residual is not None:
+        raise ValueError("residual goes with norm")
     if "xz" in b:
-        st = [("in_proj_xz", lambda: P(_lib.PROJ_IN, hs, weights["in_xz"], out=b["xz"], stream=stream))]
+        st.append(("in_proj_xz", lambda: P(_lib.PROJ_IN, hs, weights["in_xz"], out=b["xz"], stream=stream)))
     else:
-        st = [("in_proj_x", lambda: P(_lib.PROJ_IN, hs, weights["in_x"], out=b["x"], stream=stream)),
-              ("in_proj_z", lambda: P(_lib.PROJ_IN, hs, weights["in_z"], out=b["z"], stream=stream))]
+        st += [("in_proj_x", lambda: P(_lib.PROJ_IN, hs, weights["in_x"], out=b["x"], stream=stream)),
+               ("in_proj_z", lambda: P(_lib.PROJ_IN, hs, weights["in_z"], out=b["z"], stream=stream))]
     x2, z2, y2 = b["x"].view(B, -1), b["z"].view(B, -1), b["y"].view(B, -1)
     if fused:
         st.append(("decode_fused", lambda: _lib.decode_fused(x2, z2, params, weights["x_all"], weights["dt"], R, h, conv,
@@ -181,12 +233,16 @@ def decode_stages(hidden_t, weights: dict, params: dict, proj: "_lib.Projector",
 
 
 def mixer_decode_step(hidden_t, weights: dict, params: dict, proj: "_lib.Projector", h, conv, *, fused: bool = True,
-                      out_dtype=None, bufs=None, stream=None):
+                      out_dtype=None, bufs=None, stream=None, norm=None, residual=None, eps: float = 1e-5,
+                      tokens_8bit: bool = False):
     """One decoded token per batch row: hidden_t [B, d_model]; h [B, D, N] and conv [B, D, 3]
     (the cache) are updated in place.  Returns out [B, d_model], the layer's partial sum.
-    fused needs the stacked x_proj weight ("x_all") and d_state 16."""
+    fused needs the stacked x_proj weight ("x_all") and d_state 16.  norm and residual [B, d_model] as for mixer_prefill;
+    tokens_8bit: the norm in 8 bits, for an in_proj in 4 bits (bufs are then made with normed and tokens_8bit)."""
+    if tokens_8bit and norm is None:
+        raise ValueError("tokens_8bit goes with norm")
     if bufs is None:
-        bufs = alloc_decode_buffers(hidden_t, weights, params["A"].shape[1], fused, out_dtype)
-    for _, call in decode_stages(hidden_t, weights, params, proj, h, conv, bufs, fused, stream):
+        bufs = alloc_decode_buffers(hidden_t, weights, params["A"].shape[1], fused, out_dtype, norm is not None, tokens_8bit)
+    for _, call in decode_stages(hidden_t, weights, params, proj, h, conv, bufs, fused, stream, norm, residual, eps):
         call()
     return bufs["out"].view(hidden_t.shape[0], -1)
