@@ -432,7 +432,9 @@ hipError_t ring(const LinearArgs& a, hipStream_t s) {
 //          64 by 16384 x 4096   29, 18, 13.9, 17.5, 30            600 by 4096 x 4096   (128, 64) 35.6, (128, 128) 30.8
 //   e4m3   64 by 4096 x 8192   8.2, 10.8, 14.2, 22, 37            300 by 5120 x 2560   -, 19, 10.8, 10.4, 15
 // Past that the matrix cores are kept busy by two workgroups a CU: bf16 470 us for 4096 by 16384 x 4096 (1170 TFLOP/s; 555 in the
-// ring's 128 x 128, 470 in 256 x 256), e4m3 260 (2110 TFLOP/s; 330 in q4_pair's way, 425 in 128 x 64, 262 in 256 x 256).
+// ring's 128 x 128, 470 in 256 x 256).  e4m3 has room for two of 128 x 64 with two steps in the ring (600 by 4096 x 4096, 320
+// tiles: 18 us, 22 in 128 x 128), and from more than 512 tiles of 128 x 128 on 256 x 128 (4096 by 16384 x 4096 222 us, 2480
+// TFLOP/s, 255 in 128 x 128, 330 in q4_pair's way, 262 in 256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0).
 template <int X>
 hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
   const auto once = [&](int bm, int bt) { return tiles_of(a, bm, bt) <= 256; };
@@ -446,6 +448,10 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
     if (once(64, 32)) return ring<X, 64, 32, 2, 1, 4, E ? 3 : 2>(a, s);
     if (once(64, 64)) return ring<X, 64, 64, 2, 2, E ? 4 : 2, 3>(a, s);
     if (once(128, 64)) return ring<X, 128, 64, 4, 1, 2, E ? 4 : 2>(a, s);
+    if constexpr (X == X_E4M3) {
+      if (tiles_of(a, 128, 64) <= 512) return ring<X, 128, 64, 4, 1, 2, 2>(a, s);
+      if (tiles_of(a, 128, 128) > 512) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
+    }
     if constexpr (E) return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
     if (once(128, 128)) return ring<X, 128, 128, 4, 2, 1, 3>(a, s);
     if constexpr (X == X_BF16) return pair<X, 128, 128, 2, 2>(a, s);

@@ -288,6 +288,18 @@ def test_linear(T, M, K, kind):
     check_linear(T, M, K, kind, torch.bfloat16, seed=1)
 
 
+# Sizes that reach each form of the calls of few tokens (rows of a workgroup) and of tiles (how many there are).
+FORMS = [(1, 9000, 144), (4, 8209, 656), (12, 5000, 400), (16, 9000, 144), (20, 5000, 144), (32, 8300, 528), (300, 1000, 2064),
+         (520, 1000, 2064), (1000, 1100, 2064), (1030, 2100, 1552), (2050, 2100, 1040), (2100, 2101, 400), (3000, 3100, 528)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("T,M,K", FORMS)
+def test_linear_forms(T, M, K, kind):
+    check_linear(T, M, K, kind, torch.bfloat16)
+    check_linear(T, M, K, kind, torch.float32, seed=1)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
 @pytest.mark.parametrize("T", [1, 7, 16, 17, 40, 64, 150])
 def test_linear_by_the_identity_gives_the_tokens(T, kind):
