@@ -123,6 +123,12 @@ def _vector(t: torch.Tensor, name: str, n: int, device):
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _call(entry, *args, stream, device):
+    """The entry point's status.  It launches on the current device: the tensors' own, whichever that was before."""
+    with torch.cuda.device(device):
+        return entry(*args, stream_handle(stream, device))
+
+
 def _empty(shape, dtype, device, stream):
     return _made(lambda: torch.empty(shape, dtype=dtype, device=device), stream, device)
 
@@ -170,7 +176,7 @@ def rms_norm(x, weight, *, residual=None, residual_out=None, eps: float = 1e-5, 
         if scale is None:
             scale = _empty((T,), torch.float32, dev, stream)
         ps = _vector(scale, "scale", T, dev)
-    st = lib.ssm_rms_norm(T, D, io, rio, _TOKENS[out_dtype], eps, vx, pw, vr, vro, vo, ps, stream_handle(stream, dev))
+    st = _call(lib.ssm_rms_norm, T, D, io, rio, _TOKENS[out_dtype], eps, vx, pw, vr, vro, vo, ps, stream=stream, device=dev)
     if st != 0:
         _fail("ssm_rms_norm", st)
     return (out, scale) if q8 else out
@@ -262,7 +268,7 @@ def q4_quantize(w, *, out: Optional[Q4Weight] = None, stream=None) -> Q4Weight:
         out = Q4Weight(*(_empty(s, torch.uint8, dev, stream) for s in shapes), M, K)
     elif (out.out_features, out.in_features) != (M, K):
         raise ValueError(f"out is a weight of {tuple(out.shape)}, expected {(M, K)}")
-    st = lib.ssm_q4_quantize(io, vw, _q4(out, dev), stream_handle(stream, dev))
+    st = _call(lib.ssm_q4_quantize, io, vw, _q4(out, dev), stream=stream, device=dev)
     if st != 0:
         _fail("ssm_q4_quantize", st)
     return out
@@ -283,7 +289,7 @@ def q4_dequantize(w: Q4Weight, *, dtype=None, out=None, stream=None):
     q = _q4(w, dev)
     if out is None:
         out = _empty(w.shape, dtype, dev, stream)
-    st = lib.ssm_q4_dequantize(_IO[dtype], q, _rows(out, "out", w.shape, dtype, dev), stream_handle(stream, dev))
+    st = _call(lib.ssm_q4_dequantize, _IO[dtype], q, _rows(out, "out", w.shape, dtype, dev), stream=stream, device=dev)
     if st != 0:
         _fail("ssm_q4_dequantize", st)
     return out
@@ -315,7 +321,7 @@ def q4_linear(x, w: Q4Weight, *, x_scale=None, out_dtype=None, out=None, stream=
     if out is None:
         out = _empty(shape, out_dtype, dev, stream)
     vo = _rows(out, "out", shape, out_dtype, dev)
-    st = lib.ssm_q4_linear(T, _TOKENS[x.dtype], _IO[out_dtype], vx, ps, q, vo, stream_handle(stream, dev))
+    st = _call(lib.ssm_q4_linear, T, _TOKENS[x.dtype], _IO[out_dtype], vx, ps, q, vo, stream=stream, device=dev)
     if st != 0:
         _fail("ssm_q4_linear", st)
     return out

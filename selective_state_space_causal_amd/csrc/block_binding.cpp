@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Dtype.h>
@@ -37,7 +38,10 @@ struct Call {
     if (!ok || !THPVariable_Check(o)) return fail();
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda() || t.layout() != at::kStrided) return fail();
-    if (device < 0) device = t.get_device();
+    if (device < 0) {
+      device = t.get_device();
+      if (device != c10::hip::current_device()) return fail();  // block.py makes it the current one
+    }
     if (t.get_device() != device) return fail();
     return &t;
   }

@@ -1,6 +1,7 @@
 """C ABI of the residual norm and the 4-bit projections (include/ssm_block.h) without a GPU: exports and host-side
 validation.  Every call below is invalid on purpose (or has no tokens) and must be answered before any HIP call, so the fake
 device addresses are never dereferenced or launched on."""
+import contextlib
 import ctypes
 import math
 import os
@@ -158,3 +159,78 @@ def test_python_refusals_name_the_argument():
                  lambda: B.q4_linear(x, B.Q4Weight.allocate(3, 64, "cpu"), out_dtype=torch.float16)):
         with pytest.raises(TypeError):
             call()
+
+
+class Streams:
+    """torch's streams, devices and allocations replaced, and the entry points: what a call does up to its launch."""
+
+    def __init__(self, monkeypatch):
+        self.stream, self.device, self.made, self.launched = "current", "cuda:0", [], []
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: self.set("stream", s))
+        monkeypatch.setattr(torch.cuda, "device", lambda d: self.set("device", d))
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.stream)
+        monkeypatch.setattr(torch, "empty", self.empty)
+        monkeypatch.setattr(B, "_rows", lambda *a: None)
+        monkeypatch.setattr(B, "_vector", lambda *a: None)
+        monkeypatch.setattr(B, "_q4", lambda *a: None)
+        monkeypatch.setattr(B, "stream_handle", lambda s, d: s)
+        monkeypatch.setattr(B, "_native", B._NoNative)
+        monkeypatch.setattr(L, "load", lambda: self)
+
+    @contextlib.contextmanager
+    def set(self, name, value):
+        before = getattr(self, name)
+        setattr(self, name, value)
+        yield
+        setattr(self, name, before)
+
+    def empty(self, shape, dtype, device):
+        self.made.append(Block(self.stream, shape, dtype))
+        return self.made[-1]
+
+    def __getattr__(self, name):
+        if not name.startswith("ssm_"):
+            raise AttributeError(name)
+
+        def entry(*args):
+            self.launched.append((name, self.device, args[-1]))
+            return 0
+        return entry
+
+
+class Block:
+    """An allocation: its pool's stream, and the streams that its later free waits for."""
+
+    def __init__(self, pool, shape, dtype):
+        self.pool, self.recorded, self.shape, self.dtype = pool, [], shape, dtype
+
+    def record_stream(self, s):
+        self.recorded.append(s)
+
+
+class Tensor:
+    """A tensor on a second GPU, without storage."""
+    device = "cuda:1"
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+
+@pytest.mark.parametrize("stream", [None, "given"])
+def test_memory_and_launch_belong_to_the_given_stream_and_the_tensors_device(monkeypatch, stream):
+    """What a call makes comes from the pool of the stream that writes it, and is not handed out again before the current
+    stream is done with it; the launch is made with the tensors' device current."""
+    s = Streams(monkeypatch)
+    x, w = Tensor(3, 64), B.Q4Weight(Tensor(1, 1, 64, 16), Tensor(1, 1, 64, 4), 16, 64)
+    B.rms_norm(x, Tensor(64), out_dtype=B.E4M3, stream=stream)
+    B.q4_linear(x, w, stream=stream)
+    B.q4_quantize(x, stream=stream)
+    B.q4_dequantize(w, stream=stream)
+    assert [n for n, _, _ in s.launched] == ["ssm_rms_norm", "ssm_q4_linear", "ssm_q4_quantize", "ssm_q4_dequantize"]
+    assert all(device == "cuda:1" and at == stream for _, device, at in s.launched) and s.device == "cuda:0"
+    assert [tuple(t.shape) for t in s.made] == [(3, 64), (3,), (3, 16), (1, 1, 64, 16), (1, 1, 64, 4), (16, 64)]
+    for t in s.made:
+        assert (t.pool, t.recorded) == (("current", []) if stream is None else ("given", ["current"]))

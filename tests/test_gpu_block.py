@@ -373,19 +373,44 @@ def test_linear_of_no_tokens():
 
 
 def test_linear_past_32_bits():
-    """More than 2^32 bytes of codes: the last rows, for few tokens and for more."""
+    """More than 2^32 bytes of codes: the last rows, for few tokens and for more; then of tokens."""
     M, K = 1 << 20, 8720
     w = ssm.Q4Weight.allocate(M, K, DEV)
     w.codes.zero_(), w.scales.fill_(127)
     last, wv = weight(160, K, noise=False)
     w.codes[-10:] = last.codes
     w.scales[-10:] = last.scales
-    for T in (2, 20):
+    for T in (2, 20, 40):
         x = rnd(T, T, K).bfloat16()
         got = ssm.q4_linear(x.to(DEV), w, out_dtype=torch.float32)
         assert not got[:, :M - 160].any()
         want, mags = f64(x) @ wv.T, np.abs(f64(x)) @ np.abs(wv).T
         close(got[:, -160:], want, K * 2.0 ** -23 * mags, f"past 32 bits, {T} tokens")
+    del w, got
+    T, M, K = 600000, 24, 4096
+    w, wv = weight(M, K)
+    for kind in ("bf16", "e4m3"):
+        x, xs, xf = tokens(500, K, kind)
+        big = torch.zeros(T if kind == "bf16" else 2 * T, K, device=DEV, dtype=torch.bfloat16 if kind == "bf16" else torch.uint8).view(x.dtype)
+        big.view(torch.uint8)[-500:] = x.view(torch.uint8).view(500, -1).to(DEV)
+        scale = None if xs is None else torch.cat([torch.ones(len(big) - 500, device=DEV), xs])
+        got = ssm.q4_linear(big, w, x_scale=scale, out_dtype=torch.float32)
+        want, mags = xf @ wv.T, np.abs(xf) @ np.abs(wv).T
+        assert not got[:-500].any()
+        close(got[-500:], want, K * 2.0 ** -23 * mags, f"past 32 bits of tokens, {kind}")
+
+
+def test_quantize_past_32_bits():
+    """More than 2^32 bytes of a weight: the last rows, made and read back."""
+    M, K = 560000, 4096
+    w = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    tail = rnd(1, 320, K).bfloat16().to(DEV)
+    w[-320:] = tail
+    q, t = ssm.q4_quantize(w), ssm.q4_quantize(tail)
+    assert torch.equal(q.codes[-20:], t.codes) and torch.equal(q.scales[-20:], t.scales) and not q.codes[:-20].any()
+    w.fill_(1)
+    ssm.q4_dequantize(q, out=w)
+    assert torch.equal(w[-320:], ssm.q4_dequantize(t)) and not w[:-320].any()
 
 
 # ---------------------------------------------------------------- as they are used together, and how they are called
