@@ -6,7 +6,8 @@
 // its latency (a load, one reduction, a store) for few.  The sum of h^2 and the largest |h * weight| go through one
 // reduction: r > 0, and rounding keeps order, so max |(h * weight) * r| is exactly (max |h * weight|) * r.
 //
-// Threads to a row: a wave for up to 1024 values (no barrier), else 256 to 1024 threads; a call of few rows takes the form
+// Threads to a row: 16 for up to 128 values (100000 rows of 128: 25 us with a wave for each, of which 16 lanes have values), a
+// wave for up to 1024 (no barrier), else 256 to 1024 threads; a call of few rows takes the form
 // with one piece to a thread, whose chain from the first load to the last store is shortest.  A workgroup takes rows in
 // turn and loads the next one before it reduces this one.
 #include "ssm_block.h"
@@ -63,7 +64,7 @@ __device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
 template <typename IO, int RES, bool Q8, int TPR, int P>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs a) {
   using R = typename std::conditional<RES == F32_RES, float, IO>::type;
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1, NW = TPR / 64;
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1, NW = TPR < 64 ? 1 : TPR / 64;
   constexpr bool AHEAD = P <= 2;  // more pieces leave no registers for the next row
   __shared__ float red[2][2][NW];
   const int tid = threadIdx.x % TPR;
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
     }
     if (AHEAD && row + step < a.T) load(row + step);
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
+    for (int off = TPR < 64 ? TPR / 2 : 32; off >= 1; off >>= 1) {
       ss += __shfl_xor(ss, off, 64);
       if constexpr (Q8) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
     }
@@ -182,6 +183,7 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
 template <typename IO, int RES, bool Q8>
 hipError_t launch_width(const NormArgs& a, hipStream_t s) {
   const bool few = a.T <= 512;
+  if (a.W <= 128) return launch<IO, RES, Q8, 16, 1>(a, s);
   if (a.W <= 512) return launch<IO, RES, Q8, 64, 1>(a, s);
   if (a.W <= 1024 && !few) return launch<IO, RES, Q8, 64, 2>(a, s);
   if (a.W <= 2048) return launch<IO, RES, Q8, 256, 1>(a, s);

@@ -92,7 +92,7 @@ def check_norm(T, D, io, res, q8, seed=0, eps=1e-5, x=None, pad=0, in_place=Fals
     return y
 
 
-WIDTHS = [8, 72, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384, 16392, 32768]
+WIDTHS = [8, 72, 128, 136, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384, 16392, 32768]
 
 
 @pytest.mark.parametrize("D", WIDTHS)
@@ -105,7 +105,7 @@ def test_norm_widths(T, D):
     check_norm(T, D, "bf16", None, False, pad=16)
 
 
-@pytest.mark.parametrize("T,D", [(513, 1024), (1500, 4096), (700, 264), (5000, 72), (520, 8192), (9000, 128), (2100, 1544)])
+@pytest.mark.parametrize("T,D", [(513, 1024), (1500, 4096), (700, 264), (5000, 72), (520, 8192), (9000, 128), (70001, 96), (2100, 1544)])
 def test_norm_many_rows(T, D):
     """More rows than workgroups, and the forms for many."""
     check_norm(T, D, "bf16", "bf16", True)
