@@ -6,10 +6,12 @@
 // its latency (a load, one reduction, a store) for few.  The sum of h^2 and the largest |h * weight| go through one
 // reduction: r > 0, and rounding keeps order, so max |(h * weight) * r| is exactly (max |h * weight|) * r.
 //
-// Threads to a row: 16 for up to 128 values (100000 rows of 128: 25 us with a wave for each, of which 16 lanes have values), a
-// wave for up to 1024 (no barrier), else 256 to 1024 threads; a call of few rows takes the form
-// with one piece to a thread, whose chain from the first load to the last store is shortest.  A workgroup takes rows in
-// turn and loads the next one before it reduces this one.
+// Threads to a row: one for 8 values up to 8192 of them, which makes the chain from the first load to the last store short;
+// it is also the faster form for many rows (two pieces to a thread and half the threads, us: 2560 values, 1 row 2.5 against
+// 2.2, 2048 rows 9.0 against 7.9; 4096, 1024 rows 7.8 against 6.7; 8192, 2048 rows 27.9 against 25.4).  Up to 128 values 16
+// threads, so that a wave has four rows (100000 rows of 128: 18 us, 25 with a wave for each).  A workgroup takes rows in turn
+// and loads the next one before it reduces this one.  32768 rows of 4096, bf16 with residual to e4m3: 178 us, 5.3 TB/s, what
+// a copy reaches.
 #include "ssm_block.h"
 
 namespace ssm {
@@ -182,13 +184,11 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
 
 template <typename IO, int RES, bool Q8>
 hipError_t launch_width(const NormArgs& a, hipStream_t s) {
-  const bool few = a.T <= 512;
   if (a.W <= 128) return launch<IO, RES, Q8, 16, 1>(a, s);
   if (a.W <= 512) return launch<IO, RES, Q8, 64, 1>(a, s);
-  if (a.W <= 1024 && !few) return launch<IO, RES, Q8, 64, 2>(a, s);
   if (a.W <= 2048) return launch<IO, RES, Q8, 256, 1>(a, s);
-  if (a.W <= 4096) return few ? launch<IO, RES, Q8, 512, 1>(a, s) : launch<IO, RES, Q8, 256, 2>(a, s);
-  if (a.W <= 8192) return few ? launch<IO, RES, Q8, 1024, 1>(a, s) : launch<IO, RES, Q8, 512, 2>(a, s);
+  if (a.W <= 4096) return launch<IO, RES, Q8, 512, 1>(a, s);
+  if (a.W <= 8192) return launch<IO, RES, Q8, 1024, 1>(a, s);
   if (a.W <= 16384) return launch<IO, RES, Q8, 1024, 2>(a, s);
   return launch<IO, RES, Q8, 1024, 4>(a, s);
 }
