@@ -243,6 +243,8 @@ def mixer_decode_step(hidden_t, weights: dict, params: dict, proj: "_lib.Project
         raise ValueError("tokens_8bit goes with norm")
     if bufs is None:
         bufs = alloc_decode_buffers(hidden_t, weights, params["A"].shape[1], fused, out_dtype, norm is not None, tokens_8bit)
+    elif norm is not None and ("normed" not in bufs or ("scale" in bufs) != tokens_8bit):
+        raise ValueError(f"bufs were not made with normed=True, tokens_8bit={tokens_8bit}")
     for _, call in decode_stages(hidden_t, weights, params, proj, h, conv, bufs, fused, stream, norm, residual, eps):
         call()
     return bufs["out"].view(hidden_t.shape[0], -1)

@@ -1,0 +1,39 @@
+"""What layer.py and attn_layer.py refuse of a residual stream and of weights in 4 bits, without a GPU: the operators are
+replaced, so that nothing is launched."""
+import pytest
+import torch
+
+from selective_state_space_causal_amd import attn_layer, layer
+
+B, DM, D, R, N = 2, 32, 16, 4, 16
+
+
+def mixer_weights():
+    return {"in_x": torch.zeros(D, DM), "in_z": torch.zeros(D, DM), "x_dt": torch.zeros(R, D), "out": torch.zeros(DM, D),
+            "x_all": torch.zeros(R + 2 * N, D)}
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    """Names of the calls that would have launched something."""
+    done = []
+
+    def block_input(*args, **kw):
+        done.append("block_input")
+        return torch.zeros(B, DM), None
+
+    for module in (layer, attn_layer):
+        monkeypatch.setattr(module, "block_input", block_input)
+    return done
+
+
+@pytest.mark.parametrize("made,tokens_8bit", [(dict(), False), (dict(), True), (dict(normed=True), True),
+                                              (dict(normed=True, tokens_8bit=True), False)])
+def test_decode_buffers_of_another_kind(launched, made, tokens_8bit):
+    """Buffers made for other tokens than the call asks for would decide in its place."""
+    hidden, w = torch.zeros(B, DM), mixer_weights()
+    bufs = layer.alloc_decode_buffers(hidden, w, N, True, **made)
+    with pytest.raises(ValueError, match="bufs were not made with"):
+        layer.mixer_decode_step(hidden, w, {"A": torch.zeros(D, N)}, None, None, None, bufs=bufs, norm=torch.ones(DM),
+                                tokens_8bit=tokens_8bit)
+    assert launched == []
