@@ -107,9 +107,11 @@ def stages(hidden, weights: dict, params: dict, proj: "_lib.Projector", bufs: di
             pre.append((k + "_weight", lambda w=weights[k], o=b["w_" + k]: q4_dequantize(w, out=o, stream=stream)))
             weights = {**weights, k: b["w_" + k]}
     if norm is not None:
-        x, hidden = hidden, b["normed"]
-        pre.append(("norm", lambda: block_input(x.flatten(0, 1), norm, None if residual is None else residual.view(-1, x.shape[2]),
-                                                eps=eps, out=b["normed"].view(-1, x.shape[2]), stream=stream)))
+        if residual is not None and residual.shape != hidden.shape:
+            raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {tuple(hidden.shape)}")
+        x, hidden, DM = hidden, b["normed"], hidden.shape[2]
+        pre.append(("norm", lambda: block_input(x.view(-1, DM), norm, None if residual is None else residual.view(-1, DM),
+                                                eps=eps, out=b["normed"].view(-1, DM), stream=stream)))
     elif residual is not None:
         raise ValueError("residual goes with norm")
     if "xz" in b:

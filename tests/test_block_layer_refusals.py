@@ -37,3 +37,28 @@ def test_decode_buffers_of_another_kind(launched, made, tokens_8bit):
         layer.mixer_decode_step(hidden, w, {"A": torch.zeros(D, N)}, None, None, None, bufs=bufs, norm=torch.ones(DM),
                                 tokens_8bit=tokens_8bit)
     assert launched == []
+
+
+def prefill(hidden, residual):
+    w = mixer_weights()
+    bufs = layer.alloc_buffers(hidden, w, N, normed=True)
+    for name, call in layer.stages(hidden, w, {}, None, bufs, norm=torch.ones(DM), residual=residual):
+        if name == "norm":
+            return call()
+
+
+def test_prompt_s_residual_has_hidden_s_shape(launched):
+    """As many values in another order of rows are another stream."""
+    with pytest.raises(ValueError, match="residual: shape"):
+        prefill(torch.zeros(2, 5, DM), torch.zeros(5, 2, DM))
+    assert launched == []
+
+
+@pytest.mark.parametrize("which", ["hidden", "residual"])
+def test_prompt_in_rows_that_no_one_stride_reaches(launched, which):
+    """Refused: a copy of hidden would be made on another stream than the call's, one of residual would be updated in its place."""
+    t = {"hidden": torch.zeros(2, 5, DM), "residual": torch.zeros(2, 5, DM)}
+    t[which] = torch.zeros(5, 2, DM).transpose(0, 1)
+    with pytest.raises(RuntimeError, match="view"):
+        prefill(t["hidden"], t["residual"])
+    assert launched == []
