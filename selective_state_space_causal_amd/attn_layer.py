@@ -8,10 +8,10 @@ prompts and for one decoded token per sequence, composed from the operators of a
   out     = o @ out weight^T          [T, Hq D] -> [T, d_model], the rank's partial sum
 
 As with the mixer (layer.py), more than one rank adds its partial outputs outside this library.  The two
-projections are plain library GEMMs (torch.nn.functional.linear), or q4_linear (block.py) where a weight is a Q4Weight: both
-sides are token-major, a layout that
-the mixer's projections do not have over a prompt.  (For one token per sequence the layouts coincide, and a caller that
-keeps a Projector can run its two projections around attn.py's calls instead.)
+projections are plain library GEMMs (torch.nn.functional.linear), or q4_linear (block.py) where a weight is a
+Q4Weight: both sides are token-major, a layout that the mixer's projections do not have over a prompt.  (For one token per
+sequence the layouts coincide, and a caller that keeps a Projector can run its two projections around attn.py's calls
+instead.)
 
 With a norm the block takes the stack's residual stream: hidden (the last block's output) is added to it, and the
 block runs on its norm, in 8 bits for weights in 4 bits where asked (rms_norm).
@@ -24,7 +24,7 @@ from __future__ import annotations
 import torch
 
 from . import attn
-from .block import block_input, project
+from .block import Q4Weight, block_input, project
 
 
 def cache_slots(table, seq, positions, page_size: int):
@@ -39,18 +39,21 @@ def cache_slots(table, seq, positions, page_size: int):
     return torch.where(held, page * page_size + positions % page_size, -1)
 
 
-def _heads(x, weights, q_heads, cache, x_scale=None):
-    """(q, k, v): views into one packed projection."""
+def _heads(hidden, weights, q_heads, cache, norm, residual, eps, tokens_8bit):
+    """(q, k, v): views into one packed projection.  What can be refused is, before hidden goes into the residual stream."""
     Hkv, D = cache.kv_heads, cache.head_dim
-    if weights["qkv"].shape[0] != (q_heads + 2 * Hkv) * D:
-        raise ValueError(f"qkv weight has {weights['qkv'].shape[0]} rows, expected {(q_heads + 2 * Hkv) * D}")
-    x = project(x, weights["qkv"], x_scale).view(x.shape[0], q_heads + 2 * Hkv, D)
+    if tuple(weights["qkv"].shape) != ((q_heads + 2 * Hkv) * D, hidden.shape[1]):
+        raise ValueError(f"qkv weight is {tuple(weights['qkv'].shape)}, expected {((q_heads + 2 * Hkv) * D, hidden.shape[1])}")
+    if tokens_8bit and not isinstance(weights["qkv"], Q4Weight):
+        raise ValueError("8-bit tokens need a weight in 4 bits")
+    x, scale = block_input(hidden, norm, residual, eps=eps, tokens_8bit=tokens_8bit)
+    x = project(x, weights["qkv"], scale).view(x.shape[0], q_heads + 2 * Hkv, D)
     return x[:, :q_heads], x[:, q_heads:q_heads + Hkv], x[:, q_heads + Hkv:]
 
 
 def attn_block_prefill(hidden, weights: dict, q_heads: int, cache: "attn.KVCache", slots, cu_q, positions, freq, *,
-                       interleaved: bool = False, mscale: float = 1.0, context_slots=None, cu_k=None, norm=None, residual=None, eps: float = 1e-5,
-                       tokens_8bit: bool = False):
+                       interleaved: bool = False, mscale: float = 1.0, context_slots=None, cu_k=None, norm=None,
+                       residual=None, eps: float = 1e-5, tokens_8bit: bool = False):
     """hidden [T, d_model]: the new tokens of all sequences, packed (cu_q, int32 [batch + 1]), at cache rows `slots`
     and `positions` [T] int64; freq and mscale as rope_frequencies gives them.  weights: "qkv" [(Hq + 2 Hkv) D,
     d_model] and "out" [d_model, Hq D], each a tensor or a Q4Weight.  norm (fp32 [d_model]), residual [T, d_model] (updated
@@ -58,8 +61,7 @@ def attn_block_prefill(hidden, weights: dict, q_heads: int, cache: "attn.KVCache
     slots of all of each sequence's tokens, the new ones last, packed by cu_k (both or neither).  Returns [T, d_model]."""
     if (context_slots is None) != (cu_k is None):
         raise ValueError("context_slots and cu_k go together")
-    x, scale = block_input(hidden, norm, residual, eps=eps, tokens_8bit=tokens_8bit)
-    q, k, v = _heads(x, weights, q_heads, cache, scale)
+    q, k, v = _heads(hidden, weights, q_heads, cache, norm, residual, eps, tokens_8bit)
     attn.kv_write(k, v, cache, slots, q=q, positions=positions, freq=freq, interleaved=interleaved, mscale=mscale, q_out=q,
                   k_out=k)
     if context_slots is not None:
@@ -74,8 +76,7 @@ def attn_block_decode(hidden_t, weights: dict, q_heads: int, cache: "attn.KVCach
     """One token per sequence: hidden_t [B, d_model]; lens [B] int32 counts the sequence's tokens with the new one,
     which goes to position lens - 1 (a sequence of length 0 has none: nothing is written, its attention is
     zero).  table [B, width] int32.  norm, residual [B, d_model], eps and tokens_8bit as for a prompt.  Returns [B, d_model]."""
-    x, scale = block_input(hidden_t, norm, residual, eps=eps, tokens_8bit=tokens_8bit)
-    q, k, v = _heads(x, weights, q_heads, cache, scale)
+    q, k, v = _heads(hidden_t, weights, q_heads, cache, norm, residual, eps, tokens_8bit)
     positions = lens.long() - 1
     slots = cache_slots(table, torch.arange(table.shape[0], device=table.device), positions, cache.page_size)
     attn.kv_write(k, v, cache, slots, q=q, positions=positions, freq=freq, interleaved=interleaved, mscale=mscale, q_out=q)

@@ -62,3 +62,24 @@ def test_prompt_in_rows_that_no_one_stride_reaches(launched, which):
     with pytest.raises(RuntimeError, match="view"):
         prefill(t["hidden"], t["residual"])
     assert launched == []
+
+
+class Cache:
+    kv_heads, head_dim, page_size = 1, 8, 16
+
+
+@pytest.mark.parametrize("rows,tokens_8bit,match", [(3 * 8 + 1, False, "qkv weight"), (3 * 8, True, "4 bits")])
+@pytest.mark.parametrize("decode", [False, True])
+def test_attention_refuses_before_the_residual_stream_is_updated(launched, decode, rows, tokens_8bit, match):
+    """A call that is put right and made again must not add hidden twice."""
+    weights = {"qkv": torch.zeros(rows, DM), "out": torch.zeros(DM, 8)}
+    kw = dict(norm=torch.ones(DM), residual=torch.zeros(B, DM), tokens_8bit=tokens_8bit)
+    hidden, i32 = torch.zeros(B, DM), torch.int32
+    with pytest.raises(ValueError, match=match):
+        if decode:
+            attn_layer.attn_block_decode(hidden, weights, 1, Cache(), torch.zeros(B, 1, dtype=i32), torch.ones(B, dtype=i32),
+                                         torch.ones(4), **kw)
+        else:
+            attn_layer.attn_block_prefill(hidden, weights, 1, Cache(), torch.arange(B), torch.tensor([0, B], dtype=i32),
+                                          torch.arange(B), torch.ones(4), **kw)
+    assert launched == []
