@@ -24,12 +24,12 @@
  *              a row (k / 32).  Quantising: amax = max |w| of the group, rounded to three significant bits
  *              (half away from zero, bit pattern + 2^21), falls in 2^n .. 2^(n+1); e = n - 2 + 127, at most
  *              252; code = w * 2^(127 - e) to nearest, ties to the even code, at most 6 in magnitude.
- *              Groups with amax < 2^-100 get codes 0 and e = 127; what rounds to zero keeps its sign.  Every value is exact in bf16 for e in
- *              [2, 252]; other bytes are outside the contract.
+ *              Groups with amax < 2^-100 get codes 0 and e = 127; what rounds to zero keeps its sign.
+ *              Every value is exact in bf16 for e in [2, 252]; other bytes are outside the contract.
  *   linear     out[t, m] = x_scale[t] * sum_k x[t, k] w[m, k] (no x_scale for bf16 and fp32 tokens), sums
  *              in fp32.  Products are exact: bf16 tokens (and e4m3 tokens widened to it) multiply the
- *              exact 4-bit values on the matrix cores, fp32 tokens as three bf16 parts (to 2^-27 of them;
- *              magnitudes up to 2^127).  e4m3 tokens with an output in bf16 go through the instruction
+ *              exact 4-bit values on the matrix cores, fp32 tokens as three bf16 parts (to 2^-27 of them for
+ *              magnitudes from 2^-99 to 2^127).  e4m3 tokens with an output in bf16 go through the instruction
  *              that takes 8- and 4-bit values as they are: it aligns the products of eight columns to the
  *              largest and drops what is below 2^-13 of it.
  *              No sum is split differently from one call to the next: a call's bits depend on its sizes
@@ -87,7 +87,7 @@ typedef struct {
 
 /*
  * x [tokens, width] (io_dtype SSM_F32 or SSM_BF16), weight fp32 [width], width a multiple of 8 up to
- * SSM_NORM_MAX_WIDTH; eps finite and > 0.
+ * SSM_NORM_MAX_WIDTH; eps finite and at least 2^-126.
  * residual, residual_out [tokens, width] in residual_dtype (io_dtype, or SSM_F32): both or neither (NULL).
  * residual_out may be residual itself (in place: same data and stride).
  * out [tokens, width] in out_dtype: io_dtype, or SSM_E4M3 with scale fp32 [tokens] (NULL otherwise).

@@ -211,7 +211,7 @@ extern "C" int ssm_rms_norm(int64_t tokens, int64_t width, int32_t io_dtype, int
                             const ssm_rows* residual_out, const ssm_rows* out, float* scale, void* stream) {
   using namespace ssm::block;
   if (tokens < 0 || tokens > INT32_MAX || width < 8 || width > SSM_NORM_MAX_WIDTH || width % 8) return SSM_ERR_SHAPE;
-  if (!(eps > 0.0f) || !isfinite(eps)) return SSM_ERR_SHAPE;
+  if (!(eps >= 0x1p-126f) || !isfinite(eps)) return SSM_ERR_SHAPE;  // rsq takes no subnormal
   if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
   if (out_dtype != io_dtype && out_dtype != SSM_E4M3) return SSM_ERR_DTYPE;
   if (residual && residual_dtype != io_dtype && residual_dtype != SSM_F32) return SSM_ERR_DTYPE;

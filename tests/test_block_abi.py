@@ -87,6 +87,13 @@ def q4(codes=None, scales=None, m=M, k=K):
     return B._Q4(at(10) if codes is None else codes, at(11) if scales is None else scales, m, k)
 
 
+def test_norm_eps_is_a_normal_number():
+    """The reciprocal root of a row of zeros and a subnormal eps would be an infinity, the row NaN."""
+    for eps in (2.0 ** -149, 2.0 ** -127):
+        assert norm(eps=eps) == SHAPE
+    assert norm(eps=2.0 ** -126, tokens=0) == OK
+
+
 def test_sizes():
     lib = L.load()
     assert lib.ssm_q4_codes_bytes(M, K) == 6 * 2 * 1024 and lib.ssm_q4_scales_bytes(M, K) == 6 * 256

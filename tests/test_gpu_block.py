@@ -137,6 +137,15 @@ def test_norm_values():
     assert not c.float().any() and not s.any()  # below 2^-100
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30])
+def test_norm_smallest_eps(eps):
+    """A row of zeros stays zeros, and one beside it is the norm as if eps were none."""
+    x = torch.zeros(2, 64)
+    x[1] = torch.arange(64) - 31.5
+    y = check_norm(2, 64, "f32", None, False, x=x, eps=eps)
+    assert np.all(f64(y)[0] == 0)
+
+
 def test_norm_eps():
     x = rnd(5, 4, 128, scale=0.01)
     a, b = check_norm(4, 128, "f32", None, False, x=x, eps=1e-4), check_norm(4, 128, "f32", None, False, x=x, eps=1e-8)
