@@ -1,10 +1,10 @@
-// ssm_q4_few.hip -- ssm_q4_linear of include/ssm_block.h for up to 32 tokens (16 in fp32): bound by reading the weight once and by
-// the tokens' way to every CU.
+// ssm_q4_few.hip -- ssm_q4_linear of include/ssm_block.h for up to 32 tokens (16 in fp32) and, but for fp32, not too many rows
+// (few_takes): bound by reading the weight once and by the tokens' way to every CU.
 //
 // As in ssm_q4_rows.hip a wave takes NT tiles of 16 rows, and the waves of a workgroup share their columns; here a wave brings the
 // tokens of its own columns straight from memory to an LDS ring of its own, in whole lines, and no wave waits for another until
 // the sums are joined.  (Read to registers as operands, tokens come in pieces of 16 bytes of 16 rows, a quarter of the lines'
-// rate: 16 bf16 tokens by 4096 x 4096 take 6.2 us so and 5.0 through LDS, by 16384 x 4096 19 and 11.)
+// rate: 16 bf16 tokens by 4096 x 4096 take 6.2 us so and 5.0 through LDS.)
 #include "ssm_q4_linear.h"
 
 namespace ssm {
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64 * WAVES) void q4_few(const LinearArgs a, int spl
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         const int at = i * 1024 + lane * 16, t = at / RB;
-        const int off = min(t, last) * (int)a.x.stride + ((at % RB / 16) ^ swap_of<X>(t)) * 16;  // below 2^31: 63 rows of 2^23 bytes
+        const int off = min(t, last) * (int)a.x.stride + ((at % RB / 16) ^ swap_of<X>(t)) * 16;  // below 2^31: 31 rows of 2^23 bytes
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(void, ring + p * STAGE + i * 1024), 16, off, 0, 0, 0);
       }
     } else {  // the last step of an odd width: zeros past the last column
@@ -153,11 +153,14 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows to a workgroup: as few as fill the CUs once (16 bf16 tokens by 4096 x 4096 with 16, 32 or 64 rows: 5.0, 5.8, 7.9 us; by
-// 16384 x 4096 16.9, 14.1, 11.1).
+// Rows to a workgroup: as few as fill the CUs once (16 bf16 tokens by 4096 x 4096 with 16, 32 or 64 rows: 5.0, 5.8, 7.9 us).
 template <int X, int TT>
 hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
-  return a.mt <= 256 ? launch_tiles<X, 1, TT>(a, s) : a.mt <= 512 ? launch_tiles<X, 2, TT>(a, s) : launch_tiles<X, 4, TT>(a, s);
+  if constexpr (X == X_F32)
+    if (a.mt > 512) return launch_tiles<X, 4, TT>(a, s);
+  if constexpr (x_size<X>() > 1)
+    if (a.mt > 256) return launch_tiles<X, 2, TT>(a, s);
+  return launch_tiles<X, 1, TT>(a, s);
 }
 
 template <int X>

@@ -134,11 +134,18 @@ __device__ __forceinline__ void store_one(const LinearArgs& a, int64_t t, int64_
     reinterpret_cast<float*>(p)[m] = sum;
 }
 
-hipError_t launch_q4_rows(const LinearArgs& a, int x, hipStream_t s);   // up to rows_tokens(x)
-hipError_t launch_q4_few(const LinearArgs& a, int x, hipStream_t s);    // up to few_tokens(x)
-hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s);  // any number
-constexpr int64_t rows_tokens(int x) { return x == X_F32 ? 1 : 4; }
-constexpr int64_t few_tokens(int x) { return x == X_F32 ? 16 : 32; }
+hipError_t launch_q4_rows(const LinearArgs& a, int x, hipStream_t s);   // rows_takes
+hipError_t launch_q4_few(const LinearArgs& a, int x, hipStream_t s);    // few_takes
+hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s);  // any call
+inline bool rows_takes(const LinearArgs& a, int x) { return a.T <= (x == X_F32 ? 1 : 4); }
+// Up to 32 tokens, us in ssm_q4_few.hip and in tiles: where a weight's rows fill the CUs with tiles of 32 x 32, those win, since
+// the tokens are read once for 32 rows; with bf16 tokens once there are two to a CU.
+//   e4m3   32 by 4096 x 4096 5.0, 5.3; 6144 x 4096 7.3, 5.8; 16384 x 4096 11.6, 8.4; 16 by 4096 x 4096 4.1, 5.3
+//   bf16   32 by 4096 x 4096 6.2, 8.0; 8192 x 8192 11.6, 13.6; 10240 x 2560 8.7, 7.4; 16384 x 4096 12.5, 11.7
+//   fp32   16 by 8192 x 4096 11.0, 17.9; 65536 x 2560 41, 51
+inline bool few_takes(const LinearArgs& a, int x) {
+  return x == X_F32 ? a.T <= 16 : a.T <= 32 && a.mt <= (x == X_BF16 ? 512 : 256);
+}
 
 }  // namespace block
 }  // namespace ssm

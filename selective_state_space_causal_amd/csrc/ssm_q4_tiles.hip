@@ -435,22 +435,30 @@ hipError_t ring(const LinearArgs& a, hipStream_t s) {
 // ring's 128 x 128, 470 in 256 x 256).  e4m3 has room for two of 128 x 64 with two steps in the ring (600 by 4096 x 4096, 320
 // tiles: 18 us, 22 in 128 x 128), and from more than 512 tiles of 128 x 128 on 256 x 128 (4096 by 16384 x 4096 222 us, 2480
 // TFLOP/s, 255 in 128 x 128, 330 in q4_pair's way, 262 in 256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0).
+// Up to 32 and up to 64 tokens a tile has no more of them, however many rows there are: reading the weight bounds the call.
+// Without and with that, us: 32 bf16 tokens by 65536 x 2560 37, 18.5 (5.1 TB/s), by 32768 x 4096 19.7, 14.8; e4m3 17.7, 16.8 and
+// 14.0, 13.4; fp32 78, 55.  64 by 65536 x 2560 bf16 41, 31, e4m3 with an fp32 output 42, 29 (with a bf16 one 21 either way).
+// fp32 tokens by 64 rows where that is one to a CU: 32 by 16384 x 4096 28 us, 40 by 128 rows.
 template <int X>
 hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
   const auto once = [&](int bm, int bt) { return tiles_of(a, bm, bt) <= 256; };
   if constexpr (X == X_F32) {
     if (once(32, 32)) return ring<X, 32, 32, 1, 1, 4, 2>(a, s);
-    if (once(128, 32)) return ring<X, 128, 32, 4, 1, 2, 3>(a, s);
+    if (once(64, 32)) return ring<X, 64, 32, 2, 1, 2, 2>(a, s);
+    if (once(128, 32) || a.T <= 32) return ring<X, 128, 32, 4, 1, 2, 3>(a, s);
     return pair<X, 128, 64, 2, 2>(a, s);
   } else {
     constexpr bool E = x_size<X>() == 1;  // half of the LDS: more steps
     if (once(32, 32)) return ring<X, 32, 32, 1, 1, E ? 8 : 4, 3>(a, s);
     if (once(64, 32)) return ring<X, 64, 32, 2, 1, 4, E ? 3 : 2>(a, s);
+    if (a.T <= 32) return once(128, 32) ? ring<X, 128, 32, 4, 1, 2, 3>(a, s) : ring<X, 128, 32, 4, 1, 2, 2>(a, s);
     if (once(64, 64)) return ring<X, 64, 64, 2, 2, E ? 4 : 2, 3>(a, s);
     if (once(128, 64)) return ring<X, 128, 64, 4, 1, 2, E ? 4 : 2>(a, s);
     if constexpr (X == X_E4M3) {
       if (tiles_of(a, 128, 64) <= 512) return ring<X, 128, 64, 4, 1, 2, 2>(a, s);
       if (tiles_of(a, 128, 128) > 512) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
+    } else if (a.T <= 64) {
+      return E ? ring<X, 128, 64, 4, 1, 2, 2>(a, s) : ring<X, 128, 64, 4, 1, 1, 3>(a, s);
     }
     if constexpr (E) return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
     if (once(128, 128)) return ring<X, 128, 128, 4, 2, 1, 3>(a, s);
@@ -501,6 +509,8 @@ extern "C" int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype,
   a.wide = aligned(out->data, 16) && out->stride * os % 16 == 0;
   const int kind = x_dtype == SSM_E4M3 && out_dtype == SSM_F32 ? (int)X_WIDE : x_dtype;
   const hipStream_t s = ready(stream);
-  const hipError_t e = T <= rows_tokens(kind) ? launch_q4_rows(a, kind, s) : T <= few_tokens(kind) ? launch_q4_few(a, kind, s) : launch_q4_tiles(a, kind, s);
+  const hipError_t e = rows_takes(a, kind)  ? launch_q4_rows(a, kind, s)
+                       : few_takes(a, kind) ? launch_q4_few(a, kind, s)
+                                            : launch_q4_tiles(a, kind, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }

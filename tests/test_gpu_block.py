@@ -310,6 +310,15 @@ def test_linear_forms(T, M, K, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("T,M,K", [(7, 4100, 656), (5, 20005, 400), (32, 20000, 1168), (24, 12003, 528), (17, 34000, 272), (32, 33001, 1040),
+                                   (40, 33000, 272), (64, 32790, 912), (64, 66001, 144)])
+def test_linear_few_tokens_by_many_rows(T, M, K, kind):
+    """Up to 32 and up to 64 tokens have tiles of their own where there are more rows than CUs take at once."""
+    check_linear(T, M, K, kind, torch.bfloat16)
+    check_linear(T, M, K, kind, torch.float32, seed=1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
 @pytest.mark.parametrize("T", [1, 7, 16, 17, 40, 64, 150])
 def test_linear_by_the_identity_gives_the_tokens(T, kind):
     """Every value comes back from its own place, with all its bits (fp32: in three parts)."""
