@@ -429,12 +429,17 @@ hipError_t ring(const LinearArgs& a, hipStream_t s) {
 // The smallest tile of which there is at most one to a CU: each CU's share of the columns' way is then shortest, and no CU has
 // a second one while others have none.  us by tile, (32, 32), (64, 32), (64, 64), (128, 64), (128, 128) rows by tokens:
 //   bf16   128 tokens by 4096 x 4096   -, 9.9, 13.6, 17.6, 30     300 by 5120 x 2560   35, 23, 18, 12.7, 20
-//          64 by 16384 x 4096   29, 18, 13.9, 17.5, 30            600 by 4096 x 4096   (128, 64) 35.6, (128, 128) 30.8
+//          64 by 16384 x 4096   29, 18, 13.9, 17.5, 30
 //   e4m3   64 by 4096 x 8192   8.2, 10.8, 14.2, 22, 37            300 by 5120 x 2560   -, 19, 10.8, 10.4, 15
+// and past (128, 64) by 96, 128 and 192 tokens, the next form in brackets:
+//   bf16   600 by 4096 x 4096   24.5 [128: 29.9, 64: 34.5]   1000 by 2560 x 5120   30 [36.7, 41.6]
+//          1200 by 4096 x 4096   192: 43.5 [q4_pair 50.8]    1500 by 4096 x 4096   192: 47.5 [53]
+//   e4m3   600 by 4096 x 4096   16.4 [64, two to a CU: 17.8, 128: 20.4]; 192 is no better than what follows (25.7 and 25.2)
+//          with an fp32 output   25.9 [29.7, 33.4]           1500 by 4096 x 4096   192: 47 [54]
 // Past that the matrix cores are kept busy by two workgroups a CU: bf16 470 us for 4096 by 16384 x 4096 (1170 TFLOP/s; 555 in the
-// ring's 128 x 128, 470 in 256 x 256).  e4m3 has room for two of 128 x 64 with two steps in the ring (600 by 4096 x 4096, 320
-// tiles: 18 us, 22 in 128 x 128), and from more than 512 tiles of 128 x 128 on 256 x 128 (4096 by 16384 x 4096 222 us, 2480
-// TFLOP/s, 255 in 128 x 128, 330 in q4_pair's way, 262 in 256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0).
+// ring's 128 x 128, 470 in 256 x 256).  e4m3 has room for two of 128 x 64 with two steps in the ring (up to 512 tiles, 1000 by
+// 4096 x 4096), and from more than 512 tiles of 128 x 128 on 256 x 128 (4096 by 16384 x 4096 222 us, 2480 TFLOP/s, 255 in
+// 128 x 128, 330 in q4_pair's way, 262 in 256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0).
 // Up to 32 and up to 64 tokens a tile has no more of them, however many rows there are: reading the weight bounds the call.
 // Without and with that, us: 32 bf16 tokens by 65536 x 2560 37, 18.5 (5.1 TB/s), by 32768 x 4096 19.7, 14.8; e4m3 17.7, 16.8 and
 // 14.0, 13.4; fp32 78, 55.  64 by 65536 x 2560 bf16 41, 31, e4m3 with an fp32 output 42, 29 (with a bf16 one 21 either way).
@@ -454,14 +459,18 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
     if (a.T <= 32) return once(128, 32) ? ring<X, 128, 32, 4, 1, 2, 3>(a, s) : ring<X, 128, 32, 4, 1, 2, 2>(a, s);
     if (once(64, 64)) return ring<X, 64, 64, 2, 2, E ? 4 : 2, 3>(a, s);
     if (once(128, 64)) return ring<X, 128, 64, 4, 1, 2, E ? 4 : 2>(a, s);
-    if constexpr (X == X_E4M3) {
+    if (once(128, 96)) return ring<X, 128, 96, 4, 1, 2, X == X_E4M3 ? 3 : 2>(a, s);
+    if constexpr (E)
       if (tiles_of(a, 128, 64) <= 512) return ring<X, 128, 64, 4, 1, 2, 2>(a, s);
+    if constexpr (X == X_E4M3) {
       if (tiles_of(a, 128, 128) > 512) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
-    } else if (a.T <= 64) {
-      return E ? ring<X, 128, 64, 4, 1, 2, 2>(a, s) : ring<X, 128, 64, 4, 1, 1, 3>(a, s);
+    } else {
+      if (a.T <= 64) return ring<X, 128, 64, 4, 1, E ? 2 : 1, E ? 2 : 3>(a, s);
+      if constexpr (!E)
+        if (once(128, 128)) return ring<X, 128, 128, 4, 2, 1, 3>(a, s);
+      if (once(128, 192)) return ring<X, 128, 192, 4, 2, 1, 2>(a, s);
     }
     if constexpr (E) return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
-    if (once(128, 128)) return ring<X, 128, 128, 4, 2, 1, 3>(a, s);
     if constexpr (X == X_BF16) return pair<X, 128, 128, 2, 2>(a, s);
   }
   return hipErrorInvalidValue;
