@@ -1,5 +1,5 @@
-// ssm_block.h -- what the kernels of include/ssm_block.h (ssm_norm.hip, ssm_q4.hip, ssm_q4_rows.hip,
-// ssm_q4_tiles.hip) share: rows, the 4-bit layout and the host-side checks.
+// ssm_block.h -- what the kernels of include/ssm_block.h share (ssm_norm.hip, ssm_q4.hip; ssm_q4_rows.hip, ssm_q4_few.hip and
+// ssm_q4_tiles.hip by way of ssm_q4_linear.h): rows, the 4-bit layout and the host-side checks.
 #pragma once
 #include "../../include/ssm_block.h"
 #include "ssm_attn.h"

@@ -150,13 +150,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
         if constexpr (Q8) mx = fmaxf(mx, red[par][1][i]);
       }
     }
-    const float r = __builtin_amdgcn_rsqf(ss / (float)a.W + a.eps);
-    float m = 0.0f;
+    float r = __builtin_amdgcn_rsqf(ss / (float)a.W + a.eps), m = 0.0f;
     if constexpr (Q8) {
       const float amax = mx * r;
       const bool live = amax >= 0x1p-100f;
-      m = live ? (1.0f / amax) * 448.0f : 0.0f;
       if (tid == 0) a.scale[row] = live ? amax * (1.0f / 448.0f) : 0.0f;
+      // A code is h * weight over the row's largest, r over r: of r its power of two is enough, which rounds nothing.
+      r = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
+      m = live ? 448.0f / (mx * r) : 0.0f;
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {

@@ -96,7 +96,8 @@ __global__ __launch_bounds__(64 * WAVES) void quantize_tiles(const Q4Args a) {
 #pragma unroll
   for (int b = 0; b < 4; ++b)
     if (k4 * 4 + b < a.kt)
-      *reinterpret_cast<u32x4*>(a.codes + ((mt * a.kt + k4 * 4 + b) * 64 + lane) * 16) = *reinterpret_cast<const u32x4*>(x.group(4 * b + q, n));
+      *reinterpret_cast<u32x4*>(a.codes + ((mt * a.kt + k4 * 4 + b) * 64 + lane) * 16) =
+          *reinterpret_cast<const u32x4*>(x.group(4 * b + q, n));
   *reinterpret_cast<unsigned*>(a.scales + (tile * 64 + lane) * 4) = reinterpret_cast<const unsigned*>(x.scales)[lane];
 }
 
@@ -129,8 +130,9 @@ __global__ __launch_bounds__(64 * WAVES) void dequantize_tiles(const Q4Args a) {
     char* p = a.w.p + m * a.w.stride + k * (int64_t)sizeof(IO);
     if constexpr (sizeof(IO) == 2) {
       const auto two = [](auto v) { return __builtin_bit_cast(unsigned, v); };
-      *reinterpret_cast<u32x4*>(p) = u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
-                                           two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+      *reinterpret_cast<u32x4*>(p) = u32x4{
+          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
     } else {
       const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1),
                  v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);

@@ -99,7 +99,8 @@ __global__ __launch_bounds__(64 * WAVES) void q4_few(const LinearArgs a, int spl
 #pragma unroll
           for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int k = planes<X>() - 1; k >= 0; --k) acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][k], w, acc[t][i], 0, 0, 0);
+            for (int k = planes<X>() - 1; k >= 0; --k)
+              acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][k], w, acc[t][i], 0, 0, 0);
         }
       }
     }
@@ -173,7 +174,10 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_few(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32 ? launch<X_F32>(a, s) : x == X_BF16 ? launch<X_BF16>(a, s) : x == X_E4M3 ? launch<X_E4M3>(a, s) : launch<X_WIDE>(a, s);
+  return x == X_F32    ? launch<X_F32>(a, s)
+         : x == X_BF16 ? launch<X_BF16>(a, s)
+         : x == X_E4M3 ? launch<X_E4M3>(a, s)
+                       : launch<X_WIDE>(a, s);
 }
 
 }  // namespace block

@@ -50,14 +50,18 @@ __device__ __forceinline__ unsigned two(V v) {
 
 // Eight codes times s in bf16, exactly.
 __device__ __forceinline__ bf16x8 weights8(unsigned c, float s) {
-  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))});
+  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))});
 }
 
 // Eight e4m3 values in bf16, exactly.
 __device__ __forceinline__ bf16x8 widen8(unsigned lo, unsigned hi) {
-  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)), two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))});
+  return __builtin_bit_cast(bf16x8, u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                                          two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))});
 }
 
 // x = p[0] + p[1] + p[2], bf16 each, to 2^-27 of x: a part is rounded to nearest, so what it leaves is at most 2^-9 of it, and
@@ -97,7 +101,9 @@ struct Eight;
 template <>
 struct Eight<X_BF16> {
   bf16x8 v;
-  __device__ __forceinline__ void read(const char* row, int eighth, int swap) { v = *reinterpret_cast<const bf16x8*>(row + (eighth ^ swap) * 16); }
+  __device__ __forceinline__ void read(const char* row, int eighth, int swap) {
+    v = *reinterpret_cast<const bf16x8*>(row + (eighth ^ swap) * 16);
+  }
   __device__ __forceinline__ void parts(bf16x8 (&p)[1]) const { p[0] = v; }
 };
 template <>

@@ -63,8 +63,9 @@ __global__ __launch_bounds__(64 * WAVES) void q4_rows(const LinearArgs a, int sp
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float e = pow2(s[i] >> (8 * b) & 0xFFu);
-            const auto w0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[b][i][j], e, 0), w1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[b][i][j], e, 1),
-                       w2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[b][i][j], e, 2), w3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[b][i][j], e, 3);
+            const unsigned u = c[b][i][j];
+            const auto w0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, e, 0), w1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, e, 1),
+                       w2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, e, 2), w3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, e, 3);
             const float w[8] = {w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
 #pragma unroll
             for (int v = 0; v < 8; ++v) sum[i] = fmaf(w[v], __uint_as_float(x[b][2 * j + v / 4][v % 4]), sum[i]);
@@ -74,12 +75,13 @@ __global__ __launch_bounds__(64 * WAVES) void q4_rows(const LinearArgs a, int sp
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const i32x8 w = {(int)c[b][i][0], (int)c[b][i][1], (int)c[b][i][2], (int)c[b][i][3], 0, 0, 0, 0};
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xv, w, acc[i], 0, 4, 0, 0x7F7F7F7F, decltype(block)::value, (int)s[i]);
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xv, w, acc[i], 0, 4, 0, 0x7F7F7F7F, b, (int)s[i]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bf16x8 xv = X == X_BF16 ? __builtin_bit_cast(bf16x8, x[b][j % N]) : widen8(x[b][j / 2][j % 2 * 2], x[b][j / 2][j % 2 * 2 + 1]);
+          const bf16x8 xv = X == X_BF16 ? __builtin_bit_cast(bf16x8, x[b][j % N])
+                                        : widen8(x[b][j / 2][j % 2 * 2], x[b][j / 2][j % 2 * 2 + 1]);
 #pragma unroll
           for (int i = 0; i < NT; ++i)
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, weights8(c[b][i][j], pow2(s[i] >> (8 * b) & 0xFFu)), acc[i], 0, 0, 0);
@@ -140,7 +142,10 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_rows(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32 ? launch<X_F32>(a, s) : x == X_BF16 ? launch<X_BF16>(a, s) : x == X_E4M3 ? launch<X_E4M3>(a, s) : launch<X_WIDE>(a, s);
+  return x == X_F32    ? launch<X_F32>(a, s)
+         : x == X_BF16 ? launch<X_BF16>(a, s)
+         : x == X_E4M3 ? launch<X_E4M3>(a, s)
+                       : launch<X_WIDE>(a, s);
 }
 
 }  // namespace block

@@ -394,7 +394,8 @@ __global__ __launch_bounds__(64 * WM * WT * KG, 1) void q4_ring(const LinearArgs
 #pragma unroll
       for (int i = 0; i < NT * NM * 4; ++i) {
         const f32x16& v = acc[i / 4 / NM][i / 4 % NM];
-        if (group == g) mine[(g - 1) * (BM * BT / 4) + i * 64] = f32x4{v[i % 4 * 4], v[i % 4 * 4 + 1], v[i % 4 * 4 + 2], v[i % 4 * 4 + 3]};
+        const int e = i % 4 * 4;
+        if (group == g) mine[(g - 1) * (BM * BT / 4) + i * 64] = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
       }
     __syncthreads();
     if (group > 0) return;
@@ -479,7 +480,10 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32 ? launch_form<X_F32>(a, s) : x == X_BF16 ? launch_form<X_BF16>(a, s) : x == X_E4M3 ? launch_form<X_E4M3>(a, s) : launch_form<X_WIDE>(a, s);
+  return x == X_F32    ? launch_form<X_F32>(a, s)
+         : x == X_BF16 ? launch_form<X_BF16>(a, s)
+         : x == X_E4M3 ? launch_form<X_E4M3>(a, s)
+                       : launch_form<X_WIDE>(a, s);
 }
 
 }  // namespace block
@@ -500,7 +504,8 @@ extern "C" int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype,
   if (const int st = check_rows(out, os, os)) return st;
   if (!aligned(x_scale, 4)) return SSM_ERR_ALIGN;
   const Span so = rows_span(out, T, M, os);
-  if (overlaps(so, codes_span(q)) || overlaps(so, scales_span(q)) || overlaps(so, span(x_scale, x_scale ? T * 4 : 0))) return SSM_ERR_ALIAS;
+  if (overlaps(so, codes_span(q)) || overlaps(so, scales_span(q)) || overlaps(so, span(x_scale, x_scale ? T * 4 : 0)))
+    return SSM_ERR_ALIAS;
   if (!writable(out, T, M) || rows_overlap(out, M, os, x, K, es, T)) return SSM_ERR_ALIAS;
   LinearArgs a = {};
   a.x = rows_of(x, es);
