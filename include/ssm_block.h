@@ -109,7 +109,7 @@ int ssm_q4_dequantize(int32_t io_dtype, const ssm_q4_weight* q, const ssm_rows* 
 
 /*
  * out [tokens, M] (out_dtype SSM_F32 or SSM_BF16) from x [tokens, K] (x_dtype SSM_F32, SSM_BF16, or SSM_E4M3 with
- * x_scale fp32 [tokens]; NULL otherwise).  tokens below 2^24, tokens * M at most 2^36.
+ * x_scale fp32 [tokens]; NULL otherwise).  tokens below 2^24, tokens * M at most 2^35.
  */
 int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype, const ssm_rows* x, const float* x_scale,
                   const ssm_q4_weight* q, const ssm_rows* out, void* stream);

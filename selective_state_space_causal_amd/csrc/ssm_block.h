@@ -21,8 +21,9 @@ using attn::u32x4;
 
 constexpr int64_t MAX_ROW_STRIDE = int64_t(1) << 22;
 constexpr int64_t MAX_TOKENS = int64_t(1) << 24;
-// Most values of a 4-bit weight, and of a product's output: a launch has fewer than 2^32 work-items.
-constexpr int64_t MAX_WEIGHTS = int64_t(1) << 38, MAX_OUTPUTS = int64_t(1) << 36;
+// Most values of a 4-bit weight, and of a product's output: a launch has fewer than 2^32 work-items (at most one for 16 outputs,
+// and those of tiles that are not whole).
+constexpr int64_t MAX_WEIGHTS = int64_t(1) << 38, MAX_OUTPUTS = int64_t(1) << 35;
 
 // Rows with a byte stride.
 struct Rows {

@@ -5,7 +5,7 @@
 // waves that use them (one conversion for two weights).  Many tiles are bound by the matrix cores, few by a step's own latency
 // and by how many CUs have one; so the form goes by how many tiles there are (launch_form).
 //   q4_ring   everything goes straight from memory to a ring of steps in LDS; groups of waves share a tile's columns
-//   q4_pair   bf16 and fp32 tokens, many tiles: tokens through two LDS buffers, the weight straight into the operands
+//   q4_pair   bf16 and fp32 tokens, more tiles than that: tokens through two LDS buffers, the weight straight into the operands
 #include "ssm_q4_linear.h"
 
 namespace ssm {
@@ -81,13 +81,13 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, const f32x16 (&a
 
 // ---------------------------------------------------------------- many tiles
 
-// WM x WT waves, along rows and along tokens.  Tokens lie in LDS as bf16, fp32 ones as three planes of parts; bf16 tokens go there
-// straight from memory.
-template <int X, int BM, int BT, int WM, int WT>
-__global__ __launch_bounds__(64 * WM * WT, X == X_F32 ? 1 : 2) void q4_pair(const LinearArgs a) {
+// NW waves along the rows, so that each weight is loaded and converted once.  Tokens lie in LDS as bf16, fp32 ones as three planes of
+// parts; bf16 tokens go there straight from memory.
+template <int X, int BM, int BT, int NW>
+__global__ __launch_bounds__(64 * NW, X == X_F32 ? 1 : 2) void q4_pair(const LinearArgs a) {
   constexpr int ES = x_size<X>(), PL = planes<X>(), RB = 256, PLANE = BT * RB, TILE = PLANE * PL;
-  constexpr int NW = WM * WT, THREADS = 64 * NW;
-  constexpr int NT = BT / WT / 32, NM = BM / WM / 32;  // a wave's 32 x 32 tiles
+  constexpr int THREADS = 64 * NW;
+  constexpr int NT = BT / 32, NM = BM / NW / 32;  // a wave's 32 x 32 tiles
   constexpr int PIECES = BT * 128 * ES / 16 / THREADS;  // 16-byte loads of a thread for a step's tokens
   static_assert((X == X_BF16 || X == X_F32) && PIECES * THREADS * 16 == BT * 128 * ES && 2 * TILE <= 160 * 1024, "");
   __shared__ __attribute__((aligned(16))) char lds[2 * TILE];
@@ -95,9 +95,9 @@ __global__ __launch_bounds__(64 * WM * WT, X == X_F32 ? 1 : 2) void q4_pair(cons
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l32 = lane % 32, h = lane / 32;
   const Tile tile = tile_of(blockIdx.x, (unsigned)((a.T + BT - 1) / BT), (unsigned)((a.M + BM - 1) / BM));
   const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane(tile.t) * BT, m0 = (int64_t)__builtin_amdgcn_readfirstlane(tile.m) * BM;
-  const int wt = wave % WT * (NT * 32), wm = wave / WT * (NM * 32), steps = (int)a.kt;
+  const int wm = wave * (NM * 32), steps = (int)a.kt;
 
-  // a lane's rows of the weight, from the workgroup's first: below 2^27 (8 tiles of 16 rows, 2^13 of 128 columns, 1 KB each)
+  // a lane's rows of the weight, from the workgroup's first: at most 2^27 (16 tiles of 16 rows, 2^13 of 128 columns, 1 KB each)
   const int64_t first = m0 / 16;
   const char* const cbase = a.codes + first * a.kt * 1024;
   const char* const sbase = a.scales + first * a.k4 * 256;
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(64 * WM * WT, X == X_F32 ? 1 : 2) void q4_pair(cons
   // once, for which there are no registers.
   f32x16 acc[NT][NM] = {};
   const auto multiply = [&](const char* buf, const u32x4 (&cc)[NM][2], const unsigned (&ss)[NM][2]) {
-    const char* rows = buf + (wt + l32) * RB;  // of the first tile of tokens; wt and 32 are multiples of what swap_of repeats at
+    const char* rows = buf + l32 * RB;  // of the first tile of tokens; 32 is a multiple of what swap_of repeats at
     const int swap = swap_of<X>(l32);
     bf16x8 x[2][NT][PL];
     const auto read = [&](int n) {  // product n: columns 64 (n / 4) + 32 h + 8 (n % 4)
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(64 * WM * WT, X == X_F32 ? 1 : 2) void q4_pair(cons
     step(kb, lds, lds + TILE, 0);
     if (kb + 1 < steps) step(kb + 1, lds + TILE, lds, 1);
   }
-  store_tile<X>(a, acc, t0 + wt + l32, m0 + wm, h);
+  store_tile<X>(a, acc, t0 + l32, m0 + wm, h);
 }
 
 // ---------------------------------------------------------------- fewer tiles, and e4m3
@@ -415,9 +415,9 @@ __global__ __launch_bounds__(64 * WM * WT * KG, 1) void q4_ring(const LinearArgs
 
 int64_t tiles_of(const LinearArgs& a, int bm, int bt) { return (a.T + bt - 1) / bt * ((a.M + bm - 1) / bm); }
 
-template <int X, int BM, int BT, int WM, int WT>
+template <int X, int BM, int BT, int NW>
 hipError_t pair(const LinearArgs& a, hipStream_t s) {
-  q4_pair<X, BM, BT, WM, WT><<<dim3((unsigned)tiles_of(a, BM, BT)), dim3(64 * WM * WT), 0, s>>>(a);
+  q4_pair<X, BM, BT, NW><<<dim3((unsigned)tiles_of(a, BM, BT)), dim3(64 * NW), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -427,23 +427,49 @@ hipError_t ring(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// q4_pair in the tile whose fullest CU has the fewest products, each tile's weighed by what it takes for the same ones where there
+// are many tiles.  us in the tiles in this order, rows by tokens:
+//   bf16   (256, 128), (256, 96), (256, 64), (128, 96), (128, 64)
+//     4096 by 16384 x 4096   399 (1378 TFLOP/s), 422, 426, 442, 448; with four waves of 64 x 64 in (128, 128) 460
+//     1000 by 4096 x 4096   51, 42, 32.9, 39, 32.7     1200   51, 42.4, 47, 42.0, 42.9     1600   52, 66, 51, 57, 54
+//     2048 by 4096 x 4096   57, 69, 58, 63, 60         2200   84, 70, 76, 64.6, 71         3000   89, 81, 84, 87, 87
+//   fp32   (256, 32), (128, 32)
+//     4096 by 4096 x 4096   352, 405; in (128, 64) 498   1000   91, 110   600   75, 73   300 by 5120 x 2560   29, 33
+//     300 by 2560 x 2560   28, 23                        64 by 65536 x 2560   62, 75
+template <int X>
+hipError_t pair_form(const LinearArgs& a, hipStream_t s) {
+  const auto cost = [&](int bm, int bt, int us) { return (tiles_of(a, bm, bt) + 255) / 256 * (bm * bt / 64) * us; };
+  if constexpr (X == X_F32) return cost(256, 32, 352) <= cost(128, 32, 405) ? pair<X, 256, 32, 8>(a, s) : pair<X, 128, 32, 4>(a, s);
+  const int64_t c[5] = {cost(256, 128, 399), cost(256, 96, 422), cost(256, 64, 426), cost(128, 96, 442), cost(128, 64, 448)};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (c[i] < c[best]) best = i;
+  if constexpr (X == X_BF16)
+    return best == 0   ? pair<X, 256, 128, 4>(a, s)
+           : best == 1 ? pair<X, 256, 96, 4>(a, s)
+           : best == 2 ? pair<X, 256, 64, 4>(a, s)
+           : best == 3 ? pair<X, 128, 96, 4>(a, s)
+                       : pair<X, 128, 64, 4>(a, s);
+  return hipErrorInvalidValue;
+}
+
 // The smallest tile of which there is at most one to a CU: each CU's share of the columns' way is then shortest, and no CU has
 // a second one while others have none.  us by tile, (32, 32), (64, 32), (64, 64), (128, 64), (128, 128) rows by tokens:
 //   bf16   128 tokens by 4096 x 4096   -, 9.9, 13.6, 17.6, 30     300 by 5120 x 2560   35, 23, 18, 12.7, 20
 //          64 by 16384 x 4096   29, 18, 13.9, 17.5, 30
 //   e4m3   64 by 4096 x 8192   8.2, 10.8, 14.2, 22, 37            300 by 5120 x 2560   -, 19, 10.8, 10.4, 15
-// and past (128, 64) by 96, 128 and 192 tokens, the next form in brackets:
-//   bf16   600 by 4096 x 4096   24.5 [128: 29.9, 64: 34.5]   1000 by 2560 x 5120   30 [36.7, 41.6]
-//          1200 by 4096 x 4096   192: 43.5 [q4_pair 50.8]    1500 by 4096 x 4096   192: 47.5 [53]
-//   e4m3   600 by 4096 x 4096   16.4 [64, two to a CU: 17.8, 128: 20.4]; 192 is no better than what follows (25.7 and 25.2)
-//          with an fp32 output   25.9 [29.7, 33.4]           1500 by 4096 x 4096   192: 47 [54]
-// Past that the matrix cores are kept busy by two workgroups a CU: bf16 470 us for 4096 by 16384 x 4096 (1170 TFLOP/s; 555 in the
-// ring's 128 x 128, 470 in 256 x 256).  e4m3 has room for two of 128 x 64 with two steps in the ring (up to 512 tiles, 1000 by
-// 4096 x 4096), and from more than 512 tiles of 128 x 128 on 256 x 128 (4096 by 16384 x 4096 222 us, 2480 TFLOP/s, 255 in
-// 128 x 128, 330 in q4_pair's way, 262 in 256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0).
+// 96 tokens by 128 rows is the largest of those (600 by 4096 x 4096, [the next form]: bf16 24.5 [29.9], e4m3 16.4 [17.8], e4m3
+// with an fp32 output 25.9 [29.7]).  Past that:
+//   bf16   q4_pair in the tile whose fullest CU has the least to multiply (pair_form)
+//   e4m3   up to 512 tiles of 128 x 64 with two steps in the ring, two or three of them to a CU (1000 by 4096 x 4096), up to 512
+//          of 128 x 128, then 256 x 128: 4096 by 16384 x 4096 222 us, 2480 TFLOP/s (255 in 128 x 128, 330 in q4_pair's way, 262 in
+//          256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0)
+//   e4m3 with an fp32 output   the same up to 512 tiles of 128 x 64; then 128 x 192 where that is one to a CU (1500 by
+//          4096 x 4096 47 us, 54 in 128 x 128); 256 x 128 where that is (2048 by 4096 x 4096 58.6, 63) and from more than 768
+//          tiles of 128 x 128 on (4096 by 16384 x 4096 412, 453; 3000 by 4096 x 4096, 768 tiles, 90 either way); else 128 x 128
 // Up to 32 and up to 64 tokens a tile has no more of them, however many rows there are: reading the weight bounds the call.
 // Without and with that, us: 32 bf16 tokens by 65536 x 2560 37, 18.5 (5.1 TB/s), by 32768 x 4096 19.7, 14.8; e4m3 17.7, 16.8 and
-// 14.0, 13.4; fp32 78, 55.  64 by 65536 x 2560 bf16 41, 31, e4m3 with an fp32 output 42, 29 (with a bf16 one 21 either way).
+// 14.0, 13.4.  64 by 65536 x 2560 bf16 41, 31, e4m3 with an fp32 output 42, 29 (with a bf16 one 21 either way).
 // fp32 tokens by 64 rows where that is one to a CU: 32 by 16384 x 4096 28 us, 40 by 128 rows.
 template <int X>
 hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
@@ -451,8 +477,7 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
   if constexpr (X == X_F32) {
     if (once(32, 32)) return ring<X, 32, 32, 1, 1, 4, 2>(a, s);
     if (once(64, 32)) return ring<X, 64, 32, 2, 1, 2, 2>(a, s);
-    if (once(128, 32) || a.T <= 32) return ring<X, 128, 32, 4, 1, 2, 3>(a, s);
-    return pair<X, 128, 64, 2, 2>(a, s);
+    return pair_form<X>(a, s);
   } else {
     constexpr bool E = x_size<X>() == 1;  // half of the LDS: more steps
     if (once(32, 32)) return ring<X, 32, 32, 1, 1, E ? 8 : 4, 3>(a, s);
@@ -463,16 +488,15 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
     if (once(128, 96)) return ring<X, 128, 96, 4, 1, 2, X == X_E4M3 ? 3 : 2>(a, s);
     if constexpr (E)
       if (tiles_of(a, 128, 64) <= 512) return ring<X, 128, 64, 4, 1, 2, 2>(a, s);
-    if constexpr (X == X_E4M3) {
-      if (tiles_of(a, 128, 128) > 512) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
-    } else {
+    if constexpr (X != X_E4M3)
       if (a.T <= 64) return ring<X, 128, 64, 4, 1, E ? 2 : 1, E ? 2 : 3>(a, s);
-      if constexpr (!E)
-        if (once(128, 128)) return ring<X, 128, 128, 4, 2, 1, 3>(a, s);
+    if constexpr (X == X_BF16) return pair_form<X>(a, s);
+    if constexpr (X == X_WIDE)
       if (once(128, 192)) return ring<X, 128, 192, 4, 2, 1, 2>(a, s);
+    if constexpr (E) {
+      if (tiles_of(a, 128, 128) > (X == X_E4M3 ? 512 : 768) || (X == X_WIDE && once(256, 128))) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
+      return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
     }
-    if constexpr (E) return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
-    if constexpr (X == X_BF16) return pair<X, 128, 128, 2, 2>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -145,6 +145,14 @@ def test_linear_validation():
     assert linear(o=rows(1, stride=M - 1)) == ALIAS
     assert linear(x_dtype=E4M3, xs=at(2), o=rows(2, M)) == ALIAS
 
+def test_linear_has_a_most_of_outputs():
+    """What one launch's work-items can reach: 2^35 outputs."""
+    lib, m = L.load(), 1 << 20
+    q = B._Q4(at(2), at(6), m, K)
+    for tokens, st in ((1 << 15) + 1, SHAPE), ((1 << 24) - 1, SHAPE), (1 << 15, NULL):
+        assert lib.ssm_q4_linear(tokens, BF16, BF16, None, None, q, rows(5, m), None) == st
+
+
 
 def test_python_refusals_name_the_argument():
     """Host tensors: everything is refused before a launch."""

@@ -300,7 +300,8 @@ def test_linear(T, M, K, kind):
 # Sizes that reach each form of the calls of few tokens (rows of a workgroup) and of tiles (how many there are).
 FORMS = [(1, 9000, 144), (4, 8209, 656), (12, 5000, 400), (16, 9000, 144), (20, 5000, 144), (32, 8300, 528), (300, 1000, 2064),
          (520, 1000, 2064), (1000, 1100, 2064), (1030, 2100, 1552), (2050, 2100, 1040), (2100, 2101, 400), (3000, 3100, 528),
-         (91, 28001, 272), (600, 3900, 1040), (1510, 4090, 272), (1010, 4001, 272), (1300, 4095, 400)]
+         (91, 28001, 272), (600, 3900, 1040), (1510, 4090, 272), (1010, 4001, 272), (1300, 4095, 400),
+         (2040, 4090, 272), (2200, 4090, 144), (4100, 3200, 400)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
