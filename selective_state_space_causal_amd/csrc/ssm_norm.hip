@@ -10,8 +10,8 @@
 // it is also the faster form for many rows (two pieces to a thread and half the threads, us: 2560 values, 1 row 2.5 against
 // 2.2, 2048 rows 9.0 against 7.9; 4096, 1024 rows 7.8 against 6.7; 8192, 2048 rows 27.9 against 25.4).  Up to 128 values 16
 // threads, so that a wave has four rows (100000 rows of 128: 18 us, 25 with a wave for each).  A workgroup takes rows in turn
-// and loads the next one before it reduces this one.  32768 rows of 4096, bf16 with residual to e4m3: 178 us, 5.3 TB/s, what
-// a copy reaches.
+// and loads the next one before it reduces this one.  32768 rows of 4096, bf16 with residual to e4m3: 162 us, 5.8 TB/s,
+// more than a copy reaches.
 #include "ssm_block.h"
 
 namespace ssm {
@@ -178,7 +178,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
 template <typename IO, int RES, bool Q8, int TPR, int P>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, TPB = TPR < 256 ? 256 : TPR;
-  const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * (2048 / TPB);  // 2048 threads to a CU
+  // 2048 threads to a CU; of 512 for many rows half as many, whose rows are fewer places of memory at once (32768 rows of 4096, bf16
+  // with residual to e4m3 162 us, 180 with 2048; to bf16 193, 209; 1000 rows 6.6, 6.4; rows of 2048 without residual 46, 39)
+  const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * ((TPB == 512 && a.T >= 2048 ? 1024 : 2048) / TPB);
   rms_rows<IO, RES, Q8, TPR, P><<<dim3((unsigned)(want < most ? want : most)), dim3(TPB), 0, s>>>(a);
   return hipGetLastError();
 }
