@@ -16,8 +16,8 @@
  *              there is no residual); r = 1 / sqrt(mean(h^2) + eps); y = (h * weight) * r, fp32, rounded
  *              once to the output's dtype.  (h^2 is fp32: magnitudes stay below 2^63.)
  *   8-bit rows one fp32 scale per row: amax = max |y|, s = amax * (1 / 448); code = e4m3, nearest even, of
- *              (h * weight) * (448 / max |h * weight|), which is y * (448 / amax) with fewer roundings (each
- *              operation rounded to fp32), at most 448 in magnitude; value = code * s.  Rows with amax < 2^-100
+ *              (h * weight) * (448 / max |h * weight|), which is y * (448 / amax) with fewer roundings (in fp64,
+ *              rounded to fp32 before; rows of more than 8192 values in fp32); value = code * s.  Rows with amax < 2^-100
  *              get s = 0 and codes 0.
  *   4-bit      w[m, k] = c * 2^(e - 127): c one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (e2m1:
  *              sign, two bits of exponent, one of mantissa, in code order), e a byte for each 32 values of

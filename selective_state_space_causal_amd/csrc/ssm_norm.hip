@@ -62,13 +62,25 @@ __device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
   return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(in(c), in(d), w, true);
 }
 
+// 448 / x in fp64, x > 0: the reciprocal instruction and two steps of Newton's, each of which squares what is missing.
+__device__ __forceinline__ double top_over(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  y = fma(fma(-x, y, 1.0), y, y);
+  y = fma(fma(-x, y, 1.0), y, y);
+  return 448.0 * y;
+}
+
 // TPR threads to a row, P pieces of 8 values to a thread; workgroups of max(256, TPR) threads.
 template <typename IO, int RES, bool Q8, int TPR, int P>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs a) {
   using R = typename std::conditional<RES == F32_RES, float, IO>::type;
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, NW = TPR < 64 ? 1 : TPR / 64;
   constexpr bool AHEAD = P <= 2;  // more pieces leave no registers for the next row
-  __shared__ float red[2][2][NW];
+  // h * weight: of 8-bit rows in fp64, so that a code is that of the definition (of 134 million none was another, 58 in fp32), where
+  // the registers allow (32768 values: 138 us for 1024 rows so, 84 in fp32).
+  using Max = typename std::conditional<Q8 && P == 1, double, float>::type;
+  __shared__ float red[2][NW];
+  __shared__ Max red_max[2][Q8 ? NW : 1];
   const int tid = threadIdx.x % TPR;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -97,7 +109,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
   };
   if (row < a.T) load(row);
   for (int par = 0; row < a.T; row += step, par ^= 1) {
-    float h[P][8], ss = 0.0f, mx = 0.0f;
+    float h[P][8], ss = 0.0f;
+    Max z[P][8], mx = 0;
     if (!AHEAD && row >= step) load(row);  // the first was loaded above
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -126,38 +139,43 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = fmaf(h[p][i], h[p][i], ss);
-        h[p][i] *= w[p][i];
-        if constexpr (Q8) mx = fmaxf(mx, fabsf(h[p][i]));
+        z[p][i] = (Max)h[p][i] * (Max)w[p][i];
+        if constexpr (Q8) mx = fmax(mx, fabs(z[p][i]));
       }
     }
     if (AHEAD && row + step < a.T) load(row + step);
 #pragma unroll
     for (int off = TPR < 64 ? TPR / 2 : 32; off >= 1; off >>= 1) {
       ss += __shfl_xor(ss, off, 64);
-      if constexpr (Q8) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+      if constexpr (Q8) mx = fmax(mx, __shfl_xor(mx, off, 64));
     }
     if constexpr (NW > 1) {  // rows alternate between two buffers: one barrier a row
       if (tid % 64 == 0) {
-        red[par][0][tid / 64] = ss;
-        if constexpr (Q8) red[par][1][tid / 64] = mx;
+        red[par][tid / 64] = ss;
+        if constexpr (Q8) red_max[par][tid / 64] = mx;
       }
       __syncthreads();
-      ss = red[par][0][0];
-      if constexpr (Q8) mx = red[par][1][0];
+      ss = red[par][0];
+      if constexpr (Q8) mx = red_max[par][0];
 #pragma unroll
       for (int i = 1; i < NW; ++i) {
-        ss += red[par][0][i];
-        if constexpr (Q8) mx = fmaxf(mx, red[par][1][i]);
+        ss += red[par][i];
+        if constexpr (Q8) mx = fmax(mx, red_max[par][i]);
       }
     }
-    float r = __builtin_amdgcn_rsqf(ss / (float)a.W + a.eps), m = 0.0f;
+    float r = __builtin_amdgcn_rsqf(ss / (float)a.W + a.eps);
+    Max m = 0;
     if constexpr (Q8) {
-      const float amax = mx * r;
+      const float amax = (float)(mx * (Max)r);
       const bool live = amax >= 0x1p-100f;
       if (tid == 0) a.scale[row] = live ? amax * (1.0f / 448.0f) : 0.0f;
-      // A code is h * weight over the row's largest, r over r: of r its power of two is enough, which rounds nothing.
-      r = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
-      m = live ? 448.0f / (mx * r) : 0.0f;
+      // A code is h * weight over the row's largest, r over r: of r its power of two is enough, which rounds nothing (fp64: none).
+      if constexpr (sizeof(Max) == 8) {
+        m = live ? top_over(mx) : 0.0;
+      } else {
+        r = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
+        m = live ? 448.0f / (mx * r) : 0.0f;
+      }
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -165,10 +183,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
       const int64_t e = (p * TPR + tid) * 8;
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = h[p][i] * r;
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (!Q8)
+          y[i] = z[p][i] * r;
+        else if constexpr (sizeof(Max) == 8)
+          y[i] = (float)(z[p][i] * m);
+        else
+          y[i] = z[p][i] * r * m;
+      }
       if constexpr (Q8)
         *reinterpret_cast<u32x2*>(a.out.p + row * a.out.stride + e) =
-            u32x2{codes4(y[0] * m, y[1] * m, y[2] * m, y[3] * m), codes4(y[4] * m, y[5] * m, y[6] * m, y[7] * m)};
+            u32x2{codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7])};
       else
         store8<IO>(a.out.p + row * a.out.stride + e * sizeof(IO), y);
     }
