@@ -204,8 +204,10 @@ template <typename IO, int RES, bool Q8, int TPR, int P>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, TPB = TPR < 256 ? 256 : TPR;
   // 2048 threads to a CU; of 512 for many rows half as many, whose rows are fewer places of memory at once (32768 rows of 4096, bf16
-  // with residual to e4m3 162 us, 180 with 2048; to bf16 193, 209; 1000 rows 6.6, 6.4; rows of 2048 without residual 46, 39)
-  const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * ((TPB == 512 && a.T >= 2048 ? 1024 : 2048) / TPB);
+  // with residual to e4m3 162 us, 180 with 2048; to bf16 193, 209; 1000 rows 6.6, 6.4; rows of 2048 without residual 46, 39).  Of 256 to 8 bits the registers leave room for
+  // 1536 (32768 rows of 1024 48 us, 56 with 2048, of which some would wait for the others' end)
+  constexpr int MANY = TPB == 512 ? 1024 : TPB == 256 && Q8 ? 1536 : 2048;
+  const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * ((a.T >= 2048 ? MANY : 2048) / TPB);
   rms_rows<IO, RES, Q8, TPR, P><<<dim3((unsigned)(want < most ? want : most)), dim3(TPB), 0, s>>>(a);
   return hipGetLastError();
 }
