@@ -71,37 +71,23 @@ __global__ __launch_bounds__(64 * WAVES) void q4_few(const LinearArgs a, int spl
   const auto multiply = [&](int p) {
     const char* rows = ring + p * STAGE + n * RB;
     const int swap = swap_of<X>(n);
-    if constexpr (X == X_E4M3) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf16x8 x[TT][planes<X>()];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        const u32x4 lo = *reinterpret_cast<const u32x4*>(rows + t * 16 * RB + (q ^ swap) * 16);
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(rows + t * 16 * RB + ((4 + q) ^ swap) * 16);
-        const i32x8 x = __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const i32x8 w = {(int)c[p][i][0], (int)c[p][i][1], (int)c[p][i][2], (int)c[p][i][3], 0, 0, 0, 0};
-          acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, w, acc[t][i], 0, 4, 0, 0x7F7F7F7F, 0, (int)s[p][i]);
-        }
+        Eight<X> e;
+        e.read(rows + t * 16 * RB, 4 * q + j, swap);
+        e.parts(x[t]);
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 x[TT][planes<X>()];
+      for (int i = 0; i < NT; ++i) {
+        const bf16x8 w = weights8(c[p][i][j], pow2(s[p][i]));
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          Eight<X> e;
-          e.read(rows + t * 16 * RB, 4 * q + j, swap);
-          e.parts(x[t]);
-        }
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const bf16x8 w = weights8(c[p][i][j], pow2(s[p][i]));
-#pragma unroll
-          for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int k = planes<X>() - 1; k >= 0; --k)
-              acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][k], w, acc[t][i], 0, 0, 0);
-        }
+          for (int k = planes<X>() - 1; k >= 0; --k)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][k], w, acc[t][i], 0, 0, 0);
       }
     }
   };
@@ -174,10 +160,7 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_few(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32    ? launch<X_F32>(a, s)
-         : x == X_BF16 ? launch<X_BF16>(a, s)
-         : x == X_E4M3 ? launch<X_E4M3>(a, s)
-                       : launch<X_WIDE>(a, s);
+  return x == X_F32 ? launch<X_F32>(a, s) : x == X_BF16 ? launch<X_BF16>(a, s) : launch<X_E4M3>(a, s);
 }
 
 }  // namespace block

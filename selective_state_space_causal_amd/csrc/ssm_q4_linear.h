@@ -9,8 +9,6 @@
 namespace ssm {
 namespace block {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 struct LinearArgs {
   Rows x, out;
   const char* codes;
@@ -22,11 +20,10 @@ struct LinearArgs {
   bool wide;                // output rows are aligned to 16 bytes
 };
 
-// How tokens are multiplied.  e4m3 tokens go into the instruction that takes codes as they are (X_E4M3); for an output in fp32
-// they are widened to bf16 (X_WIDE): that instruction aligns the products of eight columns to the largest of them and keeps
-// 2^-13 of it, which is far below a bf16 output's own rounding (4.5e-6 of a result of 1552 columns, against 2^-9), and not
-// what an fp32 output is asked for.
-enum { X_F32 = SSM_F32, X_BF16 = SSM_BF16, X_E4M3 = SSM_E4M3, X_WIDE = 3 };
+// Tokens by their type.  e4m3 ones are widened to bf16, which is exact, as the codes are.  (The instruction that takes 8- and 4-bit
+// values as they are does not sum in fp32: it aligns the products of eight columns to the largest of them and drops what is
+// below 2^-13 of it.  Beside a column of 448 that another one cancels, results of 9.16 came out as 9.63 in bf16.)
+enum { X_F32 = SSM_F32, X_BF16 = SSM_BF16, X_E4M3 = SSM_E4M3 };
 
 template <int X>
 constexpr int x_size() {  // bytes of a token's value
@@ -34,7 +31,7 @@ constexpr int x_size() {  // bytes of a token's value
 }
 template <int X>
 constexpr bool x_scaled() {
-  return X == X_E4M3 || X == X_WIDE;
+  return X == X_E4M3;
 }
 template <int X>
 constexpr int planes() {  // bf16 parts of a value
@@ -64,8 +61,8 @@ __device__ __forceinline__ bf16x8 widen8(unsigned lo, unsigned hi) {
                                           two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))});
 }
 
-// x = p[0] + p[1] + p[2], bf16 each, to 2^-27 of x: a part is rounded to nearest, so what it leaves is at most 2^-9 of it, and
-// exact in fp32.
+// x = p[0] + p[1] + p[2], bf16 each, exactly, while no part overflows or is subnormal: a part holds 8 of x's 24 bits, rounded to
+// nearest, and what it leaves is exact in fp32, at most half of its last place: 16 bits, then 8.
 __device__ __forceinline__ void three_parts(const float (&x)[8], bf16x8 (&p)[3]) {
   float r[8];
 #pragma unroll
@@ -107,7 +104,7 @@ struct Eight<X_BF16> {
   __device__ __forceinline__ void parts(bf16x8 (&p)[1]) const { p[0] = v; }
 };
 template <>
-struct Eight<X_WIDE> {
+struct Eight<X_E4M3> {
   u32x2 v;
   __device__ __forceinline__ void read(const char* row, int eighth, int swap) {
     v = *reinterpret_cast<const u32x2*>(row + (eighth / 2 ^ swap) * 16 + eighth % 2 * 8);
@@ -146,7 +143,7 @@ hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s);  // any c
 inline bool rows_takes(const LinearArgs& a, int x) { return a.T <= (x == X_F32 ? 1 : 4); }
 // Up to 32 tokens, us in ssm_q4_few.hip and in tiles: where a weight's rows fill the CUs with tiles of 32 x 32, those win, since
 // the tokens are read once for 32 rows; with bf16 tokens once there are two to a CU.
-//   e4m3   32 by 4096 x 4096 5.0, 5.3; 6144 x 4096 7.3, 5.8; 16384 x 4096 11.6, 8.4; 16 by 4096 x 4096 4.1, 5.3
+//   e4m3   32 by 4096 x 4096 5.7, 6.3; 6144 x 4096 10.9, 6.5; 16384 x 4096 20, 9.6; 16 by 4096 x 4096 4.6, 6.2; 6144 x 4096 6.5, 6.3
 //   bf16   32 by 4096 x 4096 6.2, 8.0; 8192 x 8192 11.6, 13.6; 10240 x 2560 8.7, 7.4; 16384 x 4096 12.5, 11.7
 //   fp32   16 by 8192 x 4096 11.0, 17.9; 65536 x 2560 41, 51
 inline bool few_takes(const LinearArgs& a, int x) {

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(64 * WAVES) void q4_rows(const LinearArgs a, int sp
       for (int i = 0; i < NT; ++i) c[b][i] = *reinterpret_cast<const u32x4*>(cp[i] + (int64_t)(kb + b) * 1024);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int64_t k = (int64_t)(kb + b) * 128 + (X == X_E4M3 ? i * 64 + q * 16 : q * 32 + i * (16 / ES));
+        const int64_t k = (int64_t)(kb + b) * 128 + q * 32 + i * (16 / ES);
         // token n / 4 in lanes 0, 4, 8 and 12: its outputs are the first of a lane's four; fp32: the one token in all lanes
         const bool live = X == X_F32 || (n % 4 == 0 && n / 4 < a.T);
         x[b][i] = u32x4{0, 0, 0, 0};
@@ -70,13 +70,6 @@ __global__ __launch_bounds__(64 * WAVES) void q4_rows(const LinearArgs a, int sp
 #pragma unroll
             for (int v = 0; v < 8; ++v) sum[i] = fmaf(w[v], __uint_as_float(x[b][2 * j + v / 4][v % 4]), sum[i]);
           }
-      } else if constexpr (X == X_E4M3) {
-        const i32x8 xv = __builtin_bit_cast(i32x8, __builtin_shufflevector(x[b][0], x[b][1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const i32x8 w = {(int)c[b][i][0], (int)c[b][i][1], (int)c[b][i][2], (int)c[b][i][3], 0, 0, 0, 0};
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xv, w, acc[i], 0, 4, 0, 0x7F7F7F7F, b, (int)s[i]);
-        }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -142,10 +135,7 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_rows(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32    ? launch<X_F32>(a, s)
-         : x == X_BF16 ? launch<X_BF16>(a, s)
-         : x == X_E4M3 ? launch<X_E4M3>(a, s)
-                       : launch<X_WIDE>(a, s);
+  return x == X_F32 ? launch<X_F32>(a, s) : x == X_BF16 ? launch<X_BF16>(a, s) : launch<X_E4M3>(a, s);
 }
 
 }  // namespace block

@@ -1,9 +1,9 @@
 // ssm_q4_tiles.hip -- ssm_q4_linear of include/ssm_block.h for any number of tokens, in tiles of BM rows of the weight by BT
 // tokens, 128 columns at a step, 32 x 32 products.
 //
-// The codes go into the operands as they are (e4m3 tokens: the instruction takes codes and scales) or are widened to bf16 by the
-// waves that use them (one conversion for two weights).  Many tiles are bound by the matrix cores, few by a step's own latency
-// and by how many CUs have one; so the form goes by how many tiles there are (launch_form).
+// The codes are widened to bf16 by the waves that use them (one conversion for two weights), and e4m3 tokens likewise.  Many
+// tiles are bound by the matrix cores, few by a step's own latency and by how many CUs have one; so the form goes by how many
+// tiles there are (launch_form).
 //   q4_ring   everything goes straight from memory to a ring of steps in LDS; groups of waves share a tile's columns
 //   q4_pair   bf16 and fp32 tokens, more tiles than that: tokens through two LDS buffers, the weight straight into the operands
 #include "ssm_q4_linear.h"
@@ -309,53 +309,31 @@ __global__ __launch_bounds__(64 * WM * WT * KG, 1) void q4_ring(const LinearArgs
         cc[i][v] = *reinterpret_cast<const u32x4*>(codes + i * 2048 + v * 512);
         ss[i][v] = *reinterpret_cast<const uint8_t*>(scales + i * 512 + v * 128);
       }
-    if constexpr (X == X_E4M3) {
-      u32x4 x[2][NT][2];
+    // Product n: columns 64 (n / 4) + 32 h + 8 (n % 4); fp32 tokens are read one product ahead, the others all at once.
+    constexpr int AHEAD = X == X_F32 ? 2 : 8;
+    Eight<X> x[AHEAD][NT];
+    const auto read = [&](int n) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
+      for (int t = 0; t < NT; ++t) x[n % AHEAD][t].read(rows + t * 32 * RB, n / 4 * 8 + h * 4 + n % 4, swap);
+    };
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int n = 0; n < AHEAD - 1; ++n) read(n);
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-            x[v][t][p] = *reinterpret_cast<const u32x4*>(rows + t * 32 * RB + (((4 * v + 2 * p + h) ^ swap) * 16));
+    for (int n = 0; n < 8; ++n) {
+      if (n + AHEAD - 1 < 8) read(n + AHEAD - 1);
+      bf16x8 w[NM];
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
+      for (int i = 0; i < NM; ++i) w[i] = weights8(cc[i][n / 4][n % 4], pow2(ss[i][n / 4]));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const i32x8 xv = __builtin_bit_cast(i32x8, __builtin_shufflevector(x[v][t][0], x[v][t][1], 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int t = 0; t < NT; ++t) {
+        bf16x8 p[planes<X>()];
+        x[n % AHEAD][t].parts(p);
 #pragma unroll
-          for (int i = 0; i < NM; ++i) {
-            const i32x8 w = {(int)cc[i][v][0], (int)cc[i][v][1], (int)cc[i][v][2], (int)cc[i][v][3], 0, 0, 0, 0};
-            acc[t][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, xv, acc[t][i], 4, 0, 0, (int)ss[i][v], 0, 0x7F7F7F7F);
-          }
-        }
-    } else {
-      // Product n: columns 64 (n / 4) + 32 h + 8 (n % 4); fp32 tokens are read one product ahead, the others all at once.
-      constexpr int AHEAD = X == X_F32 ? 2 : 8;
-      Eight<X> x[AHEAD][NT];
-      const auto read = [&](int n) {
+        for (int k = planes<X>() - 1; k >= 0; --k)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[n % AHEAD][t].read(rows + t * 32 * RB, n / 4 * 8 + h * 4 + n % 4, swap);
-      };
-#pragma unroll
-      for (int n = 0; n < AHEAD - 1; ++n) read(n);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        if (n + AHEAD - 1 < 8) read(n + AHEAD - 1);
-        bf16x8 w[NM];
-#pragma unroll
-        for (int i = 0; i < NM; ++i) w[i] = weights8(cc[i][n / 4][n % 4], pow2(ss[i][n / 4]));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          bf16x8 p[planes<X>()];
-          x[n % AHEAD][t].parts(p);
-#pragma unroll
-          for (int k = planes<X>() - 1; k >= 0; --k)
-#pragma unroll
-            for (int i = 0; i < NM; ++i) acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], p[k], acc[t][i], 0, 0, 0);
-        }
-        if constexpr (X == X_F32) __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < NM; ++i) acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], p[k], acc[t][i], 0, 0, 0);
       }
+      if constexpr (X == X_F32) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -457,19 +435,17 @@ hipError_t pair_form(const LinearArgs& a, hipStream_t s) {
 // a second one while others have none.  us by tile, (32, 32), (64, 32), (64, 64), (128, 64), (128, 128) rows by tokens:
 //   bf16   128 tokens by 4096 x 4096   -, 9.9, 13.6, 17.6, 30     300 by 5120 x 2560   35, 23, 18, 12.7, 20
 //          64 by 16384 x 4096   29, 18, 13.9, 17.5, 30
-//   e4m3   64 by 4096 x 8192   8.2, 10.8, 14.2, 22, 37            300 by 5120 x 2560   -, 19, 10.8, 10.4, 15
-// 96 tokens by 128 rows is the largest of those (600 by 4096 x 4096, [the next form]: bf16 24.5 [29.9], e4m3 16.4 [17.8], e4m3
-// with an fp32 output 25.9 [29.7]).  Past that:
+//   e4m3   64 by 4096 x 8192   9.6, 14.8, 19, 36, 59   128 by 4096 x 4096   11.4, 9.0, 11.7, 20, -
+//          300 by 5120 x 2560   -, 23, 17, 14.3, 21.5
+// 96 tokens by 128 rows is the largest of those (600 by 4096 x 4096, [the next form]: bf16 24.5 [29.9], e4m3 24.3 [29]).  Past that:
 //   bf16   q4_pair in the tile whose fullest CU has the least to multiply (pair_form)
-//   e4m3   up to 512 tiles of 128 x 64 with two steps in the ring, two or three of them to a CU (1000 by 4096 x 4096), up to 512
-//          of 128 x 128, then 256 x 128: 4096 by 16384 x 4096 222 us, 2480 TFLOP/s (255 in 128 x 128, 330 in q4_pair's way, 262 in
-//          256 x 256; with 512 tiles, 2048 by 4096 x 4096, 32.6 and 32.0)
-//   e4m3 with an fp32 output   the same up to 512 tiles of 128 x 64; then 128 x 192 where that is one to a CU (1500 by
-//          4096 x 4096 47 us, 54 in 128 x 128); 256 x 128 where that is (2048 by 4096 x 4096 58.6, 63) and from more than 768
-//          tiles of 128 x 128 on (4096 by 16384 x 4096 412, 453; 3000 by 4096 x 4096, 768 tiles, 90 either way); else 128 x 128
+//   e4m3   up to 512 tiles of 128 x 64 with two steps in the ring, two or three of them to a CU (1000 by 4096 x 4096 33.5, 35 in
+//          128 x 128); then 128 x 192 where that is one to a CU (1500 by 4096 x 4096 46.6, 53 in 128 x 128); 256 x 128 where that
+//          is (2048 by 4096 x 4096 58.6, 61) and from more than 768 tiles of 128 x 128 on (4096 by 16384 x 4096 404, 450; 3000 by
+//          4096 x 4096, 768 tiles, 89, 88); else 128 x 128
 // Up to 32 and up to 64 tokens a tile has no more of them, however many rows there are: reading the weight bounds the call.
-// Without and with that, us: 32 bf16 tokens by 65536 x 2560 37, 18.5 (5.1 TB/s), by 32768 x 4096 19.7, 14.8; e4m3 17.7, 16.8 and
-// 14.0, 13.4.  64 by 65536 x 2560 bf16 41, 31, e4m3 with an fp32 output 42, 29 (with a bf16 one 21 either way).
+// Without and with that, us: 32 bf16 tokens by 65536 x 2560 37, 18.5 (5.1 TB/s), by 32768 x 4096 19.7, 14.8; e4m3 29, 18.3 and
+// 21, 15.5.  64 by 65536 x 2560 bf16 41, 31, e4m3 41, 27.
 // fp32 tokens by 64 rows where that is one to a CU: 32 by 16384 x 4096 28 us, 40 by 128 rows.
 template <int X>
 hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
@@ -485,16 +461,14 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
     if (a.T <= 32) return once(128, 32) ? ring<X, 128, 32, 4, 1, 2, 3>(a, s) : ring<X, 128, 32, 4, 1, 2, 2>(a, s);
     if (once(64, 64)) return ring<X, 64, 64, 2, 2, E ? 4 : 2, 3>(a, s);
     if (once(128, 64)) return ring<X, 128, 64, 4, 1, 2, E ? 4 : 2>(a, s);
-    if (once(128, 96)) return ring<X, 128, 96, 4, 1, 2, X == X_E4M3 ? 3 : 2>(a, s);
+    if (once(128, 96)) return ring<X, 128, 96, 4, 1, 2, 2>(a, s);
     if constexpr (E)
       if (tiles_of(a, 128, 64) <= 512) return ring<X, 128, 64, 4, 1, 2, 2>(a, s);
-    if constexpr (X != X_E4M3)
-      if (a.T <= 64) return ring<X, 128, 64, 4, 1, E ? 2 : 1, E ? 2 : 3>(a, s);
+    if (a.T <= 64) return ring<X, 128, 64, 4, 1, E ? 2 : 1, E ? 2 : 3>(a, s);
     if constexpr (X == X_BF16) return pair_form<X>(a, s);
-    if constexpr (X == X_WIDE)
-      if (once(128, 192)) return ring<X, 128, 192, 4, 2, 1, 2>(a, s);
     if constexpr (E) {
-      if (tiles_of(a, 128, 128) > (X == X_E4M3 ? 512 : 768) || (X == X_WIDE && once(256, 128))) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
+      if (once(128, 192)) return ring<X, 128, 192, 4, 2, 1, 2>(a, s);
+      if (tiles_of(a, 128, 128) > 768 || once(256, 128)) return ring<X, 256, 128, 4, 2, 1, 2>(a, s);
       return ring<X, 128, 128, 4, 2, 1, 2>(a, s);
     }
   }
@@ -504,10 +478,7 @@ hipError_t launch_form(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_tiles(const LinearArgs& a, int x, hipStream_t s) {
-  return x == X_F32    ? launch_form<X_F32>(a, s)
-         : x == X_BF16 ? launch_form<X_BF16>(a, s)
-         : x == X_E4M3 ? launch_form<X_E4M3>(a, s)
-                       : launch_form<X_WIDE>(a, s);
+  return x == X_F32 ? launch_form<X_F32>(a, s) : x == X_BF16 ? launch_form<X_BF16>(a, s) : launch_form<X_E4M3>(a, s);
 }
 
 }  // namespace block
@@ -545,10 +516,9 @@ extern "C" int ssm_q4_linear(int64_t tokens, int32_t x_dtype, int32_t out_dtype,
   a.mt = (M + 15) / 16;
   a.out_bf16 = out_dtype == SSM_BF16;
   a.wide = aligned(out->data, 16) && out->stride * os % 16 == 0;
-  const int kind = x_dtype == SSM_E4M3 && out_dtype == SSM_F32 ? (int)X_WIDE : x_dtype;
   const hipStream_t s = ready(stream);
-  const hipError_t e = rows_takes(a, kind)  ? launch_q4_rows(a, kind, s)
-                       : few_takes(a, kind) ? launch_q4_few(a, kind, s)
-                                            : launch_q4_tiles(a, kind, s);
+  const hipError_t e = rows_takes(a, x_dtype)  ? launch_q4_rows(a, x_dtype, s)
+                       : few_takes(a, x_dtype) ? launch_q4_few(a, x_dtype, s)
+                                               : launch_q4_tiles(a, x_dtype, s);
   return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
