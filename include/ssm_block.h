@@ -14,11 +14,11 @@
  * Formulas.
  *   norm       h = x + residual, summed in fp32 and rounded once to the residual's dtype (h = x where
  *              there is no residual); r = 1 / sqrt(mean(h^2) + eps); y = (h * weight) * r, fp32, rounded
- *              once to the output's dtype.  (h^2 is fp32: magnitudes stay below 2^63.)
+ *              once to the output's dtype.  (The sum of h^2 is fp32: magnitudes stay below 2^56.)
  *   8-bit rows one fp32 scale per row: amax = max |y|, s = amax * (1 / 448); code = e4m3, nearest even, of
  *              (h * weight) * (448 / max |h * weight|), which is y * (448 / amax) with fewer roundings (in fp64,
  *              rounded to fp32 before; rows of more than 8192 values in fp32); value = code * s.  Rows with amax < 2^-100
- *              get s = 0 and codes 0.
+ *              get s = 0 and codes 0.  A row with a NaN or an infinity gets s = NaN: all of it reads back as NaN.
  *   4-bit      w[m, k] = c * 2^(e - 127): c one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (e2m1:
  *              sign, two bits of exponent, one of mantissa, in code order), e a byte for each 32 values of
  *              a row (k / 32).  Quantising: amax = max |w| of the group, rounded to three significant bits
@@ -48,8 +48,10 @@
  *
  * Conventions (ownership, ordering, errors before any HIP call, no allocation, no mutable global state,
  * no host synchronisation, the current device) as in ssm.h.  Outputs may not overlap inputs or each
- * other, except where said.  0 tokens: a call that does nothing.  Non-finite inputs are outside the
- * contract; a row's values stay in that row.
+ * other, except where said.  0 tokens: a call that does nothing.  Non-finite inputs stay in their row
+ * (ssm_rms_norm, a token's row of ssm_q4_linear) and are not lost there: the norm in the io dtype and the
+ * products give what the formulas give (an infinity among fp32 tokens may give NaN), the norm in 8 bits
+ * what is said above.
  */
 #ifndef SSM_BLOCK_H
 #define SSM_BLOCK_H

@@ -56,10 +56,11 @@ __device__ __forceinline__ void store8(char* p, const float (&y)[8]) {
   }
 }
 
+// Magnitudes of at most 448 and a few roundings of that, far from the 464 where the next code would begin: nothing to clamp, which
+// would make a number of a NaN.
 __device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
-  const auto in = [](float x) { return fminf(fmaxf(x, -448.0f), 448.0f); };
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(in(a), in(b), 0, false);
-  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(in(c), in(d), w, true);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 // 448 / x in fp64, x > 0: the reciprocal instruction and two steps of Newton's, each of which squares what is missing.
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
     Max m = 0;
     if constexpr (Q8) {
       const float amax = (float)(mx * (Max)r);
-      const bool live = amax >= 0x1p-100f;
+      const bool live = !(amax < 0x1p-100f);  // a row with a NaN or an infinity, whose r is NaN or 0, has a scale of NaN
       if (tid == 0) a.scale[row] = live ? amax * (1.0f / 448.0f) : 0.0f;
       // A code is h * weight over the row's largest, r over r: of r its power of two is enough, which rounds nothing (fp64: none).
       if constexpr (sizeof(Max) == 8) {
