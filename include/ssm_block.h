@@ -25,6 +25,7 @@
  *              (half away from zero, bit pattern + 2^21), falls in 2^n .. 2^(n+1); e = n - 2 + 127, at most
  *              252; code = w * 2^(127 - e) to nearest, ties to the even code, at most 6 in magnitude.
  *              Groups with amax < 2^-100 get codes 0 and e = 127; what rounds to zero keeps its sign.
+ *              Groups with a NaN or an infinity get codes 0 and e = 255, for which every value is NaN.
  *              Every value is exact in bf16 for e in [2, 252]; other bytes are outside the contract.
  *   linear     out[t, m] = x_scale[t] * sum_k x[t, k] w[m, k] (no x_scale for bf16 and fp32 tokens), sums
  *              in fp32.  Products are exact: bf16 tokens (and e4m3 tokens widened to it) multiply the
@@ -51,7 +52,7 @@
  * other, except where said.  0 tokens: a call that does nothing.  Non-finite inputs stay in their row
  * (ssm_rms_norm, a token's row of ssm_q4_linear) and are not lost there: the norm in the io dtype and the
  * products give what the formulas give (an infinity among fp32 tokens may give NaN), the norm in 8 bits
- * what is said above.
+ * and a weight in 4 bits what is said above.
  */
 #ifndef SSM_BLOCK_H
 #define SSM_BLOCK_H

@@ -204,7 +204,7 @@ class Q4Weight(NamedTuple):
     @classmethod
     def pack(cls, codes, scales):
         """From codes [M, K] uint8 (0 .. 15: sign, two bits of exponent, one of mantissa) and scales [M, ceil(K / 32)]
-        uint8 (127 + the exponent of two, 2 .. 252), in rows, on any device."""
+        uint8 (127 + the exponent of two, 2 .. 252; 255: the group is NaN), in rows, on any device."""
         if codes.dim() != 2 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise ValueError("codes must be [out_features, in_features] uint8, and scales uint8")
         (M, K), dev = codes.shape, codes.device

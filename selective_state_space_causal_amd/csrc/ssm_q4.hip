@@ -39,11 +39,14 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
+// The larger of two values, NaN where one is (fmaxf drops it).
+__device__ __forceinline__ float largest(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // The largest of four neighbouring lanes' values, in all of them.
 __device__ __forceinline__ float quad_max(float v) {
   // lanes 1 0 3 2, then 2 3 0 1 of each four
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true)));
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true)));
+  v = largest(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true)));
+  return largest(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true)));
 }
 
 template <typename IO>
@@ -76,11 +79,11 @@ __global__ __launch_bounds__(64 * WAVES) void quantize_tiles(const Q4Args a) {
           y[i] = __uint_as_float(i % 2 ? v[r][0][i / 2] & 0xFFFF0000u : v[r][0][i / 2] << 16);
         else
           y[i] = __uint_as_float(v[r][i / 4][i % 4]);
-        amax = fmaxf(amax, fabsf(y[i]));
+        amax = largest(amax, fabsf(y[i]));
       }
       amax = quad_max(amax);
-      const bool live = amax >= 0x1p-100f;
-      const unsigned e = live ? min(((__float_as_uint(amax) + 0x200000u) >> 23) - 2, 252u) : 127u;
+      const bool finite = amax < __builtin_inff(), live = finite && amax >= 0x1p-100f;
+      const unsigned e = live ? min(((__float_as_uint(amax) + 0x200000u) >> 23) - 2, 252u) : finite ? 127u : 255u;
       unsigned c = 0;
       c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[0], y[1], pow2(e), 0);
       c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], pow2(e), 1);

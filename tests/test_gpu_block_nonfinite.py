@@ -1,6 +1,6 @@
-"""The 8-bit norm of rows that hold a NaN or an infinity: they read back as NaN, as by the definition (the row's largest magnitude,
-and with it its scale, is NaN), and do not turn into plausible numbers on the way through a 4-bit product; other rows are as
-without them."""
+"""NaN and infinities in the operators that store 8 or 4 bits.  Rows of the 8-bit norm that hold one read back as NaN, as by the
+definition (the row's largest magnitude, and with it its scale, is NaN), and do not turn into plausible numbers on the way through a
+4-bit product; other rows are as without them.  Likewise the groups of a weight in 4 bits."""
 import pytest
 import torch
 
@@ -65,3 +65,29 @@ def test_a_weight_that_is_nan_stays_in_its_column(D):
     got = values(*ssm.rms_norm(x, w, out_dtype=E4M3))
     keep = torch.arange(D, device=DEV) != 7
     assert got[:, 7].isnan().all() and torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 16), (5, 48), (40, 1040)])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_a_group_of_a_weight_that_is_not_finite_reads_back_as_nan(M, K, io, bad):
+    """4 bits hold no NaN or infinity: the group's scale does, and a product with its row is NaN."""
+    w = rnd(1, M, K).to(io).to(DEV)
+    want, wb = ssm.q4_quantize(w), w.clone()
+    rows = sorted({0, M // 2, M - 1})
+    places = [(5 + 37 * i) % K for i in rows]
+    for row, place in zip(rows, places):
+        wb[row, place] = bad
+    q = ssm.q4_quantize(wb)
+    gone = torch.zeros(M, K, dtype=torch.bool, device=DEV)
+    for row, place in zip(rows, places):
+        gone[row, place // 32 * 32:place // 32 * 32 + 32] = True
+    for dt in (torch.bfloat16, torch.float32):
+        a, b = ssm.q4_dequantize(q, dtype=dt), ssm.q4_dequantize(want, dtype=dt)
+        assert a[gone].isnan().all() and torch.equal(a[~gone], b[~gone])
+    keep = [m for m in range(M) if m not in rows]
+    for T in (1, 3, 7, 20, 40, 130):
+        x = rnd(T, T, K).to(DEV)
+        for xt, xs in ((x, None), (x.bfloat16(), None), (x.to(E4M3), torch.ones(T, device=DEV))):
+            y, y0 = (ssm.q4_linear(xt, v, x_scale=xs) for v in (q, want))
+            assert y[:, rows].isnan().all() and torch.equal(y[:, keep], y0[:, keep])
