@@ -35,8 +35,13 @@ projections are in the mixer's own channel-major layouts.
 
 With a norm the layer takes the stack's residual stream: hidden (the last block's output) is added to it, and in_proj
 reads its norm, in 8 bits for a decoded token where asked (rms_norm).
+
+Given a stream, a layer takes the memory of all that it makes from that stream's pool: a block of the current stream's may
+still be in use by work queued there, which nothing orders before the layer's.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -67,8 +72,21 @@ def _used(weights: dict, stacked: bool) -> tuple:
     return ("in_xz", "out") if stacked else ("in_x", "in_z", "out")
 
 
+def _on(stream):
+    """With `stream` (None: as it is) current, for what is allocated."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _returned(tensors, stream, device):
+    """Tensors of `stream`'s pool, for use on the current stream: not handed out again before that is done with them."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(device))
+    return tensors
+
+
 def alloc_buffers(hidden, weights: dict, d_state: int, out_dtype=None, normed: bool = False) -> dict:
-    """Every tensor the layer writes, on hidden's device."""
+    """Every tensor the layer writes, on hidden's device, from the current stream's memory."""
     B, L, DM = hidden.shape
     D = weights["in_x"].shape[0]
     R = weights["x_dt"].shape[0]
@@ -141,17 +159,19 @@ def mixer_prefill(hidden, weights: dict, params: dict, proj: "_lib.Projector", *
     """Returns (out [B, L, d_model] partial in out_dtype (default: hidden's dtype), h [B, D, N],
     conv [B, D, 3]).  norm (fp32 [d_model]): in_proj reads the norm of hidden, or with residual [B, L, d_model] (hidden's
     dtype or fp32, contiguous, updated in place) of its sum with hidden."""
-    bufs = alloc_buffers(hidden, weights, params["A"].shape[1], out_dtype, norm is not None)
-    for _, call in stages(hidden, weights, params, proj, bufs, stream, norm, residual, eps):
-        call()
-    return bufs["out"], bufs["h"], bufs["c"]
+    with _on(stream):
+        bufs = alloc_buffers(hidden, weights, params["A"].shape[1], out_dtype, norm is not None)
+        for _, call in stages(hidden, weights, params, proj, bufs, stream, norm, residual, eps):
+            call()
+    return _returned((bufs["out"], bufs["h"], bufs["c"]), stream, hidden.device)
 
 
 # ---- decode: one token per batch row through the layer, from the cache ----
 
 def alloc_decode_buffers(hidden_t, weights: dict, d_state: int, fused: bool, out_dtype=None, normed: bool = False,
                          tokens_8bit: bool = False) -> dict:
-    """Every tensor a decode step writes besides the cache and the residual stream, on hidden_t's device."""
+    """Every tensor a decode step writes besides the cache and the residual stream, on hidden_t's device, from the current
+    stream's memory."""
     B, DM = hidden_t.shape
     D, R = weights["in_x"].shape[0], weights["x_dt"].shape[0]
     dev, dt = hidden_t.device, hidden_t.dtype
@@ -243,10 +263,14 @@ def mixer_decode_step(hidden_t, weights: dict, params: dict, proj: "_lib.Project
     tokens_8bit: the norm in 8 bits, for an in_proj in 4 bits (bufs are then made with normed and tokens_8bit)."""
     if tokens_8bit and norm is None:
         raise ValueError("tokens_8bit goes with norm")
-    if bufs is None:
-        bufs = alloc_decode_buffers(hidden_t, weights, params["A"].shape[1], fused, out_dtype, norm is not None, tokens_8bit)
-    elif norm is not None and ("normed" not in bufs or ("scale" in bufs) != tokens_8bit):
+    if bufs is not None and norm is not None and ("normed" not in bufs or ("scale" in bufs) != tokens_8bit):
         raise ValueError(f"bufs were not made with normed=True, tokens_8bit={tokens_8bit}")
-    for _, call in decode_stages(hidden_t, weights, params, proj, h, conv, bufs, fused, stream, norm, residual, eps):
-        call()
+    made = bufs is None
+    with _on(stream):
+        if made:
+            bufs = alloc_decode_buffers(hidden_t, weights, params["A"].shape[1], fused, out_dtype, norm is not None, tokens_8bit)
+        for _, call in decode_stages(hidden_t, weights, params, proj, h, conv, bufs, fused, stream, norm, residual, eps):
+            call()
+    if made:
+        _returned((bufs["out"],), stream, hidden_t.device)
     return bufs["out"].view(hidden_t.shape[0], -1)
