@@ -22,6 +22,7 @@ from ._lib import SSM_BF16, SSM_F32, SsmError, stream_handle
 KV_IO, KV_I8, KV_E4M3 = 0, 1, 2
 MIN_PAGE, MAX_PAGE = 16, 1024
 MAX_HEAD_DIM = 256
+MAX_HEADS, MAX_BATCH = 1024, 65535
 
 _IO = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
 _CODES = {torch.int8: KV_I8, torch.float8_e4m3fn: KV_E4M3}

@@ -343,6 +343,18 @@ def block_input(hidden, norm=None, residual=None, *, eps: float = 1e-5, tokens_8
     return y if tokens_8bit else (y, None)
 
 
+def check_weight(w, name, shape, dtype, device):
+    """Refuses a projection's weight (a tensor or a Q4Weight) that is not [out, in] `shape`, of `dtype` and on `device`."""
+    if tuple(w.shape) != tuple(shape):
+        raise ValueError(f"{name} weight is {tuple(w.shape)}, expected {tuple(shape)}")
+    if isinstance(w, Q4Weight):
+        _q4(w, device)
+    elif w.dtype != dtype:
+        raise TypeError(f"{name} weight is {w.dtype}, expected {dtype}")
+    elif w.device != device:
+        raise ValueError(f"{name} weight is on {w.device}, expected {device}")
+
+
 def project(x, w, x_scale=None):
     """x [T, K] times the transpose of w [M, K]: a Q4Weight (q4_linear), or a tensor of x's dtype (a plain library GEMM)."""
     if isinstance(w, Q4Weight):

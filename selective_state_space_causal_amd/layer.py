@@ -34,7 +34,8 @@ token is multiplied with them as they are (q4_linear); a prompt reads them back 
 projections are in the mixer's own channel-major layouts.
 
 With a norm the layer takes the stack's residual stream: hidden (the last block's output) is added to it, and in_proj
-reads its norm, in 8 bits for a decoded token where asked (rms_norm).
+reads its norm, in 8 bits for a decoded token where asked (rms_norm).  A call that is refused for its arguments has left
+the stream as it was; only memory that runs out or a launch that fails can end one after the norm.
 
 Given a stream, a layer takes the memory of all that it makes from that stream's pool: a block of the current stream's may
 still be in use by work queued there, which nothing orders before the layer's.
@@ -46,7 +47,7 @@ import contextlib
 import torch
 
 from . import _lib
-from .block import E4M3, Q4Weight, block_input, q4_dequantize, q4_linear
+from .block import E4M3, Q4Weight, _check_features, _q4_shapes, block_input, q4_dequantize, q4_linear
 
 CONV_W = 4
 
@@ -83,6 +84,97 @@ def _returned(tensors, stream, device):
         for t in tensors:
             t.record_stream(torch.cuda.current_stream(device))
     return tensors
+
+
+# What the stages after the norm would refuse is refused before hidden goes into the residual stream, so that a call that is put right
+# and made again does not add it twice: what is missing, or of another size, type, device or alignment than they take.  (Tensors
+# that share memory, and a seqlen of 2^24 or more, they still refuse themselves.  11 us of the host for a decode step.)
+
+def _look(what, device):
+    """what: (name, tensor, shape, dtype, bytes its address is a multiple of) of each."""
+    index = device.index
+    for name, t, shape, dtype, align in what:
+        if t is not None and t.shape == shape and t.dtype == dtype and t.get_device() == index and t.is_contiguous() and not t.data_ptr() % align:
+            continue
+        _lib._check(t, name, shape, dtype, device)
+        raise ValueError(f"{name} must be aligned to {align} bytes")
+
+
+def _weights(weights: dict, shapes: dict, dtype):
+    """The weights of those names as _look takes them."""
+    for k, (shape, align) in shapes.items():
+        w = weights[k]
+        if not isinstance(w, Q4Weight):
+            yield k, w, shape, dtype, align
+            continue
+        M, K = shape
+        if (w.out_features, w.in_features) != shape:
+            raise ValueError(f"{k} weight is {tuple(w.shape)}, expected {shape}")
+        _check_features(M, K)
+        codes, scales = _q4_shapes(M, K)
+        yield k + " codes", w.codes, codes, torch.uint8, 16
+        yield k + " scales", w.scales, scales, torch.uint8, 16
+
+
+def _parameters(params: dict, D: int, N: int):
+    f32 = torch.float32
+    if not 1 <= N <= _lib.MAX_STATE:
+        raise ValueError(f"d_state is {N}, up to {_lib.MAX_STATE}")
+    p = [("A", params["A"], (D, N), f32, 16), ("Dskip", params["Dskip"], (D,), f32, 4), ("dt_bias", params["dt_bias"], (D,), f32, 4),
+         ("conv_w", params["conv_w"], (D, CONV_W), f32, 16)]
+    bias = params.get("conv_b")
+    return p if bias is None else p + [("conv_b", bias, (D,), f32, 4)]
+
+
+def _projector(proj):
+    if proj is None or proj.handle is None:
+        raise ValueError("a projector, not closed, is required")
+
+
+def _check_prefill(hidden, weights: dict, params: dict, proj, b: dict):
+    (B, L, DM), D, R, N = hidden.shape, weights["in_x"].shape[0], weights["x_dt"].shape[0], params["A"].shape[1]
+    dt, f32, stacked, conv_xproj = hidden.dtype, torch.float32, "xz" in b, "u" not in b
+    _projector(proj)
+    shapes = dict(in_xz=((2 * D, DM), 16)) if stacked else dict(in_x=((D, DM), 16), in_z=((D, DM), 16))
+    shapes.update(dict(x_all=((R + 2 * N, D), 16)) if conv_xproj else dict(x_dt=((R, D), 16), x_B=((N, D), 16), x_C=((N, D), 16)),
+                  dt=((D, R), 16), out=((DM, D), 16))
+    _lib._io_code(b["out"].dtype)
+    rows = ("dt", "y") if conv_xproj else ("u", "dt", "y")
+    _look((*_weights(weights, shapes, dt), *_parameters(params, D, N),
+           *((("xz", b["xz"], (1, 2 * D, L), dt, 16),) if stacked else ()),
+           *((k, b[k], (B, D, L), dt, 16) for k in ("x", "z", *rows)),
+           *((k, b[k], (B, L, n), dt, 16) for k, n in (("lowrank", R), ("Bm", N), ("Cm", N))),
+           ("h", b["h"], (B, D, N), f32, 16), ("c", b["c"], (B, D, CONV_W - 1), f32, 16), ("out", b["out"], (B, L, DM), b["out"].dtype, 16)),
+          hidden.device)
+
+
+def _check_decode(hidden_t, weights: dict, params: dict, proj, h, conv, b: dict, fused: bool):
+    (B, DM), D, R, N = hidden_t.shape, weights["in_x"].shape[0], weights["x_dt"].shape[0], params["A"].shape[1]
+    dt, dev, f32, stacked = hidden_t.dtype, hidden_t.device, torch.float32, "xz" in b
+    es = dt.itemsize  # the fused step takes its weights and rows at any address
+    shapes = dict(in_xz=((2 * D, DM), 16)) if stacked else dict(in_x=((D, DM), 16), in_z=((D, DM), 16))
+    shapes["out"] = ((DM, D), 16)
+    if not fused or not all(isinstance(weights[k], Q4Weight) for k in shapes):
+        _projector(proj)
+    if fused:
+        shapes.update(x_all=((R + 2 * N, D), es), dt=((D, R), es))
+    else:
+        shapes.update(dict(x_all=((R + 2 * N, D), 16)) if "xo" in b else dict(x_dt=((R, D), 16), x_B=((N, D), 16), x_C=((N, D), 16)),
+                      dt=((D, R), 16))
+    _lib._io_code(b["out"].dtype)
+    _look((*_weights(weights, shapes, dt), *_parameters(params, D, N), ("h", h, (B, D, N), f32, 16), ("conv", conv, (B, D, CONV_W - 1), f32, 4),
+           *((("xz", b["xz"], (1, 2 * D, 1), dt, 16),) if stacked else ()),
+           *((k, b[k], (B, D, 1), dt, es if stacked else 16) for k in ("x", "z")), ("y", b["y"], (B, D, 1), dt, 16),
+           ("out", b["out"], (B, 1, DM), b["out"].dtype, 16)), dev)
+    if fused:
+        need, ws = _lib.decode_fused_workspace_bytes(B, D, R, N, dt), b["ws"]
+        if need == 0:
+            raise ValueError(f"the fused step takes no d_state of {N} with a rank of {R}")
+        if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+            raise ValueError(f"ws must be a contiguous tensor of {need} bytes on {dev}")
+        return
+    _look((*((("xo", b["xo"], (1, 1, R + 2 * N), dt, 16),) if "xo" in b else ()), ("u", b["u"], (B, D, 1), dt, 16), ("dt", b["dt"], (B, D, 1), dt, 16),
+           *((k, b[k], (B, 1, n), dt, es if "xo" in b and k != "lowrank" else 16) for k, n in (("lowrank", R), ("Bt", N), ("Ct", N)))), dev)
 
 
 def alloc_buffers(hidden, weights: dict, d_state: int, out_dtype=None, normed: bool = False) -> dict:
@@ -128,8 +220,13 @@ def stages(hidden, weights: dict, params: dict, proj: "_lib.Projector", bufs: di
         if residual is not None and residual.shape != hidden.shape:
             raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {tuple(hidden.shape)}")
         x, hidden, DM = hidden, b["normed"], hidden.shape[2]
-        pre.append(("norm", lambda: block_input(x.view(-1, DM), norm, None if residual is None else residual.view(-1, DM),
-                                                eps=eps, out=b["normed"].view(-1, DM), stream=stream)))
+
+        def norm_stage():
+            tokens, rows = x.view(-1, DM), None if residual is None else residual.view(-1, DM)
+            if residual is not None:
+                _check_prefill(x, weights, params, proj, b)
+            block_input(tokens, norm, rows, eps=eps, out=b["normed"].view(-1, DM), stream=stream)
+        pre.append(("norm", norm_stage))
     elif residual is not None:
         raise ValueError("residual goes with norm")
     if "xz" in b:
@@ -226,8 +323,11 @@ def decode_stages(hidden_t, weights: dict, params: dict, proj: "_lib.Projector",
     R = weights["x_dt"].shape[0]
     st = []
     if norm is not None:
-        st.append(("norm", lambda: block_input(hidden_t, norm, residual, eps=eps, tokens_8bit=scale is not None, out=b["normed"],
-                                               scale=scale, stream=stream)))
+        def norm_stage():
+            if residual is not None:
+                _check_decode(hidden_t, weights, params, proj, h, conv, b, fused)
+            block_input(hidden_t, norm, residual, eps=eps, tokens_8bit=scale is not None, out=b["normed"], scale=scale, stream=stream)
+        st.append(("norm", norm_stage))
     elif residual is not None:
         raise ValueError("residual goes with norm")
     if "xz" in b:
