@@ -78,7 +78,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, NW = TPR < 64 ? 1 : TPR / 64;
   constexpr bool AHEAD = P <= 2;  // more pieces leave no registers for the next row
   // h * weight: of 8-bit rows in fp64, so that a code is that of the definition (of 134 million none was another, 58 in fp32), where
-  // the registers allow (32768 values: 138 us for 1024 rows so, 84 in fp32).
+  // the registers allow (32768 values: 138 us for 1024 rows so, 84 in fp32).  It costs what it costs, us in fp64 and in fp32:
+  // 32768 rows without a residual of 1024 39.3, 30.5; of 2048 49.7, 40.9; of 2560 102, 81; of 4096 112, 90; with one of 1024
+  // 47.5, 45.0; of 4096 165.8, 164.8; 16384 of 8192 178, 165; one row of 4096 2.7, 2.5.
   using Max = typename std::conditional<Q8 && P == 1, double, float>::type;
   __shared__ float red[2][NW];
   __shared__ Max red_max[2][Q8 ? NW : 1];
@@ -204,9 +206,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_rows(const NormArgs
 template <typename IO, int RES, bool Q8, int TPR, int P>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, TPB = TPR < 256 ? 256 : TPR;
-  // 2048 threads to a CU; of 512 for many rows half as many, whose rows are fewer places of memory at once (32768 rows of 4096, bf16
-  // with residual to e4m3 162 us, 180 with 2048; to bf16 193, 209; 1000 rows 6.6, 6.4; rows of 2048 without residual 46, 39).  Of 256 to 8 bits the registers leave room for
-  // 1536 (32768 rows of 1024 48 us, 56 with 2048, of which some would wait for the others' end)
+  // 2048 threads to a CU; of 512 for many rows half as many, whose rows are fewer places of memory at once; of 256 to 8 bits the
+  // registers leave room for 1536, and some of 2048 would wait for the others' end.  Many begin at 2048 rows; us with 2048
+  // threads and with fewer, bf16, by rows:
+  //   4096 with a residual to e4m3   1000 7.7, 7.3   2000 12.3, 11.5   2500 14.0, 13.6   32768 170, 165
+  //   4096 with a residual to bf16   1000 6.5, 6.8   2000 10.7, 10.9   2500 14.8, 14.2   32768 209, 190
+  //   4096 without one to bf16       2048 7.2, 7.2   3000 8.9, 9.4     8192 25.4, 24.6   32768 99, 90
+  //   1024 with a residual to e4m3   1000 3.8, 3.8   2048 5.3, 5.3     4096 9.1, 7.9     32768 57, 48
   constexpr int MANY = TPB == 512 ? 1024 : TPB == 256 && Q8 ? 1536 : 2048;
   const int64_t want = (a.T + RPB - 1) / RPB, most = 256 * ((a.T >= 2048 ? MANY : 2048) / TPB);
   rms_rows<IO, RES, Q8, TPR, P><<<dim3((unsigned)(want < most ? want : most)), dim3(TPB), 0, s>>>(a);

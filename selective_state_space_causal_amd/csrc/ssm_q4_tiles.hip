@@ -411,6 +411,7 @@ hipError_t ring(const LinearArgs& a, hipStream_t s) {
 //     4096 by 16384 x 4096   399 (1378 TFLOP/s), 422, 426, 442, 448; with four waves of 64 x 64 in (128, 128) 460
 //     1000 by 4096 x 4096   51, 42, 32.9, 39, 32.7     1200   51, 42.4, 47, 42.0, 42.9     1600   52, 66, 51, 57, 54
 //     2048 by 4096 x 4096   57, 69, 58, 63, 60         2200   84, 70, 76, 64.6, 71         3000   89, 81, 84, 87, 87
+//     5000 by 2560 x 5120   116, 139, 129, 125, 124: it takes the last, where the first is faster   8192   184, 189, 181, 191, 192
 //   fp32   (256, 32), (128, 32)
 //     4096 by 4096 x 4096   352, 405; in (128, 64) 498   1000   91, 110   600   75, 73   300 by 5120 x 2560   29, 33
 //     300 by 2560 x 2560   28, 23                        64 by 65536 x 2560   62, 75
