@@ -14,8 +14,8 @@ sequence the layouts coincide, and a caller that keeps a Projector can run its t
 instead.)
 
 With a norm the block takes the stack's residual stream: hidden (the last block's output) is added to it, and the
-block runs on its norm, in 8 bits for weights in 4 bits where asked (rms_norm).  A call that is refused for its arguments
-has left the stream as it was.
+block runs on its norm, in 8 bits for weights in 4 bits where asked (rms_norm).  A call that is refused for what is missing, or of
+another size, type or device, has left the stream as it was.
 
 A mixer layer's hidden is [B, L, d_model]; hidden.view(-1, d_model) with row ends at multiples of L is the packed
 form of the same tokens.

@@ -34,8 +34,8 @@ token is multiplied with them as they are (q4_linear); a prompt reads them back 
 projections are in the mixer's own channel-major layouts.
 
 With a norm the layer takes the stack's residual stream: hidden (the last block's output) is added to it, and in_proj
-reads its norm, in 8 bits for a decoded token where asked (rms_norm).  A call that is refused for its arguments has left
-the stream as it was; only memory that runs out or a launch that fails can end one after the norm.
+reads its norm, in 8 bits for a decoded token where asked (rms_norm).  A call that is refused for what is missing, or of another
+size, type, device or alignment, has left the stream as it was.
 
 Given a stream, a layer takes the memory of all that it makes from that stream's pool: a block of the current stream's may
 still be in use by work queued there, which nothing orders before the layer's.
@@ -88,7 +88,8 @@ def _returned(tensors, stream, device):
 
 # What the stages after the norm would refuse is refused before hidden goes into the residual stream, so that a call that is put right
 # and made again does not add it twice: what is missing, or of another size, type, device or alignment than they take.  (Tensors
-# that share memory, and a seqlen of 2^24 or more, they still refuse themselves.  11 us of the host for a decode step.)
+# that share memory, and a seqlen of 2^24 or more, they refuse themselves, and memory may run out in one.  11 us of the host for a
+# decode step.)
 
 def _look(what, device):
     """what: (name, tensor, shape, dtype, bytes its address is a multiple of) of each."""
