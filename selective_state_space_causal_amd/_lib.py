@@ -168,6 +168,25 @@ def stream_handle(stream=None, device=None) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _made(make, stream, device, returned=True):
+    """make()'s tensor, from the memory pool of the stream that writes it: a block of the current stream's pool may still
+    be in use by work queued there, which nothing orders before `stream`'s.  A returned one is used on the
+    current stream, so its memory is not handed out again before that is done with it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _made(lambda: torch.empty(shape, dtype=dtype, device=device), stream, device, returned)
+
+
 def workspace_bytes(batch, seqlen, d_inner, d_state, io_dtype=torch.bfloat16, chunk_hint=0) -> int:
     d = Dims(batch, seqlen, d_inner, d_state, CONV_W, _io_code(io_dtype), chunk_hint)
     return int(load().ssm_prefill_workspace_bytes(ctypes.byref(d)))
@@ -188,16 +207,16 @@ def prefill(x, dt, z, Bm, Cm, params: dict, h0=None, conv0=None, *, chunk_hint: 
     _check(h0, "h0", (Bsz, D, N), torch.float32, dev, optional=True)
     _check(conv0, "conv0", (Bsz, D, CONV_W - 1), torch.float32, dev, optional=True)
     _check_params(params, D, N, dev)
-    y = torch.empty_like(x) if y is None else y
-    h_out = torch.empty(Bsz, D, N, dtype=torch.float32, device=dev) if h_out is None else h_out
-    conv_out = torch.empty(Bsz, D, CONV_W - 1, dtype=torch.float32, device=dev) if conv_out is None else conv_out
+    y = _empty((Bsz, D, L), io, dev, stream) if y is None else y
+    h_out = _empty((Bsz, D, N), torch.float32, dev, stream) if h_out is None else h_out
+    conv_out = _empty((Bsz, D, CONV_W - 1), torch.float32, dev, stream) if conv_out is None else conv_out
     _check(y, "y", (Bsz, D, L), io, dev)   # given outputs are written in full: their sizes must match
     _check(h_out, "h_out", (Bsz, D, N), torch.float32, dev)
     _check(conv_out, "conv_out", (Bsz, D, CONV_W - 1), torch.float32, dev)
     d = Dims(Bsz, L, D, N, CONV_W, _io_code(io), chunk_hint)
     need = int(lib.ssm_prefill_workspace_bytes(ctypes.byref(d)))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty((need,), torch.uint8, dev, stream, returned=False)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     p = make_params(params)
     st = lib.ssm_prefill(ctypes.byref(d), ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(z), _ptr(Bm), _ptr(Cm),
@@ -222,7 +241,7 @@ def decode_step(x_t, dt_t, z_t, B_t, C_t, params: dict, h, conv, *, y_t=None, st
     _check(h, "h", (Bsz, D, N), torch.float32, dev)
     _check(conv, "conv", (Bsz, D, CONV_W - 1), torch.float32, dev)
     _check_params(params, D, N, dev)
-    y_t = torch.empty_like(x_t) if y_t is None else y_t
+    y_t = _empty((Bsz, D), io, dev, stream) if y_t is None else y_t
     _check(y_t, "y_t", (Bsz, D), io, dev)
     d = Dims(Bsz, 1, D, N, CONV_W, _io_code(io), 0)
     p = make_params(params)
@@ -260,7 +279,7 @@ def prefill_pool(x, dt, z, Bm, Cm, params: dict, slots, h_pool, conv_pool, *, se
     _check(h_pool, "h_pool", (S, D, N), torch.float32, dev)
     _check(conv_pool, "conv_pool", (S, D, CONV_W - 1), torch.float32, dev)
     _check_params(params, D, N, dev)
-    y = torch.empty_like(x) if y is None else y
+    y = _empty((Bsz, D, L), io, dev, stream) if y is None else y
     _check(y, "y", (Bsz, D, L), io, dev)
     d = Dims(Bsz, L, D, N, CONV_W, _io_code(io), chunk_hint)
     p = make_params(params)
@@ -287,7 +306,7 @@ def decode_step_pool(x_t, dt_t, z_t, B_t, C_t, params: dict, slots, h_pool, conv
     _check(h_pool, "h_pool", (S, D, N), torch.float32, dev)
     _check(conv_pool, "conv_pool", (S, D, CONV_W - 1), torch.float32, dev)
     _check_params(params, D, N, dev)
-    y_t = torch.empty_like(x_t) if y_t is None else y_t
+    y_t = _empty((Bsz, D), io, dev, stream) if y_t is None else y_t
     _check(y_t, "y_t", (Bsz, D), io, dev)
     d = Dims(Bsz, 1, D, N, CONV_W, _io_code(io), 0)
     p = make_params(params)
@@ -318,9 +337,9 @@ def q8_quantize(x, block: int = 128, *, q=None, scales=None, stream=None):
     n = x.numel()
     nb = q8_num_blocks(n, block)
     if q is None:
-        q = torch.empty(n, dtype=torch.int8, device=x.device)
+        q = _empty((n,), torch.int8, x.device, stream)
     if scales is None:
-        scales = torch.empty(max(nb, 1), dtype=torch.float32, device=x.device)
+        scales = _empty((max(nb, 1),), torch.float32, x.device, stream)
     _check(q, "q", (n,), torch.int8, x.device)
     _check(scales, "scales", (max(nb, 1),), torch.float32, x.device)
     st = lib.ssm_q8_quantize(n, block, _io_code(x.dtype), _ptr(x), _ptr(q), _ptr(scales),
@@ -343,7 +362,7 @@ def q8_dequant_sum(q_parts, scale_parts, block: int = 128, dtype=torch.bfloat16,
         _check(q_parts[i], f"q_parts[{i}]", (n,), torch.int8, dev)
         _check(scale_parts[i], f"scale_parts[{i}]", (max(nb, 1),), torch.float32, dev)
     if y is None:
-        y = torch.empty(n, dtype=dtype, device=dev)
+        y = _empty((n,), dtype, dev, stream)
     _check(y, "y", (n,), dtype, dev)
     qa = (ctypes.c_void_p * parts)(*[t.data_ptr() for t in q_parts])
     sa = (ctypes.c_void_p * parts)(*[t.data_ptr() for t in scale_parts])
@@ -400,7 +419,7 @@ class Projector:
             out_dtype = x.dtype if out is None else out.dtype
         shape = (Bn, M, L) if token_major_in else (Bn, L, M)
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+            out = _empty(shape, out_dtype, x.device, stream)
         _check(x, "x", tuple(x.shape), x.dtype, x.device)
         _check(w, "w", (M, K), x.dtype, x.device)
         _check(out, "out", shape, out_dtype, x.device)
@@ -416,7 +435,7 @@ def conv_silu(x, params: dict, conv0=None, *, u=None, stream=None):
     lib = load()
     Bn, D, L = x.shape
     if u is None:
-        u = torch.empty_like(x)
+        u = _made(lambda: torch.empty_like(x), stream, x.device)
     _check(u, "u", (Bn, D, L), x.dtype, x.device)
     _check(conv0, "conv0", (Bn, D, CONV_W - 1), torch.float32, x.device, optional=True)
     d = Dims(Bn, L, D, 1, CONV_W, _io_code(x.dtype), 0)
@@ -444,7 +463,7 @@ def conv_xproj(x, params: dict, w, rank: int, conv0=None, *, lowrank=None, Bm=No
     outs = []
     for t, name, width in ((lowrank, "lowrank", rank), (Bm, "Bm", N), (Cm, "Cm", N)):
         if t is None:
-            t = torch.empty(Bn, L, width, dtype=x.dtype, device=x.device)
+            t = _empty((Bn, L, width), x.dtype, x.device, stream)
         _check(t, name, (Bn, L, width), x.dtype, x.device)
         outs.append(t)
     d = Dims(Bn, L, D, N, CONV_W, _io_code(x.dtype), 0)
@@ -479,12 +498,12 @@ def decode_fused(x_t, z_t, params: dict, w_x, w_dt, rank: int, h, conv, *, y_t=N
     _check(h, "h", (Bsz, D, N), torch.float32, dev)
     _check(conv, "conv", (Bsz, D, CONV_W - 1), torch.float32, dev)
     _check_params(params, D, N, dev)
-    y_t = torch.empty_like(x_t) if y_t is None else y_t
+    y_t = _empty((Bsz, D), io, dev, stream) if y_t is None else y_t
     _check(y_t, "y_t", (Bsz, D), io, dev)
     d = Dims(Bsz, 1, D, N, CONV_W, _io_code(io), 0)
     need = int(lib.ssm_decode_fused_workspace_bytes(ctypes.byref(d), rank))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 1),), torch.uint8, dev, stream, returned=False)
     p = make_params(params)
     st = lib.ssm_decode_fused(ctypes.byref(d), ctypes.byref(p), _ptr(w_x), _ptr(w_dt), rank, _ptr(x_t), _ptr(z_t),
                               _ptr(y_t), _ptr(h), _ptr(conv), _ptr(workspace),
@@ -508,7 +527,7 @@ def decode_fused_noalloc(x_t, z_t, params: dict, w_x, w_dt, rank: int, h, conv, 
     _check(h, "h", (Bsz, D, N), torch.float32, dev)
     _check(conv, "conv", (Bsz, D, CONV_W - 1), torch.float32, dev)
     _check_params(params, D, N, dev)
-    y_t = torch.empty_like(x_t) if y_t is None else y_t
+    y_t = _empty((Bsz, D), io, dev, stream) if y_t is None else y_t
     _check(y_t, "y_t", (Bsz, D), io, dev)
     d = Dims(Bsz, 1, D, N, CONV_W, _io_code(io), 0)
     p = make_params(params)
@@ -530,8 +549,8 @@ def calib_issue(kind: int, workgroups: int, iters: int, split: int = 0, *, devic
     """ssm_calib_issue: returns (stamps [waves, 8] int64 on the device, sink); run on `stream`."""
     lib = load()
     dev = torch.device(device)
-    stamps = torch.zeros(workgroups * 4, CALIB_STAMP_WORDS, dtype=torch.int64, device=dev)
-    sink = torch.empty(workgroups * CALIB_THREADS, dtype=torch.float32, device=dev)
+    stamps = _made(lambda: torch.zeros(workgroups * 4, CALIB_STAMP_WORDS, dtype=torch.int64, device=dev), stream, dev)
+    sink = _empty((workgroups * CALIB_THREADS,), torch.float32, dev, stream)
     st = lib.ssm_calib_issue(kind, workgroups, iters, split, _ptr(stamps), _ptr(sink), stream_handle(stream, dev))
     if st != 0:
         raise SsmError("ssm_calib_issue", st, lib.ssm_status_str(st).decode())
@@ -556,7 +575,7 @@ def calib_read(src, sink=None, *, stream=None):
     if not (src.is_cuda and src.is_contiguous()):
         raise ValueError("calib_read: a contiguous GPU tensor expected")
     nsink = int(lib.ssm_calib_read_sink_floats())
-    sink = torch.empty(nsink, dtype=torch.float32, device=src.device) if sink is None else sink
+    sink = _empty((nsink,), torch.float32, src.device, stream) if sink is None else sink
     if sink.numel() < nsink or sink.dtype != torch.float32:
         raise ValueError(f"calib_read: sink must hold {nsink} float32")
     st = lib.ssm_calib_read(_ptr(src), src.numel() * src.element_size(), _ptr(sink), stream_handle(stream, src.device))

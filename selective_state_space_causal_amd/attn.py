@@ -17,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import SSM_BF16, SSM_F32, SsmError, stream_handle
+from ._lib import SSM_BF16, SSM_F32, SsmError, _made, stream_handle
 
 KV_IO, KV_I8, KV_E4M3 = 0, 1, 2
 MIN_PAGE, MAX_PAGE = 16, 1024
@@ -153,19 +153,6 @@ def _view(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name}: the values of a head must be contiguous (stride {one})")
     # the stride of an axis of length 1 is never used, and torch leaves it arbitrary
     return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
-
-
-def _made(make, stream, device, returned=True):
-    """make()'s tensor, from the memory pool of the stream that writes it: a block of the current stream's pool may still
-    be in use by work queued there, which nothing orders before `stream`'s.  A returned one is used on the
-    current stream, so its memory is not handed out again before that is done with it."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        t = make()
-    if returned:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _new(like: torch.Tensor, shape, stream):

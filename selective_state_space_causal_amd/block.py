@@ -13,8 +13,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._lib import SSM_BF16, SSM_F32, SsmError, stream_handle
-from .attn import _made
+from ._lib import SSM_BF16, SSM_F32, SsmError, _made, stream_handle
 
 SSM_E4M3 = 2
 GROUP = 32
