@@ -434,6 +434,7 @@ def conv_silu(x, params: dict, conv0=None, *, u=None, stream=None):
     """u = silu(conv(x)) for x [B, D, L] (the scan's front end, materialised)."""
     lib = load()
     Bn, D, L = x.shape
+    _check(x, "x", (Bn, D, L), x.dtype, x.device)
     if u is None:
         u = _made(lambda: torch.empty_like(x), stream, x.device)
     _check(u, "u", (Bn, D, L), x.dtype, x.device)
@@ -458,6 +459,7 @@ def conv_xproj(x, params: dict, w, rank: int, conv0=None, *, lowrank=None, Bm=No
     N = (M - rank) // 2
     if w.dim() != 2 or w.shape[1] != D or rank < 1 or N < 1 or rank + 2 * N != M:
         raise ValueError(f"w must be [rank + 2 N, {D}] with rank={rank}; got {tuple(w.shape)}")
+    _check(x, "x", (Bn, D, L), x.dtype, x.device)
     _check(w, "w", (M, D), x.dtype, x.device)
     _check(conv0, "conv0", (Bn, D, CONV_W - 1), torch.float32, x.device, optional=True)
     outs = []
